@@ -469,6 +469,131 @@ KDA_API kda_status kda_chunk_fwd_noalloc_device_status(kda_dtype dtype, const in
                                                        int C, void* stream);
 
 
+/*
+ * Linear attention with one decay a head: the recurrence without the delta
+ * rule's read-back,
+ *
+ *     S_t = a_t S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t,     a_t = exp(log_alpha_t)
+ *
+ * with one number a_t for a whole head where KDA has one for each key channel.
+ * (The essay's account of the path from linear attention to KDA: "From GPT-2 to
+ * Kimi K3", pwwt.cn/news/3716252, linear-attention paragraphs.)  Layers of this
+ * kind stand beside KDA layers, and share its layouts, states and call forms.
+ *
+ * The decay is given in one of two forms:
+ *   KDA_DECAY_TOKEN : log_alpha is [B, T, H] in the inputs' dtype, data dependent
+ *   KDA_DECAY_HEAD  : log_alpha is [H] fp32, the same for every token
+ * Either way log_alpha <= 0 and the floor of -100 applies, as in the KDA calls.
+ */
+typedef enum {
+    KDA_DECAY_TOKEN = 0,
+    KDA_DECAY_HEAD = 1
+} kda_decay;
+
+/*
+ * Chunkwise prefill; arguments as kda_chunk_fwd without beta and the chunk size
+ * (the library's choice; the result does not depend on it beyond rounding).
+ *   q, k      : device [B, T, H, dk]      v, o : device [B, T, H, dv]
+ *   workspace : >= kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
+ *               aligned, contents on entry ignored; calls that overlap on the
+ *               GPU need workspaces of their own
+ * final_state may alias init_state; o must not overlap an input.  Packed batches
+ * (cu_seqlens_host, B = 1) and empty sequences as in kda_chunk_fwd.  bf16 with
+ * dk = dv = 128 runs on the tensor cores: products of bf16 operands with fp32
+ * accumulation; the state's update takes the decayed keys as a bf16 pair (16
+ * bits), so states keep fp32-like accuracy, while the scores and the state's
+ * copy that the queries read are rounded to bf16 once, as o itself is.  Other
+ * shapes and fp32 run in fp32 on the CUDA cores.  H <= 65535.
+ * Errors as kda_chunk_fwd; an unknown decay is KDA_ERR_SHAPE.
+ */
+KDA_API size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
+                                                   const int32_t* cu_seqlens_host, int n_seqs);
+KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, const void* log_alpha,
+                                        kda_decay decay, kda_dtype dtype, const float* init_state,
+                                        const int32_t* cu_seqlens_host, int n_seqs, int B, int T, int H, int dk,
+                                        int dv, void* o, float* final_state, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum(d_o * o) + sum(d_final_state * final_state) for the call
+ * above (training).  The forward's states are recomputed inside the call.
+ *   dq, dk_out : device [B, T, H, dk], dv_out : [B, T, H, dv], dtype `dtype` (written)
+ *   dlog_alpha : device [B, T, H], dtype `dtype` (written; zero where log_alpha
+ *                is below the floor of -100).  KDA_DECAY_HEAD: a fixed decay has
+ *                no gradient here; the argument is ignored and may be NULL
+ *   d_init_state : device [N, H, dk, dv] fp32, or NULL (not written)
+ * d_final_state may be NULL (zero) and may alias d_init_state.  The other
+ * outputs must not overlap an input.  Results are reproducible bit for bit.
+ */
+KDA_API size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
+                                                   const int32_t* cu_seqlens_host, int n_seqs);
+KDA_API kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, const void* log_alpha,
+                                        kda_decay decay, kda_dtype dtype, const float* init_state,
+                                        const int32_t* cu_seqlens_host, int n_seqs, int B, int T, int H, int dk,
+                                        int dv, const void* d_o, const float* d_final_state, void* dq, void* dk_out,
+                                        void* dv_out, void* dlog_alpha, float* d_init_state, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of N sequences, the states updated in place (as
+ * kda_decode_step): q, k [N, H, dk], v, o [N, H, dv], state [N, H, dk, dv] fp32,
+ * log_alpha [N, H] (KDA_DECAY_TOKEN) or [H] fp32 (KDA_DECAY_HEAD).
+ */
+KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const void* log_alpha,
+                                          kda_decay decay, kda_dtype dtype, float* state, int N, int H, int dk,
+                                          int dv, void* o, void* stream);
+
+/*
+ * RMS norm of every query and key head and the rotation by position, in one
+ * pass (the usual step between the projections and the attention):
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ * over the d channels of a head, then the first `rot` channels of y turn in
+ * pairs by the angle position * inv_freq[pair], pair = 0 .. rot / 2 - 1:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ *   pairs        : channels (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0
+ *   q, q_out     : Hq heads a token; k, k_out : Hk heads (the counts may differ)
+ *   kda_rows     : rows of d contiguous channels; row (t, h) starts at element
+ *                  t * token_stride + h * head_stride, so views of a fused
+ *                  projection need no copy.  Starts and strides are multiples of
+ *                  16 bytes; written rows must not overlap one another; q_out may
+ *                  be q itself and k_out k itself (same strides)
+ *   q_weight, k_weight : device [d] of weight_dtype, or NULL (ones)
+ *   positions    : device [T] int32, any value (angles are reduced in fp64)
+ *   inv_freq     : device [rot / 2] fp32, angle per position
+ *   d            : 64 or 128; rot : 0 (norm alone; positions and inv_freq may be
+ *                  NULL) or a multiple of 16 up to d; Hq, Hk 1 .. 65535
+ *   eps          : >= 0; with eps = 0 an all-zero row stays zero
+ * All arithmetic in fp32; y is rounded once.  Asynchronous on `stream`.
+ */
+typedef struct {
+    void* data;
+    int64_t token_stride, head_stride;   /* in elements */
+} kda_rows;
+
+KDA_API kda_status kda_qk_norm_rope(const kda_rows* q, const kda_rows* k, const void* q_weight,
+                                    const void* k_weight, kda_dtype weight_dtype, const int32_t* positions,
+                                    const float* inv_freq, kda_dtype dtype, long long T, int Hq, int Hk, int d,
+                                    int rot, float eps, int interleaved, const kda_rows* q_out,
+                                    const kda_rows* k_out, void* stream);
+
+/*
+ * Its gradients: from the inputs of the call above and the gradients d_q_out,
+ * d_k_out of its results, dq and dk (rows, dtype `dtype`; dq may be q's or
+ * d_q_out's memory with the same strides, dk likewise) and the weights'
+ * gradients dq_weight, dk_weight ([d] of weight_dtype, each or NULL).
+ *   workspace : >= kda_qk_norm_rope_bwd_workspace_size(...) bytes, 256-byte aligned
+ * The weight gradients are summed in a fixed order (reproducible bit for bit).
+ */
+KDA_API size_t kda_qk_norm_rope_bwd_workspace_size(long long T, int Hq, int Hk, int d, int rot);
+KDA_API kda_status kda_qk_norm_rope_bwd(const kda_rows* q, const kda_rows* k, const void* q_weight,
+                                        const void* k_weight, kda_dtype weight_dtype, const int32_t* positions,
+                                        const float* inv_freq, kda_dtype dtype, long long T, int Hq, int Hk, int d,
+                                        int rot, float eps, int interleaved, const kda_rows* d_q_out,
+                                        const kda_rows* d_k_out, const kda_rows* dq, const kda_rows* dk,
+                                        void* dq_weight, void* dk_weight, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,8 +11,12 @@ Calls:
 * :func:`decode_step` -- one recurrent step, state updated in place
   (``kda_decode_step``).
 * :func:`chunk_bwd` -- gradients of the prefill for training (``kda_chunk_bwd``).
+* :func:`linear_chunk_fwd`, :func:`linear_chunk_bwd`, :func:`linear_decode_step`
+  -- the same three for linear attention with one decay a head.
+* :func:`qk_norm_rope`, :func:`qk_norm_rope_bwd` -- RMS norm of query and key
+  heads with the rotation by position, and its gradients.
 
-Both take ``prep`` (a bitwise OR of the ``PREP_*`` flags): raw q/k, gate
+The first two take ``prep`` (a bitwise OR of the ``PREP_*`` flags): raw q/k, gate
 logits and beta logits are then normalised / activated inside the kernels
 (``kda_chunk_fwd_prep``, ``kda_decode_step_prep``).
 """
@@ -47,6 +51,10 @@ class KdaError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+
+
+class _Rows(ctypes.Structure):   # kda_rows (include/kda.h)
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 def _declare(lib):
@@ -103,6 +111,26 @@ def _declare(lib):
     lib.kda_chunk_fwd_host.restype = c_int
     lib.kda_chunk_fwd_host_device_status.argtypes = [vp, vp]
     lib.kda_chunk_fwd_host_device_status.restype = c_int
+    lib.kda_linear_chunk_fwd_workspace_size.argtypes = [c_int] * 6 + [i32p, c_int]
+    lib.kda_linear_chunk_fwd_workspace_size.restype = c_size
+    lib.kda_linear_chunk_fwd.argtypes = [vp] * 4 + [c_int, c_int, vp, i32p, c_int] + [c_int] * 5 + \
+        [vp, vp, vp, c_size, vp]
+    lib.kda_linear_chunk_fwd.restype = c_int
+    lib.kda_linear_chunk_bwd_workspace_size.argtypes = [c_int] * 6 + [i32p, c_int]
+    lib.kda_linear_chunk_bwd_workspace_size.restype = c_size
+    lib.kda_linear_chunk_bwd.argtypes = [vp] * 4 + [c_int, c_int, vp, i32p, c_int] + [c_int] * 5 + [vp] * 7 + \
+        [vp, c_size, vp]
+    lib.kda_linear_chunk_bwd.restype = c_int
+    lib.kda_linear_decode_step.argtypes = [vp] * 4 + [c_int, c_int, vp] + [c_int] * 4 + [vp, vp]
+    lib.kda_linear_decode_step.restype = c_int
+    rows, c_ll, c_float = ctypes.POINTER(_Rows), ctypes.c_longlong, ctypes.c_float
+    norm = [rows, rows, vp, vp, c_int, vp, vp, c_int, c_ll] + [c_int] * 4 + [c_float, c_int]
+    lib.kda_qk_norm_rope.argtypes = norm + [rows, rows, vp]
+    lib.kda_qk_norm_rope.restype = c_int
+    lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [c_ll] + [c_int] * 4
+    lib.kda_qk_norm_rope_bwd_workspace_size.restype = c_size
+    lib.kda_qk_norm_rope_bwd.argtypes = norm + [rows] * 4 + [vp, vp, vp, c_size, vp]
+    lib.kda_qk_norm_rope_bwd.restype = c_int
     return lib
 
 
@@ -138,7 +166,9 @@ def exported_symbols():
             "kda_chunk_bwd", "kda_chunk_fwd_device_status", "kda_chunk_bwd_device_status",
             "kda_chunk_fwd_noalloc_device_status", "kda_chunk_segment_map", "kda_compose_states",
             "kda_set_test_wait_limit", "kda_chunk_fwd_host_buffer_size", "kda_chunk_fwd_host",
-            "kda_chunk_fwd_host_device_status"]
+            "kda_chunk_fwd_host_device_status", "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
+            "kda_linear_chunk_bwd_workspace_size", "kda_linear_chunk_bwd", "kda_linear_decode_step",
+            "kda_qk_norm_rope", "kda_qk_norm_rope_bwd_workspace_size", "kda_qk_norm_rope_bwd"]
 
 
 def _ptr(t):
@@ -615,3 +645,292 @@ def decode_step(q, k, v, log_alpha, beta, state, o=None, stream=None, prep: int 
     if st != 0:
         raise KdaError(st, what)
     return o
+
+
+# kda_decay (include/kda.h)
+DECAY_TOKEN, DECAY_HEAD = 0, 1
+
+
+def _check_shape(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _linear_decay(log_alpha, dt, token_shape):
+    """The kda_decay form of ``log_alpha``: per token ``token_shape`` in the
+    inputs' dtype, or per head ``[H]`` in fp32."""
+    if log_alpha.dim() == 1:
+        _check_cuda("log_alpha", log_alpha, torch.float32)
+        _check_shape("log_alpha", log_alpha, token_shape[-1:])
+        return DECAY_HEAD
+    _check_cuda("log_alpha", log_alpha, dt)
+    _check_shape("log_alpha", log_alpha, token_shape)
+    return DECAY_TOKEN
+
+
+def _linear_sizes(q, k, v, cu_seqlens):
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_cuda(name, t, dt)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must have 4 dimensions [B, T, H, d]")
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    _check_shape("k", k, q.shape)
+    _check_shape("v", v, (B, T, H, dv))
+    cu, n_seqs, keep = _cu_arg(cu_seqlens)
+    return B, T, H, dk, dv, cu, n_seqs, keep, (n_seqs if cu_seqlens is not None else B)
+
+
+def linear_workspace_size(B, T, H, dk, dv, dtype, cu_seqlens=None, backward: bool = False) -> int:
+    """Device scratch bytes of linear_chunk_fwd (or linear_chunk_bwd) for these
+    sizes; 0 when they are invalid."""
+    cu, n, _keep = _cu_arg(cu_seqlens)
+    d = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    f = lib().kda_linear_chunk_bwd_workspace_size if backward else lib().kda_linear_chunk_fwd_workspace_size
+    return int(f(B, T, H, dk, dv, d, cu, n))
+
+
+def linear_chunk_fwd(q, k, v, log_alpha, init_state=None, cu_seqlens=None, output_final_state: bool = True,
+                     o=None, final_state=None, workspace=None, stream=None):
+    """Chunkwise prefill of linear attention with one decay a head
+    (``kda_linear_chunk_fwd``): S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t,
+    a_t = exp(log_alpha_t).
+
+    q, k ``[B, T, H, dk]``; v ``[B, T, H, dv]``, one dtype (bf16 or fp32),
+    contiguous, on one CUDA device.  ``log_alpha`` is ``[B, T, H]`` in that
+    dtype, or ``[H]`` fp32 for a fixed decay a head.  ``init_state``,
+    ``cu_seqlens`` and the results as :func:`chunk_fwd`."""
+    B, T, H, dk, dv, cu, n_seqs, _keep, N = _linear_sizes(q, k, v, cu_seqlens)
+    dt, dev = q.dtype, q.device
+    decay = _linear_decay(log_alpha, dt, (B, T, H))
+    _check_cuda("init_state", init_state, torch.float32)
+    _check_shape("init_state", init_state, (N, H, dk, dv))
+    with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("init_state", init_state), ("o", o),
+                                  ("final_state", final_state), ("workspace", workspace))) as (s, allocated):
+        if o is None:
+            o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+            allocated.append(o)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+            allocated.append(final_state)
+        _check_cuda("o", o, dt)
+        _check_shape("o", o, (B, T, H, dv))
+        _check_cuda("final_state", final_state, torch.float32)
+        _check_shape("final_state", final_state, (N, H, dk, dv))
+        if workspace is None:
+            need = lib().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, _DTYPES[dt], cu, n_seqs)
+            workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+            allocated.append(workspace)
+        _check_cuda("workspace", workspace)
+        st = lib().kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), decay, _DTYPES[dt],
+                                        _ptr(init_state), cu, n_seqs, B, T, H, dk, dv, _ptr(o), _ptr(final_state),
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                        _stream_handle(s))
+    if st != 0:
+        raise KdaError(st, "kda_linear_chunk_fwd")
+    return o, final_state
+
+
+def linear_chunk_bwd(q, k, v, log_alpha, d_o, init_state=None, d_final_state=None, cu_seqlens=None,
+                     need_d_init_state: bool = True, grads=None, workspace=None, stream=None):
+    """Gradients of ``sum(d_o * o) + sum(d_final_state * final_state)`` for
+    :func:`linear_chunk_fwd` on the same inputs.  Returns ``(dq, dk, dv,
+    dlog_alpha, d_init_state)``; ``dlog_alpha`` is None for a fixed decay a head
+    (``[H]``), ``d_init_state`` fp32 ``[N, H, dk, dv]`` or None.  ``grads`` may
+    pass preallocated outputs in that order."""
+    B, T, H, dk, dv, cu, n_seqs, _keep, N = _linear_sizes(q, k, v, cu_seqlens)
+    dt, dev = q.dtype, q.device
+    decay = _linear_decay(log_alpha, dt, (B, T, H))
+    _check_cuda("d_o", d_o, dt)
+    _check_shape("d_o", d_o, v.shape)
+    for name, t in (("init_state", init_state), ("d_final_state", d_final_state)):
+        _check_cuda(name, t, torch.float32)
+        _check_shape(name, t, (N, H, dk, dv))
+    given = () if grads is None else tuple((f"grads[{i}]", t) for i, t in enumerate(grads))
+    with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("d_o", d_o),
+                                  ("init_state", init_state), ("d_final_state", d_final_state),
+                                  ("workspace", workspace)) + given) as (s, allocated):
+        if grads is None:
+            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+                     torch.empty_like(log_alpha) if decay == DECAY_TOKEN else None,
+                     torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if need_d_init_state else None)
+            allocated.extend(grads)
+        dq, dk_, dv_, dla, dinit = grads
+        for name, t, like in (("dq", dq, q), ("dk", dk_, k), ("dv", dv_, v), ("dlog_alpha", dla, log_alpha)):
+            _check_cuda(name, t, like.dtype)
+            _check_shape(name, t, like.shape)
+        _check_cuda("d_init_state", dinit, torch.float32)
+        _check_shape("d_init_state", dinit, (N, H, dk, dv))
+        if workspace is None:
+            need = lib().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, _DTYPES[dt], cu, n_seqs)
+            workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+            allocated.append(workspace)
+        _check_cuda("workspace", workspace)
+        st = lib().kda_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), decay, _DTYPES[dt],
+                                        _ptr(init_state), cu, n_seqs, B, T, H, dk, dv, _ptr(d_o), _ptr(d_final_state),
+                                        _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dla), _ptr(dinit), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream_handle(s))
+    if st != 0:
+        raise KdaError(st, "kda_linear_chunk_bwd")
+    return dq, dk_, dv_, dla, dinit
+
+
+def linear_decode_step(q, k, v, log_alpha, state, o=None, stream=None):
+    """One token of linear attention with one decay a head for N sequences
+    (``kda_linear_decode_step``); ``state`` ``[N, H, dk, dv]`` fp32 is updated in
+    place.  q, k ``[N, H, dk]``, v ``[N, H, dv]``, log_alpha ``[N, H]`` or ``[H]``
+    fp32.  Returns o ``[N, H, dv]``."""
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_cuda(name, t, dt)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must have 3 dimensions [N, H, d]")
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    _check_shape("k", k, q.shape)
+    _check_shape("v", v, (N, H, dv))
+    decay = _linear_decay(log_alpha, dt, (N, H))
+    _check_cuda("state", state, torch.float32)
+    _check_shape("state", state, (N, H, dk, dv))
+    dev = q.device
+    with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("state", state), ("o", o))) \
+            as (s, allocated):
+        if o is None:
+            o = torch.empty((N, H, dv), dtype=dt, device=dev)
+            allocated.append(o)
+        _check_cuda("o", o, dt)
+        _check_shape("o", o, (N, H, dv))
+        st = lib().kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), decay, _DTYPES[dt],
+                                          _ptr(state), N, H, dk, dv, _ptr(o), _stream_handle(s))
+    if st != 0:
+        raise KdaError(st, "kda_linear_decode_step")
+    return o
+
+
+def _rows(name, t, dt, shape=None):
+    """``t`` ``[..., H, d]`` as a kda_rows of its tokens: any strides that let the
+    leading dimensions be walked with one step."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype != dt:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have shape [..., H, d]")
+    if shape is not None:
+        _check_shape(name, t, shape)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.numel() == 0:
+        return _Rows(None, 0, 0)
+    steps = [(n, st) for n, st in zip(t.shape[:-2], t.stride()[:-2]) if n > 1]
+    for (_, outer), (n, inner) in zip(steps[:-1], steps[1:]):
+        if outer != n * inner:
+            raise ValueError(f"{name}'s token dimensions must be walkable with one stride")
+    # a stride that no step is made along is taken as that of packed heads
+    head = t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+    return _Rows(t.data_ptr(), steps[-1][1] if steps else t.shape[-2] * head, head)
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq):
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    rq, rk = _rows("q", q, dt), _rows("k", k, dt)
+    d, lead = q.shape[-1], tuple(q.shape[:-2])
+    _check_shape("k", k, lead + (k.shape[-2], d))
+    T = 1
+    for n in lead:
+        T *= n
+    wdt = next((w.dtype for w in (q_weight, k_weight) if w is not None), dt)
+    if wdt not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {wdt}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _check_cuda(name, w, wdt)
+        _check_shape(name, w, (d,))
+    rot = 0
+    if inv_freq is not None:
+        _check_cuda("inv_freq", inv_freq, torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have one dimension [rot / 2]")
+        rot = 2 * inv_freq.shape[0]
+        if positions is None:
+            raise ValueError("positions are required with inv_freq")
+        _check_cuda("positions", positions, torch.int32)
+        _check_shape("positions", positions, lead)
+    return dt, rq, rk, T, q.shape[-2], k.shape[-2], d, rot, wdt
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head, then the rotation of the first
+    ``2 * len(inv_freq)`` channels by ``positions * inv_freq``
+    (``kda_qk_norm_rope``).
+
+    q ``[..., Hq, d]``, k ``[..., Hk, d]`` (bf16 or fp32, d 64 or 128): the last
+    dimension contiguous, views of a fused projection included.  ``q_weight``,
+    ``k_weight`` ``[d]`` (bf16 or fp32) or None; ``positions`` int32 of the
+    leading shape and ``inv_freq`` fp32 ``[rot / 2]``, or neither for the norm
+    alone.  ``interleaved`` pairs channels (2 i, 2 i + 1) instead of
+    (i, i + rot / 2).  Returns ``(q_out, k_out)``; ``q_out=q, k_out=k`` works in
+    place."""
+    dt, rq, rk, T, Hq, Hk, d, rot, wdt = _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq)
+    dev = q.device
+    with _launch_on(dev, stream, (("k", k), ("q_weight", q_weight), ("k_weight", k_weight),
+                                  ("positions", positions), ("inv_freq", inv_freq), ("q_out", q_out),
+                                  ("k_out", k_out))) as (s, allocated):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+            allocated.append(q_out)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=dev)
+            allocated.append(k_out)
+        oq, ok = _rows("q_out", q_out, dt, q.shape), _rows("k_out", k_out, dt, k.shape)
+        st = lib().kda_qk_norm_rope(rq, rk, _ptr(q_weight), _ptr(k_weight), _DTYPES[wdt], _ptr(positions),
+                                    _ptr(inv_freq), _DTYPES[dt], T, Hq, Hk, d, rot, float(eps), int(interleaved),
+                                    oq, ok, _stream_handle(s))
+    if st != 0:
+        raise KdaError(st, "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, eps: float = 1e-6,
+                     interleaved: bool = False, need_weight_grads: bool = True, grads=None, workspace=None,
+                     stream=None):
+    """Gradients of :func:`qk_norm_rope` on the same inputs, from the gradients
+    of its results.  Returns ``(dq, dk, dq_weight, dk_weight)``, the last two in
+    the weights' dtype (None for a weight that is None, or without
+    ``need_weight_grads``).  ``grads`` may pass preallocated outputs."""
+    dt, rq, rk, T, Hq, Hk, d, rot, wdt = _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq)
+    gq, gk = _rows("d_q_out", d_q_out, dt, q.shape), _rows("d_k_out", d_k_out, dt, k.shape)
+    dev = q.device
+    given = () if grads is None else tuple((f"grads[{i}]", t) for i, t in enumerate(grads))
+    with _launch_on(dev, stream, (("k", k), ("q_weight", q_weight), ("k_weight", k_weight),
+                                  ("positions", positions), ("inv_freq", inv_freq), ("d_q_out", d_q_out),
+                                  ("d_k_out", d_k_out), ("workspace", workspace)) + given) as (s, allocated):
+        if grads is None:
+            grads = (torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev),
+                     *(torch.empty_like(w) if w is not None and need_weight_grads else None
+                       for w in (q_weight, k_weight)))
+            allocated.extend(grads)
+        dq, dk_, dwq, dwk = grads
+        oq, ok = _rows("dq", dq, dt, q.shape), _rows("dk", dk_, dt, k.shape)
+        for name, w in (("dq_weight", dwq), ("dk_weight", dwk)):
+            _check_cuda(name, w, wdt)
+            _check_shape(name, w, (d,))
+        if workspace is None:
+            need = lib().kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d, rot)
+            workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+            allocated.append(workspace)
+        _check_cuda("workspace", workspace)
+        st = lib().kda_qk_norm_rope_bwd(rq, rk, _ptr(q_weight), _ptr(k_weight), _DTYPES[wdt], _ptr(positions),
+                                        _ptr(inv_freq), _DTYPES[dt], T, Hq, Hk, d, rot, float(eps), int(interleaved),
+                                        gq, gk, oq, ok, _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream_handle(s))
+    if st != 0:
+        raise KdaError(st, "kda_qk_norm_rope_bwd")
+    return dq, dk_, dwq, dwk

@@ -6,7 +6,7 @@
 #include <mutex>
 #include <vector>
 
-#include "kda_internal.cuh"
+#include "kda_host.cuh"
 
 namespace kda {
 
@@ -41,12 +41,15 @@ extern const int kTcKernelCount;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 const char* const kSimtKernelNames[] = {"k1_cumsum", "k2_wy", "k3_state", "k4_output"};
+
+}  // namespace
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+namespace {
 
 // Sequence tables reach the device as kernel arguments: the launch copies its
 // parameters when it is issued, so the host neither waits for the stream nor
@@ -78,14 +81,12 @@ __global__ void __launch_bounds__(256) chunk_table_fill(const SeqInfo* __restric
     dst[c] = make_int4(sq.tok0 + idx * C, min(C, sq.len - idx * C), sq.seq, idx);
 }
 
-// the per-chunk table follows the two sequence tables
+}  // namespace
+
 int4* chunk_table(SeqInfo* tables, size_t n_seqs) { return reinterpret_cast<int4*>(tables + 2 * n_seqs); }
 
-// natural order then longest first, 2 n_seqs entries at `dst`, then the per-chunk
-// table of n_chunks entries of C tokens; returns the number of launches (with `mark`,
-// timing-hook event i follows the i-th of them)
 int upload_tables(SeqInfo* dst, const std::vector<SeqInfo>& natural, const std::vector<SeqInfo>& by_len,
-                  int n_chunks, int C, cudaStream_t s, cudaError_t* err, bool mark = false) {
+                  int n_chunks, int C, cudaStream_t s, cudaError_t* err, bool mark) {
     const size_t n = natural.size();
     int launches = 0;
     TableBatch b;
@@ -110,20 +111,14 @@ int upload_tables(SeqInfo* dst, const std::vector<SeqInfo>& natural, const std::
     return launches;
 }
 
+namespace {
+
 // launches of upload_tables: the sequence-table batches, then the chunk table
 int table_launches(size_t n_seqs, int n_chunks) {
     return (int)((2 * n_seqs + kTableBatch - 1) / kTableBatch) + (n_chunks > 0 ? 1 : 0);
 }
 
-// Problem geometry shared by the workspace query and the launch.
-struct Plan {
-    int n_seqs = 0;
-    int n_chunks = 0;
-    long long total_tokens = 0;
-    bool varlen = false;
-    std::vector<SeqInfo> natural;   // chunk0 non-decreasing (varlen only)
-    std::vector<SeqInfo> by_len;    // longest first (varlen only)
-};
+}  // namespace
 
 kda_status make_plan(int B, int T, int H, int dk, int dv, int C, const int32_t* cu, int n_seqs, Plan& p) {
     if (H <= 0 || B < 0 || T < 0) return KDA_ERR_SHAPE;
@@ -162,6 +157,8 @@ kda_status make_plan(int B, int T, int H, int dk, int dv, int C, const int32_t* 
 size_t table_bytes(const Plan& p) {
     return p.varlen ? align_up(2 * sizeof(SeqInfo) * (size_t)p.n_seqs + sizeof(int4) * (size_t)p.n_chunks) : 0;
 }
+
+namespace {
 
 struct SimtLayout {
     size_t off[6];
@@ -233,7 +230,8 @@ size_t workspace_for(const Plan& p, int H, int dk, int dv, int C, kda_algo algo)
     return simt_layout(p, H, dk, dv).total;
 }
 
-// Device capability check, cached per device ordinal.
+}  // namespace
+
 kda_status check_device() {
     static std::mutex mu;
     static int cached[64];
@@ -253,7 +251,16 @@ kda_status check_device() {
     return cached[dev] ? KDA_OK : KDA_ERR_DEVICE;
 }
 
-}  // namespace
+kda_status read_error_word(const void* workspace, size_t offset, void* stream) {
+    int word = 0;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cudaMemcpyAsync(&word, (const char*)workspace + offset, sizeof(int), cudaMemcpyDeviceToHost, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    return word == 0 ? KDA_OK : (kda_status)word;
+}
+
 }  // namespace kda
 
 using namespace kda;
@@ -279,7 +286,7 @@ const char* kda_status_string(int status) {
     }
 }
 
-int kda_version(void) { return 100; }
+int kda_version(void) { return 200; }
 
 size_t kda_chunk_fwd_workspace_size_ex(int B, int T, int H, int dk, int dv, int C, kda_dtype dtype,
                                        const int32_t* cu_seqlens_host, int n_seqs, kda_algo algo) {
@@ -598,21 +605,6 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, const void
 }
 
 }  // extern "C"
-
-namespace {
-
-// Copy the error word at `offset` of the workspace to the host after `stream` finishes.
-kda_status read_error_word(const void* workspace, size_t offset, void* stream) {
-    int word = 0;
-    cudaStream_t s = (cudaStream_t)stream;
-    if (cudaMemcpyAsync(&word, (const char*)workspace + offset, sizeof(int), cudaMemcpyDeviceToHost, s) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    return word == 0 ? KDA_OK : (kda_status)word;
-}
-
-}  // namespace
 
 extern "C" {
 

@@ -1,0 +1,50 @@
+// Internal declarations of linear attention with one decay a head,
+//   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_t = exp(log_alpha_t),
+// shared by its CUDA sources (not part of the ABI).
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// The decay argument: one log decay per token and head in the inputs' dtype, or one
+// per head in fp32.
+struct LinDecay {
+    const void* la;
+    int per_head;
+};
+
+template <typename Tin>
+__device__ __forceinline__ float lin_raw_decay(const LinDecay& d, size_t tok, int H, int h) {
+    return d.per_head ? reinterpret_cast<const float*>(d.la)[h]
+                      : to_f32(reinterpret_cast<const Tin*>(d.la)[tok * (size_t)H + h]);
+}
+template <typename Tin>
+__device__ __forceinline__ float lin_log_decay(const LinDecay& d, size_t tok, int H, int h) {
+    return fmaxf(lin_raw_decay<Tin>(d, tok, H, h), kLogAlphaFloor);
+}
+
+// ---- CUDA-core path (fp32 inputs, or a width of 64): 64-token chunks -------------
+constexpr int kLinSimtChunk = 64;
+
+struct LinSimtWorkspace {
+    float* S;       // [chunks, H, dk, dv] each chunk's update, then its start state
+    float* dS;      // [chunks, H, dk, dv] (backward) the same for the reversed chain: gradient of the end state
+    float* gam;     // [chunks, H] a chunk's whole decay
+};
+
+cudaError_t launch_lin_simt_fwd(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
+                                const float* init_state, void* o, float* final_state, const ChunkMap& cmap,
+                                const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
+                                const LinSimtWorkspace& ws, cudaStream_t stream);
+
+cudaError_t launch_lin_simt_bwd(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
+                                const float* init_state, const void* d_o, const float* d_final, void* dq, void* dk_out,
+                                void* dv_out, void* dla, float* d_init, const ChunkMap& cmap, const SeqMap& smap,
+                                int n_chunks, int n_seqs, int H, int dk, int dv, const LinSimtWorkspace& ws,
+                                cudaStream_t stream);
+
+cudaError_t launch_lin_decode(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
+                              float* state, int N, int H, int dk, int dv, void* o, cudaStream_t stream);
+
+}  // namespace kda

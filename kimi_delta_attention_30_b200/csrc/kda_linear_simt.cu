@@ -1,0 +1,524 @@
+// Linear attention with one decay a head on the CUDA cores: the path for fp32 inputs
+// and for widths of 64.
+//
+// With g_i the inclusive sum of log decays inside a chunk of C = 64 tokens and S the
+// chunk's start state,
+//   S'  = e^{g_C} S + sum_j e^{g_C - g_j} k_j v_j^T
+//   o_i = e^{g_i} S^T q_i + sum_{j <= i} e^{g_i - g_j} (q_i . k_j) v_j
+// so the only sequential part is S' from S, an elementwise multiply and add once every
+// chunk's own sum is known.  Forward: (1) each chunk's sum, all chunks at once; (2) the
+// chain over chunks, one thread per four state elements, which leaves every chunk's
+// start state; (3) the outputs, all chunks at once.  Backward: the same two steps give
+// the start states, and once more with (q, d_o), weights e^{g_i} and the order reversed
+// the gradients dS' of the end states; then all chunks at once
+//   P_ij = D_ij (q_i . k_j),  dA_ij = D_ij (d_o_i . v_j),  D_ij = e^{g_i - g_j} (j <= i)
+//   dq_i = e^{g_i} S d_o_i + sum_j dA_ij k_j
+//   dk_j = e^{g_C - g_j} dS' v_j + sum_i dA_ij q_i
+//   dv_j = e^{g_C - g_j} dS'^T k_j + sum_i P_ij d_o_i
+//   dlog_alpha_t = sum_{i >= t} e^{g_i} q_i . S d_o_i + sum_{j < t} e^{g_C - g_j} k_j . dS' v_j
+//                + e^{g_C} <dS', S> + sum_{i >= t > j} dA_ij (q_i . k_j)
+// where every term of the last lines is one that t's decay enters, so nothing cancels:
+// the last sum runs over a rectangle of the pair products, taken as running sums along
+// each row and then down the columns.  (Suffix sums of q_i . dq_i - k_i . dk_i give the
+// same number, but the pairs with both ends behind t cancel there and leave their
+// roundings: 4e-6 where the gradient is exactly zero.)
+//
+// Products are 64 x 64 register tiles (256 threads, 4 x 4 each) over operands in shared
+// memory, every operand read as 16-byte vectors where its layout allows; fp32 throughout,
+// as fp32 inputs ask for.  Decays are formed from g as a (hi, lo) pair.
+#include "kda_linear.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kC = kLinSimtChunk;
+constexpr int kThreads = 256;
+constexpr int kLdM = kC + 1;   // pitch of the pair products, walked along rows and columns
+constexpr int kLdP = kC + 4;   // row pitch of 64-wide tiles: rows start 4 banks apart
+
+// acc += A B over K, A 64 x K and B K x 64.  Thread (ty, tx) owns rows 4 ty + r and
+// columns 4 tx + c, or tx + 16 c with CI (which keeps reads of a B stored [column][k]
+// free of bank conflicts).  AT: A stored [k][row].  BT: B stored [column][k].
+template <int K, bool AT, bool BT, bool CI>
+__device__ __forceinline__ void mm64(float (&acc)[4][4], const float* __restrict__ A, int lda,
+                                     const float* __restrict__ B, int ldb, int ty, int tx) {
+#pragma unroll 4
+    for (int k = 0; k < K; k += 4) {
+        float a[4][4], b[4][4];   // [k][row], [k][column]
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (AT) {
+                const float4 x = *reinterpret_cast<const float4*>(A + (k + u) * lda + 4 * ty);
+                a[u][0] = x.x; a[u][1] = x.y; a[u][2] = x.z; a[u][3] = x.w;
+            } else {
+                const float4 x = *reinterpret_cast<const float4*>(A + (4 * ty + u) * lda + k);
+                a[0][u] = x.x; a[1][u] = x.y; a[2][u] = x.z; a[3][u] = x.w;
+            }
+            if (BT) {
+                const float4 x = *reinterpret_cast<const float4*>(B + (CI ? tx + 16 * u : 4 * tx + u) * ldb + k);
+                b[0][u] = x.x; b[1][u] = x.y; b[2][u] = x.z; b[3][u] = x.w;
+            } else if (CI) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) b[u][c] = B[(k + u) * ldb + tx + 16 * c];
+            } else {
+                const float4 x = *reinterpret_cast<const float4*>(B + (k + u) * ldb + 4 * tx);
+                b[u][0] = x.x; b[u][1] = x.y; b[u][2] = x.z; b[u][3] = x.w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(a[u][r], b[u][c], acc[r][c]);
+    }
+}
+
+__device__ __forceinline__ void clear(float (&acc)[4][4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+}
+
+__device__ __forceinline__ void load_vec(const float* p, float (&x)[4]) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[4]) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// 64 token rows of COLS columns from column c0 of a [tokens, H, D] array; rows past
+// `len` are zero (they belong to the next sequence).
+template <typename Tin, int COLS>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const Tin* __restrict__ src, size_t tok0, int len, int H,
+                                          int h, int D, int c0) {
+    constexpr int V = COLS / 4;
+    for (int u = threadIdx.x; u < kC * V; u += kThreads) {
+        const int r = u / V, c = (u % V) * 4;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < len) load_vec(src + ((tok0 + r) * (size_t)H + h) * D + c0 + c, x);
+        *reinterpret_cast<float4*>(dst + r * ld + c) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+}
+
+// The chunk's inclusive cumulative log decay as (hi, lo), by the first warp; tokens past
+// `len` add nothing, so g stays at the last token's value there.
+template <typename Tin>
+__device__ __forceinline__ void chunk_decay(float* gh, float* gl, const LinDecay& dec, size_t tok0, int len, int H,
+                                            int h) {
+    if (threadIdx.x < 32) {
+        const int t = 2 * threadIdx.x;
+        const double a = t < len ? (double)lin_log_decay<Tin>(dec, tok0 + t, H, h) : 0.0;
+        const double b = t + 1 < len ? (double)lin_log_decay<Tin>(dec, tok0 + t + 1, H, h) : 0.0;
+        double s = a + b;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, off);
+            if ((int)threadIdx.x >= off) s += y;
+        }
+        const double g0 = s - b;
+        gh[t] = (float)g0;
+        gl[t] = (float)(g0 - (double)gh[t]);
+        gh[t + 1] = (float)s;
+        gl[t + 1] = (float)(s - (double)gh[t + 1]);
+    }
+}
+
+// ---- (1) each chunk's own sum: one 64 x 64 tile of the state a block ---------------
+// Forward: sum_j e^{g_C - g_j} a_j b_j^T (a = k, b = v); REV: sum_i e^{g_i} a_i b_i^T (q, d_o).
+template <typename Tin, bool REV>
+__global__ void __launch_bounds__(kThreads) lin_update(const Tin* __restrict__ a, const Tin* __restrict__ b,
+                                                       LinDecay dec, ChunkMap cmap, int H, int DK, int DV,
+                                                       float* __restrict__ U, float* __restrict__ gam) {
+    __shared__ __align__(16) float sa[kC * kLdP], sb[kC * kLdP];
+    __shared__ float gh[kC], gl[kC], w[kC];
+    int seq, tok0, len, idx;
+    cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
+    const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int nv = DV / 64, k0 = ((int)blockIdx.z / nv) * 64, v0 = ((int)blockIdx.z % nv) * 64;
+    chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
+    load_rows<Tin, 64>(sa, kLdP, a, tok0, len, H, h, DK, k0);
+    load_rows<Tin, 64>(sb, kLdP, b, tok0, len, H, h, DV, v0);
+    __syncthreads();
+    if (tid < kC)
+        w[tid] = REV ? exp_g(gh[tid], gl[tid]) : exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
+    __syncthreads();
+    for (int u = tid; u < kC * 16; u += kThreads) {
+        float4* p = reinterpret_cast<float4*>(sb + (u >> 4) * kLdP + (u & 15) * 4);
+        const float s = w[u >> 4];
+        *p = make_float4(p->x * s, p->y * s, p->z * s, p->w * s);
+    }
+    __syncthreads();
+    float acc[4][4];
+    clear(acc);
+    mm64<kC, true, false, false>(acc, sa, kLdP, sb, kLdP, ty, tx);
+    const size_t unit = (size_t)blockIdx.x * H + h;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(U + (unit * DK + k0 + 4 * ty + r) * DV + v0 + 4 * tx) =
+            make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    if (blockIdx.z == 0 && tid == 0) gam[unit] = exp_g(gh[kC - 1], gl[kC - 1]);
+}
+
+// ---- (2) the chain over chunks, in place: X[n] = state before chunk n (REV: behind it)
+template <bool REV>
+__global__ void __launch_bounds__(kThreads) lin_chain(float* __restrict__ X, const float* __restrict__ gam,
+                                                      const float* __restrict__ start, float* __restrict__ end,
+                                                      SeqMap smap, int H, int E4) {
+    const SeqInfo sq = smap.get((int)blockIdx.x / H);
+    const int h = (int)blockIdx.x % H;
+    const int e = (int)blockIdx.y * kThreads + threadIdx.x;
+    if (e >= E4) return;
+    const int n = (sq.len + smap.C - 1) / smap.C;
+    float4* x4 = reinterpret_cast<float4*>(X);
+    const size_t sh = ((size_t)sq.seq * H + h) * E4 + e;
+    float4 s = start ? reinterpret_cast<const float4*>(start)[sh] : make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 8;   // loads of that many chunks stand before the first is used
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        float4 u[kAhead];
+        float g[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i0 + j < n) {
+                const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i0 - j : i0 + j)) * H + h;
+                u[j] = x4[unit * E4 + e];
+                g[j] = gam[unit];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i0 + j < n) {
+                const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i0 - j : i0 + j)) * H + h;
+                x4[unit * E4 + e] = s;
+                s.x = fmaf(g[j], s.x, u[j].x);
+                s.y = fmaf(g[j], s.y, u[j].y);
+                s.z = fmaf(g[j], s.z, u[j].z);
+                s.w = fmaf(g[j], s.w, u[j].w);
+            }
+        }
+    }
+    if (end) reinterpret_cast<float4*>(end)[sh] = s;
+}
+
+// ---- (3) outputs: 64 tokens x 64 value columns a block -----------------------------
+template <int DK> constexpr size_t out_smem() { return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * kLdP + DK * kLdP); }
+
+template <typename Tin, int DK>
+__global__ void __launch_bounds__(kThreads) lin_out(const Tin* __restrict__ q, const Tin* __restrict__ k,
+                                                    const Tin* __restrict__ v, LinDecay dec, ChunkMap cmap, int H,
+                                                    int DV, const float* __restrict__ S, Tin* __restrict__ o) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ float gh[kC], gl[kC];
+    constexpr int LD = DK + 4;
+    float *sq = sm, *sk = sq + kC * LD, *sv = sk + kC * LD, *sp = sv + kC * kLdP, *ss = sp + kC * kLdP;
+    int seq, tok0, len, idx;
+    cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
+    const int h = blockIdx.y, v0 = blockIdx.z * 64, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
+    load_rows<Tin, DK>(sq, LD, q, tok0, len, H, h, DK, 0);
+    load_rows<Tin, DK>(sk, LD, k, tok0, len, H, h, DK, 0);
+    load_rows<Tin, 64>(sv, kLdP, v, tok0, len, H, h, DV, v0);
+    const float* Sn = S + ((size_t)blockIdx.x * H + h) * DK * DV + v0;
+    for (int u = tid; u < DK * 16; u += kThreads)
+        *reinterpret_cast<float4*>(ss + (u >> 4) * kLdP + (u & 15) * 4) =
+            *reinterpret_cast<const float4*>(Sn + (size_t)(u >> 4) * DV + (u & 15) * 4);
+    __syncthreads();
+    float acc[4][4];
+    clear(acc);
+    mm64<DK, false, true, true>(acc, sq, LD, sk, LD, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = 4 * ty + r, j = tx + 16 * c;
+            sp[i * kLdP + j] = j <= i ? acc[r][c] * exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
+        }
+    clear(acc);
+    mm64<DK, false, false, false>(acc, sq, LD, ss, kLdP, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float e = exp_g(gh[4 * ty + r], gl[4 * ty + r]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] *= e;
+    }
+    __syncthreads();
+    mm64<kC, false, false, false>(acc, sp, kLdP, sv, kLdP, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = 4 * ty + r;
+        if (i < len) {
+            Tin* dst = o + ((size_t)(tok0 + i) * H + h) * DV + v0 + 4 * tx;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dst[c] = from_f32<Tin>(acc[r][c]);
+        }
+    }
+}
+
+// ---- backward: one (chunk, head) a block -------------------------------------------
+template <int DK, int DV> constexpr size_t grad_smem() {
+    constexpr int tile = (64 * (DV + 4) > DK * kLdP) ? 64 * (DV + 4) : DK * kLdP;
+    return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * (DV + 4) + tile + 2 * kC * kLdP);
+}
+
+// sum over the 16 threads that share rows 4 ty + r, added to dst by the first of them
+__device__ __forceinline__ void add_row_sums(float* dst, const float (&s)[4], int ty, int tx) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float x = s[r];
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (tx == 0) dst[4 * ty + r] += x;
+    }
+}
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, LinDecay dec,
+         const Tin* __restrict__ d_o, ChunkMap cmap, int H, const float* __restrict__ S, const float* __restrict__ dS,
+         Tin* __restrict__ dq, Tin* __restrict__ dk, Tin* __restrict__ dv, Tin* __restrict__ dla) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ float gh[kC], gl[kC], wq[kC], wk[kC], ra[kC], rb[kC], rx[kC], red[kThreads / 32];
+    constexpr int LK = DK + 4, LV = DV + 4;
+    float *sq = sm, *sk = sq + kC * LK, *sv = sk + kC * LK, *sd = sv + kC * LV;
+    float *sp = sd + kC * LV, *sa = sp + kC * kLdP, *tile = sa + kC * kLdP;
+    int seq, tok0, len, idx;
+    cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
+    const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const size_t unit = (size_t)blockIdx.x * H + h;
+    const float *Sn = S + unit * DK * DV, *dSn = dS + unit * DK * DV;
+    chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
+    load_rows<Tin, DK>(sq, LK, q, tok0, len, H, h, DK, 0);
+    load_rows<Tin, DK>(sk, LK, k, tok0, len, H, h, DK, 0);
+    load_rows<Tin, DV>(sv, LV, v, tok0, len, H, h, DV, 0);
+    load_rows<Tin, DV>(sd, LV, d_o, tok0, len, H, h, DV, 0);
+    float e = 0.f;   // <dS', S>
+    for (int u = tid; u < DK * DV / 4; u += kThreads) {
+        const float4 x = reinterpret_cast<const float4*>(Sn)[u], y = reinterpret_cast<const float4*>(dSn)[u];
+        e += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+    if ((tid & 31) == 0) red[tid >> 5] = e;
+    __syncthreads();
+    if (tid < kC) {
+        wq[tid] = exp_g(gh[tid], gl[tid]);
+        wk[tid] = exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
+        ra[tid] = rb[tid] = 0.f;
+    }
+    float p[4][4], a[4][4];
+    clear(p);
+    clear(a);
+    mm64<DK, false, true, true>(p, sq, LK, sk, LK, ty, tx);
+    mm64<DV, false, true, true>(a, sd, LV, sv, LV, ty, tx);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = 4 * ty + r, j = tx + 16 * c;
+            const float d = j <= i ? exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
+            sp[i * kLdP + j] = j <= i ? p[r][c] * d : 0.f;
+            sa[i * kLdP + j] = j <= i ? a[r][c] * d : 0.f;
+            tile[i * kLdM + j] = j < i ? p[r][c] * a[r][c] * d : 0.f;
+        }
+    __syncthreads();
+    {   // rx[t] = sum of the pair products over i >= t > j, four threads a row, then four a column
+        const int i = tid >> 2, part = tid & 3;
+        float* row = tile + i * kLdM + 16 * part;
+        float run = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) run += row[j];
+        float before = 0.f;
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            const float y = __shfl_sync(0xffffffffu, run, u, 4);
+            if (u < part) before += y;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            before += row[j];
+            row[j] = before;
+        }
+        __syncthreads();
+        const int t = tid >> 2;
+        float sum = 0.f;
+        for (int r = t + ((part - t) & 3); t > 0 && r < kC; r += 4) sum += tile[r * kLdM + t - 1];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (part == 0) rx[t] = sum;
+    }
+    for (int k0 = 0; k0 < DK; k0 += 64) {
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {   // dq from S and dA k, then dk from dS' and dA^T q
+            __syncthreads();
+            const float* src = (side ? dSn : Sn) + (size_t)k0 * DV;
+            for (int u = tid; u < 64 * DV / 4; u += kThreads)
+                *reinterpret_cast<float4*>(tile + (u / (DV / 4)) * LV + (u % (DV / 4)) * 4) =
+                    reinterpret_cast<const float4*>(src)[u];
+            __syncthreads();
+            float s1[4];
+            clear(p);
+            clear(a);
+            if (side == 0) {
+                mm64<DV, false, true, true>(p, sd, LV, tile, LV, ty, tx);
+                mm64<kC, false, false, true>(a, sa, kLdP, sk + k0, LK, ty, tx);
+            } else {
+                mm64<DV, false, true, true>(p, sv, LV, tile, LV, ty, tx);
+                mm64<kC, true, false, true>(a, sa, kLdP, sq + k0, LK, ty, tx);
+            }
+            const float *w = side ? wk : wq, *x = (side ? sk : sq) + k0;
+            Tin* out = side ? dk : dq;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * ty + r;
+                const float wi = w[i];
+                s1[r] = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = tx + 16 * c;
+                    const float xi = x[i * LK + j], inter = wi * p[r][c];
+                    s1[r] = fmaf(xi, inter, s1[r]);
+                    if (i < len) out[((size_t)(tok0 + i) * H + h) * DK + k0 + j] = from_f32<Tin>(inter + a[r][c]);
+                }
+            }
+            add_row_sums(side ? rb : ra, s1, ty, tx);
+        }
+    }
+    for (int v0 = 0; v0 < DV; v0 += 64) {
+        __syncthreads();
+        for (int u = tid; u < DK * 16; u += kThreads)
+            *reinterpret_cast<float4*>(tile + (u >> 4) * kLdP + (u & 15) * 4) =
+                *reinterpret_cast<const float4*>(dSn + (size_t)(u >> 4) * DV + v0 + (u & 15) * 4);
+        __syncthreads();
+        clear(p);
+        mm64<DK, false, false, false>(p, sk, LK, tile, kLdP, ty, tx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[r][c] *= wk[4 * ty + r];
+        mm64<kC, true, false, false>(p, sp, kLdP, sd + v0, LV, ty, tx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * ty + r;
+            if (i < len) {
+                Tin* dst = dv + ((size_t)(tok0 + i) * H + h) * DV + v0 + 4 * tx;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dst[c] = from_f32<Tin>(p[r][c]);
+            }
+        }
+    }
+    if (dla != nullptr && tid < 32) {
+        // suffix sums of ra, exclusive prefix sums of rb, two tokens a lane
+        __syncwarp();
+        const int t = 2 * tid;
+        float suf = ra[t] + ra[t + 1], pre = rb[t] + rb[t + 1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, suf, off), z = __shfl_up_sync(0xffffffffu, pre, off);
+            if (tid + off < 32) suf += y;
+            if (tid >= off) pre += z;
+        }
+        // the lane's own terms are left out by taking its neighbour's sums, not by subtraction
+        float suf_next = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+        if (tid == 31) suf_next = 0.f;
+        pre = tid == 0 ? 0.f : before;
+        float whole = 0.f;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) whole += red[i];
+        whole *= exp_g(gh[kC - 1], gl[kC - 1]);
+        const float x0 = suf + pre + whole + rx[t];
+        const float x1 = suf_next + ra[t + 1] + pre + rb[t] + whole + rx[t + 1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (t + u < len) {
+                const size_t tok = (size_t)tok0 + t + u;
+                const bool floored = lin_raw_decay<Tin>(dec, tok, H, h) < kLogAlphaFloor;
+                dla[tok * H + h] = from_f32<Tin>(floored ? 0.f : (u ? x1 : x0));
+            }
+    }
+}
+
+template <typename Tin, bool REV>
+cudaError_t update_and_chain(const void* a, const void* b, LinDecay dec, const float* start, float* end,
+                             const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
+                             float* X, float* gam, cudaStream_t s) {
+    if (n_chunks > 0)
+        lin_update<Tin, REV><<<dim3(n_chunks, H, (dk / 64) * (dv / 64)), kThreads, 0, s>>>(
+            (const Tin*)a, (const Tin*)b, dec, cmap, H, dk, dv, X, gam);
+    const int e4 = dk * dv / 4;
+    lin_chain<REV><<<dim3((unsigned)n_seqs * H, e4 / kThreads), kThreads, 0, s>>>(X, gam, start, end, smap, H, e4);
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init, void* o, float* final,
+                const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
+                const LinSimtWorkspace& ws, cudaStream_t s) {
+    cudaError_t err = update_and_chain<Tin, false>(k, v, dec, init, final, cmap, smap, n_chunks, n_seqs, H, dk, dv,
+                                                   ws.S, ws.gam, s);
+    if (err != cudaSuccess || n_chunks == 0) return err;
+    const dim3 grid(n_chunks, H, dv / 64);
+    auto kern = dk == 128 ? lin_out<Tin, 128> : lin_out<Tin, 64>;
+    const size_t smem = dk == 128 ? out_smem<128>() : out_smem<64>();
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+        return err;
+    kern<<<grid, kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, cmap, H, dv, ws.S, (Tin*)o);
+    return cudaGetLastError();
+}
+
+template <typename Tin, int DK, int DV>
+cudaError_t grad(const void* q, const void* k, const void* v, LinDecay dec, const void* d_o, void* dq, void* dk,
+                 void* dv, void* dla, const ChunkMap& cmap, int n_chunks, int H, const LinSimtWorkspace& ws,
+                 cudaStream_t s) {
+    auto kern = lin_grad<Tin, DK, DV>;
+    constexpr size_t smem = grad_smem<DK, DV>();
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    kern<<<dim3(n_chunks, H), kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, (const Tin*)d_o,
+                                                   cmap, H, ws.S, ws.dS, (Tin*)dq, (Tin*)dk, (Tin*)dv,
+                                                   dec.per_head ? nullptr : (Tin*)dla);
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t bwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init, const void* d_o,
+                const float* d_final, void* dq, void* dk_out, void* dv_out, void* dla, float* d_init,
+                const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
+                const LinSimtWorkspace& ws, cudaStream_t s) {
+    cudaError_t err = update_and_chain<Tin, false>(k, v, dec, init, nullptr, cmap, smap, n_chunks, n_seqs, H, dk, dv,
+                                                   ws.S, ws.gam, s);
+    if (err != cudaSuccess) return err;
+    err = update_and_chain<Tin, true>(q, d_o, dec, d_final, d_init, cmap, smap, n_chunks, n_seqs, H, dk, dv, ws.dS,
+                                      ws.gam, s);
+    if (err != cudaSuccess || n_chunks == 0) return err;
+    if (dk == 128 && dv == 128)
+        return grad<Tin, 128, 128>(q, k, v, dec, d_o, dq, dk_out, dv_out, dla, cmap, n_chunks, H, ws, s);
+    if (dk == 128) return grad<Tin, 128, 64>(q, k, v, dec, d_o, dq, dk_out, dv_out, dla, cmap, n_chunks, H, ws, s);
+    if (dv == 128) return grad<Tin, 64, 128>(q, k, v, dec, d_o, dq, dk_out, dv_out, dla, cmap, n_chunks, H, ws, s);
+    return grad<Tin, 64, 64>(q, k, v, dec, d_o, dq, dk_out, dv_out, dla, cmap, n_chunks, H, ws, s);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_simt_fwd(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
+                                const float* init_state, void* o, float* final_state, const ChunkMap& cmap,
+                                const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
+                                const LinSimtWorkspace& ws, cudaStream_t stream) {
+    auto f = dtype == KDA_F32 ? fwd<float> : fwd<__nv_bfloat16>;
+    return f(q, k, v, dec, init_state, o, final_state, cmap, smap, n_chunks, n_seqs, H, dk, dv, ws, stream);
+}
+
+cudaError_t launch_lin_simt_bwd(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
+                                const float* init_state, const void* d_o, const float* d_final, void* dq, void* dk_out,
+                                void* dv_out, void* dla, float* d_init, const ChunkMap& cmap, const SeqMap& smap,
+                                int n_chunks, int n_seqs, int H, int dk, int dv, const LinSimtWorkspace& ws,
+                                cudaStream_t stream) {
+    auto f = dtype == KDA_F32 ? bwd<float> : bwd<__nv_bfloat16>;
+    return f(q, k, v, dec, init_state, d_o, d_final, dq, dk_out, dv_out, dla, d_init, cmap, smap, n_chunks, n_seqs, H,
+             dk, dv, ws, stream);
+}
+
+}  // namespace kda

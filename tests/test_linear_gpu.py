@@ -1,0 +1,418 @@
+"""Linear attention with one decay a head on the GPU against the fp64 recurrence.
+
+Tolerances.  Every output is a sum of products; with all inputs replaced by their
+absolute values the same recurrence gives, element by element, the sum A of the
+terms' magnitudes, and an output whose terms are each off by at most a relative u is
+off by at most u A.
+* fp32 arithmetic: a term passes the decay (2^-22 from 2^x, 3 * 2^-24 from its
+  argument), at most 128 + 64 + 64 additions inside a chunk and two roundings a chunk
+  for the carry: u = 2^-15 holds up to 100 chunks.
+* tensor cores (bf16, 128 x 128): an operand rounded to bf16 is off by 2^-8 at most;
+  the terms of o and of dq, dk, dv carry one such operand (the scores, or the state's
+  copy), those of dlog_alpha two (the state and its gradient): u = 2^-8, 2^-7, plus
+  the fp32 part.  States see the weighted keys or queries as a bf16 pair (2^-16) and
+  fp32 sums (2^-17 a chunk): u = 2^-15.
+* bf16 results are rounded once more: 2^-8 of the value.
+The same results are also held to the framework's parity bound on max |d| / rms.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.linear as ol
+from kda_inputs import to_f64
+from kda_testlib import TOL, parity
+
+pytestmark = pytest.mark.gpu
+
+F32U = 2.0 ** -15
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _tc(dt, dk, dv):
+    return dt == "bf16" and dk == 128 and dv == 128
+
+
+def make(dt, lens, H, dk, dv, packed, decay="token", init=True, seed=0, la="mixed"):
+    """Inputs on the GPU; `lens` of equal lengths when not packed."""
+    g = torch.Generator().manual_seed(seed)
+    N, n = len(lens), sum(lens)
+    rows = (1, n) if packed else (N, lens[0])
+    unit = lambda *s: torch.nn.functional.normalize(torch.randn(*s, generator=g), dim=-1)
+    x = dict(q=unit(*rows, H, dk), k=unit(*rows, H, dk), v=torch.randn(*rows, H, dv, generator=g),
+             d_o=torch.randn(*rows, H, dv, generator=g))
+    if decay == "head":
+        a = -0.5 * torch.rand(H, generator=g)
+        a[0] = 0.0
+    else:
+        a = -torch.nn.functional.softplus(torch.randn(*rows, H, generator=g) - 2)
+        if la == "hard":     # resets, the floor and no decay at all among ordinary tokens
+            pick = torch.randint(0, 6, a.shape, generator=g)
+            a = torch.where(pick == 0, torch.full_like(a, -float("inf")), a)
+            a = torch.where(pick == 1, torch.full_like(a, -150.0), a)
+            a = torch.where(pick == 2, torch.zeros_like(a), a)
+            a = torch.where(pick == 3, torch.full_like(a, -30.0), a)
+    out = {k: v.to(DT[dt]).cuda() for k, v in x.items()}
+    out["log_alpha"] = (a if decay == "head" else a.to(DT[dt])).cuda()
+    out["init"] = (0.5 * torch.randn(N, H, dk, dv, generator=g)).cuda() if init else None
+    out["d_final"] = (0.5 * torch.randn(N, H, dk, dv, generator=g)).cuda() if init else None
+    out["ss"] = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    out["cu"] = [int(c) for c in out["ss"]] if packed else None
+    return out
+
+
+def ref_args(x, absolute=False):
+    f = (lambda t: np.abs(to_f64(t))) if absolute else to_f64
+    flat = lambda t: f(t).reshape(-1, *t.shape[2:])
+    q, k, v = (flat(x[n]) for n in ("q", "k", "v"))
+    la = to_f64(x["log_alpha"])
+    la = np.broadcast_to(la, q.shape[:2]) if la.ndim == 1 else la.reshape(q.shape[:2])
+    opt = lambda t: None if t is None else f(t)
+    return q, k, v, la, opt(x["init"]), flat(x["d_o"]), opt(x["d_final"])
+
+
+def close(label, got, ref, bound):
+    """|got - ref| within the element's bound everywhere; says by how much of it."""
+    got = to_f64(got).reshape(ref.shape)
+    assert np.isfinite(got).all(), label
+    d = np.abs(got - ref)
+    worst = float((d / np.maximum(bound, 1e-30)).max()) if d.size else 0.0
+    assert worst <= 1.0, f"{label}: {worst:.3f} of the bound"
+
+
+def check_fwd(x, dt, dk, dv, o, fs, label):
+    q, k, v, la, s0, _, _ = ref_args(x)
+    o_ref, fs_ref = ol.forward(q, k, v, la, x["ss"], s0)
+    q, k, v, la, s0, _, _ = ref_args(x, True)
+    o_abs, fs_abs = ol.forward(q, k, v, la, x["ss"], s0)
+    u = F32U + (2.0 ** -8 if _tc(dt, dk, dv) else 0.0)
+    if o_ref.size:
+        close(label + " o", o, o_ref, u * o_abs + (2.0 ** -8 * np.abs(o_ref) if dt == "bf16" else 0.0))
+        assert parity(label + " o", to_f64(o).reshape(o_ref.shape), o_ref, TOL[dt], stored_as=dt) <= TOL[dt]
+    if fs is not None:
+        close(label + " state", fs, fs_ref, F32U * fs_abs)
+        assert parity(label + " state", to_f64(fs), fs_ref, TOL["f32"]) <= TOL["f32"]
+
+
+def check_bwd(x, dt, dk, dv, grads, label):
+    q, k, v, la, s0, do, df = ref_args(x)
+    ref = ol.backward(q, k, v, la, x["ss"], do, df, s0)
+    q, k, v, la, s0, do, df = ref_args(x, True)
+    mag = ol.backward(q, k, v, la, x["ss"], do, df, s0)
+    tc = _tc(dt, dk, dv)
+    for name, got in zip(("dq", "dk", "dv", "dlog_alpha", "d_init_state"), grads):
+        if got is None or ref[name].size == 0:
+            continue
+        u = F32U
+        if tc and name != "d_init_state":
+            u += 2.0 ** -7 if name == "dlog_alpha" else 2.0 ** -8
+        b = u * mag[name]
+        if got.dtype == torch.bfloat16:
+            b = b + 2.0 ** -8 * np.abs(ref[name])
+        close(f"{label} {name}", got, ref[name], b)
+        tol = TOL["f32"] if name == "d_init_state" else TOL[dt]
+        assert parity(f"{label} {name}", to_f64(got).reshape(ref[name].shape), ref[name], tol,
+                      stored_as="bf16" if got.dtype == torch.bfloat16 else None) <= tol
+
+
+SHAPES = [  # dtype, lengths, heads, dk, dv, packed, decay, initial state, gates
+    ("f32", (256,), 2, 64, 64, False, "token", False, "mixed"),
+    ("f32", (1,), 1, 64, 128, False, "token", True, "mixed"),
+    ("f32", (65, 65), 3, 128, 64, False, "head", True, "mixed"),
+    ("f32", (130, 0, 1, 64, 63), 2, 128, 128, True, "token", True, "hard"),
+    ("bf16", (100, 37), 2, 64, 64, True, "token", True, "mixed"),
+    ("bf16", (70,), 2, 64, 128, False, "head", False, "mixed"),
+    ("bf16", (1,), 1, 128, 128, False, "token", True, "mixed"),
+    ("bf16", (1, 1, 1), 2, 128, 128, False, "head", True, "mixed"),
+    ("bf16", (127,), 2, 128, 128, False, "token", False, "mixed"),
+    ("bf16", (128, 128), 2, 128, 128, False, "token", True, "hard"),
+    ("bf16", (129, 129), 1, 128, 128, False, "token", True, "mixed"),
+    ("bf16", (700,), 2, 128, 128, False, "token", True, "mixed"),
+    ("bf16", (300, 0, 1, 64, 511, 0), 3, 128, 128, True, "token", True, "hard"),
+    ("bf16", (257, 900, 2), 2, 128, 128, True, "head", False, "mixed"),
+    ("bf16", (1400, 5, 640), 1, 128, 128, True, "token", True, "mixed"),
+]
+IDS = ["-".join(str(y) for y in s).replace(" ", "") for s in SHAPES]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_forward(cuda_ok, shape):
+    import kimi_delta_attention_30_b200 as kda
+    dt, lens, H, dk, dv, packed, decay, init, la = shape
+    x = make(dt, lens, H, dk, dv, packed, decay, init, seed=3, la=la)
+    o, fs = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"])
+    torch.cuda.synchronize()
+    check_fwd(x, dt, dk, dv, o, fs, "lin_fwd " + IDS[SHAPES.index(shape)])
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_backward(cuda_ok, shape):
+    import kimi_delta_attention_30_b200 as kda
+    dt, lens, H, dk, dv, packed, decay, init, la = shape
+    x = make(dt, lens, H, dk, dv, packed, decay, init, seed=4, la=la)
+    grads = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                 d_final_state=x["d_final"], cu_seqlens=x["cu"])
+    torch.cuda.synchronize()
+    assert (grads[3] is None) == (decay == "head")
+    check_bwd(x, dt, dk, dv, grads, "lin_bwd " + IDS[SHAPES.index(shape)])
+
+
+@pytest.mark.parametrize("dt,N,H,dk,dv,decay", [
+    ("bf16", 1, 1, 128, 128, "token"), ("bf16", 7, 5, 64, 128, "head"), ("f32", 3, 2, 128, 64, "token"),
+    ("f32", 1, 32, 64, 64, "head"), ("bf16", 80, 8, 128, 128, "token"), ("f32", 150, 2, 128, 128, "token")])
+def test_decode(cuda_ok, dt, N, H, dk, dv, decay):
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, (1,) * N, H, dk, dv, False, decay, True, seed=6, la="hard")
+    state = x["init"].clone()
+    la = x["log_alpha"] if decay == "head" else x["log_alpha"][:, 0]
+    o = kda.linear_decode_step(x["q"][:, 0], x["k"][:, 0], x["v"][:, 0], la, state)
+    torch.cuda.synchronize()
+    sq = lambda t: to_f64(t)[:, 0]
+    la64 = np.broadcast_to(to_f64(la), (N, H))
+    o_ref, s_ref = ol.decode_step(sq(x["q"]), sq(x["k"]), sq(x["v"]), la64, to_f64(x["init"]))
+    ab = lambda t: np.abs(sq(t))
+    o_abs, s_abs = ol.decode_step(ab(x["q"]), ab(x["k"]), ab(x["v"]), la64, np.abs(to_f64(x["init"])))
+    close("o", o, o_ref, F32U * o_abs + (2.0 ** -8 * np.abs(o_ref) if dt == "bf16" else 0.0))
+    close("state", state, s_ref, 2.0 ** -21 * s_abs)   # exp (2 ulp), a product and a sum
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_no_tokens(cuda_ok, dt):
+    import kimi_delta_attention_30_b200 as kda
+    d = 128
+    for T, B, cu in ((0, 2, None), (0, 1, [0, 0, 0])):
+        e = torch.zeros(B, T, 3, d, dtype=DT[dt], device="cuda")
+        la = torch.zeros(B, T, 3, dtype=DT[dt], device="cuda")
+        s0 = torch.randn(2, 3, d, d, device="cuda")
+        _, fs = kda.linear_chunk_fwd(e, e, e, la, init_state=s0, cu_seqlens=cu)
+        assert torch.equal(fs, s0)
+        _, fs = kda.linear_chunk_fwd(e, e, e, la, cu_seqlens=cu)
+        assert not fs.any()
+        assert torch.equal(kda.linear_chunk_bwd(e, e, e, la, e, init_state=s0, d_final_state=s0, cu_seqlens=cu)[4], s0)
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_other_sequences_do_not_matter(cuda_ok, dt, d):
+    """A packed sequence's results are the same bits whatever stands in its neighbours,
+    NaN and infinities among them; and they do not depend on what the workspace held."""
+    import kimi_delta_attention_30_b200 as kda
+    lens = (70, 90, 200, 3, 131)
+    x = make(dt, lens, 2, d, d, True, seed=8)
+    need = kda.linear_workspace_size(1, sum(lens), 2, d, d, DT[dt], cu_seqlens=x["cu"], backward=True)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def run(x):
+        ws.fill_(0xFF)
+        o, fs = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"],
+                                     cu_seqlens=x["cu"], workspace=ws)
+        ws.fill_(0xFF)
+        g = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                 d_final_state=x["d_final"], cu_seqlens=x["cu"], workspace=ws)
+        torch.cuda.synchronize()
+        return o, fs, g
+
+    o, fs, g = run(x)
+    y = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in x.items()}
+    for s in (0, 2, 4):
+        a, b = x["cu"][s], x["cu"][s + 1]
+        y["q"][:, a:b], y["k"][:, a:b] = float("nan"), float("inf")
+        y["v"][:, a:b], y["d_o"][:, a:b] = float("nan"), float("-inf")
+        y["init"][s] = float("nan")
+    o2, fs2, g2 = run(y)
+    for s in (1, 3):
+        a, b = x["cu"][s], x["cu"][s + 1]
+        assert torch.equal(o[:, a:b], o2[:, a:b]) and torch.equal(fs[s], fs2[s])
+        for t, u in zip(g[:4], g2[:4]):
+            assert torch.equal(t[:, a:b], u[:, a:b])
+        assert torch.equal(g[4][s], g2[4][s])
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_optional_outputs_aliases_and_repeats(cuda_ok, dt, d):
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, (300, 300), 2, d, d, False, seed=9)
+    args = (x["q"], x["k"], x["v"], x["log_alpha"])
+    o, fs = kda.linear_chunk_fwd(*args, init_state=x["init"])
+    s = x["init"].clone()
+    o2, s2 = kda.linear_chunk_fwd(*args, init_state=s, final_state=s)
+    assert s2 is s and torch.equal(o, o2) and torch.equal(fs, s)
+    o3, none = kda.linear_chunk_fwd(*args, init_state=x["init"], output_final_state=False)
+    assert none is None and torch.equal(o, o3)
+    g = kda.linear_chunk_bwd(*args, x["d_o"], init_state=x["init"], d_final_state=x["d_final"])
+    ds = x["d_final"].clone()
+    like = tuple(torch.empty_like(t) for t in args)
+    g2 = kda.linear_chunk_bwd(*args, x["d_o"], init_state=x["init"], d_final_state=ds,
+                              grads=(like[0], like[1], like[2], like[3], ds))
+    assert all(torch.equal(a, b) for a, b in zip(g, g2))
+    g3 = kda.linear_chunk_bwd(*args, x["d_o"], init_state=x["init"], d_final_state=x["d_final"],
+                              need_d_init_state=False)
+    assert g3[4] is None and all(torch.equal(a, b) for a, b in zip(g[:4], g3[:4]))
+    # no final gradient is a zero one; no initial state a zero one
+    g4 = kda.linear_chunk_bwd(*args, x["d_o"])
+    z = torch.zeros_like(x["init"])
+    g5 = kda.linear_chunk_bwd(*args, x["d_o"], init_state=z, d_final_state=z)
+    assert all(torch.equal(a, b) for a, b in zip(g4, g5))
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_streams_and_graphs(cuda_ok, dt, d):
+    """Two calls at once on two streams, and a captured forward and backward replayed on
+    new inputs while an eager call with a workspace of its own runs in between."""
+    import kimi_delta_attention_30_b200 as kda
+    xs = [make(dt, (260, 70, 3), 4, d, d, True, seed=s) for s in (20, 21, 22)]
+
+    def both(x):
+        o, fs = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"])
+        g = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                 d_final_state=x["d_final"], cu_seqlens=x["cu"])
+        return (o, fs) + g
+
+    want = [both(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for x, s in zip(xs, streams):
+        with torch.cuda.stream(s):
+            got.append(both(x))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(t, u) for t, u in zip(a, b))
+    # explicit stream argument
+    s = streams[0]
+    s.wait_stream(torch.cuda.current_stream())
+    x = xs[1]
+    o, _ = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"],
+                                stream=s)
+    s.synchronize()
+    assert torch.equal(o, want[1][0])
+
+    static = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in xs[0].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(static)
+    for i in (1, 2, 0):
+        for k in ("q", "k", "v", "log_alpha", "init", "d_o", "d_final"):
+            static[k].copy_(xs[i][k])
+        both(xs[(i + 1) % 3])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_padded_rows_stay(cuda_ok, dt, d):
+    """Rows behind the last sequence are no part of the call: outputs passed in keep them."""
+    import kimi_delta_attention_30_b200 as kda
+    lens = (70, 30)
+    x = make(dt, lens, 2, d, d, True, seed=30)
+    n, pad = sum(lens), 28
+    base = torch.full((1, n + pad, 2, d), 7.0, dtype=DT[dt], device="cuda")
+    kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"],
+                         o=base[:, :n])
+    want, _ = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"])
+    assert torch.equal(base[:, :n], want) and (base[:, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_prompt_then_tokens(cuda_ok, dt, d):
+    """A prompt, then single tokens, equal the whole sequence at once; the norm with
+    rotation before either, by positions."""
+    import kimi_delta_attention_30_b200 as kda
+    N, T, n, H = 2, 150, 4, 2
+    g = torch.Generator().manual_seed(40)
+    proj = torch.randn(N, T + n, 3 * H * d, generator=g).to(DT[dt]).cuda()
+    la = (-0.1 * torch.rand(N, T + n, H, generator=g)).to(DT[dt]).cuda()
+    w = (1 + 0.1 * torch.randn(d, generator=g)).to(DT[dt]).cuda()
+    fr = (10000.0 ** (-torch.arange(0, d, 2) / d)).float().cuda()
+
+    def step(a, b):
+        x = proj[:, a:b].unflatten(-1, (3 * H, d))
+        pos = torch.arange(a, b, dtype=torch.int32, device="cuda").expand(N, b - a).contiguous()
+        x = x.contiguous() if (a, b) != (0, T + n) else x
+        q, k = kda.qk_norm_rope(x[:, :, :H], x[:, :, H:2 * H], w, w, pos, fr)
+        return q, k, x[:, :, 2 * H:].contiguous()
+
+    q, k, v = step(0, T + n)
+    whole, final = kda.linear_chunk_fwd(q, k, v, la)
+    q0, k0, v0 = step(0, T)
+    o, state = kda.linear_chunk_fwd(q0, k0, v0, la[:, :T].contiguous())
+    outs = [o]
+    for t in range(T, T + n):
+        q1, k1, v1 = step(t, t + 1)
+        outs.append(kda.linear_decode_step(q1[:, 0], k1[:, 0], v1[:, 0], la[:, t].contiguous(), state)[:, None])
+    torch.cuda.synchronize()
+    # |q| = |k| = sqrt(d): terms are d times larger than with unit rows, so are the bounds
+    ss = np.array([0, T + n, 2 * (T + n)])
+    fl = lambda t: to_f64(t).reshape(-1, *t.shape[2:])
+    o_ref, f_ref = ol.forward(fl(q), fl(k), fl(v), fl(la), ss)
+    o_abs, f_abs = ol.forward(np.abs(fl(q)), np.abs(fl(k)), np.abs(fl(v)), fl(la), ss)
+    u = F32U + (2.0 ** -8 if _tc(dt, d, d) else 0.0)
+    b = u * o_abs + (2.0 ** -8 * np.abs(o_ref) if dt == "bf16" else 0.0)
+    close("whole", whole, o_ref, b)
+    close("in parts", torch.cat(outs, 1), o_ref, b)
+    close("whole state", final, f_ref, F32U * f_abs)
+    close("state in parts", state, f_ref, F32U * f_abs)
+
+
+def test_autograd_matches_linear_chunk_bwd(cuda_ok):
+    import kimi_delta_attention_30_b200 as kda
+    from kimi_delta_attention_30_b200.autograd import linear_chunk
+    x = make("bf16", (200, 90), 2, 128, 128, True, seed=50)
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "log_alpha", "init")]
+    o, fs = linear_chunk(*leaves, cu_seqlens=x["cu"])
+    torch.autograd.backward([o, fs], [x["d_o"], x["d_final"]])
+    ref = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                               d_final_state=x["d_final"], cu_seqlens=x["cu"])
+    for a, b in zip(leaves, ref):
+        assert a.grad.dtype == a.dtype and torch.equal(a.grad, b)
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128)])
+def test_gradients_against_differences(cuda_ok, dt, d):
+    """The loss's change along a random direction, from the fp64 recurrence at the same
+    (rounded) inputs, against the kernels' gradients: relative to the sum of magnitudes,
+    2^-8 for gradients that are stored as bf16, fp32 sums otherwise."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, (150,), 1, d, d, False, seed=60)
+    grads = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                 d_final_state=x["d_final"])
+    q, k, v, la, s0, do, df = ref_args(x)
+    mag = ol.backward(*ref_args(x, True)[:4], x["ss"], *(ref_args(x, True)[i] for i in (5, 6, 4)))
+    r = np.random.default_rng(0)
+    args = [q, k, v, la, s0]
+    h = 1e-6
+    for i, name in enumerate(("dq", "dk", "dv", "dlog_alpha", "d_init_state")):
+        u = r.normal(size=args[i].shape)
+        up, dn = list(args), list(args)
+        up[i], dn[i] = args[i] + h * u, args[i] - h * u
+        f = lambda a: [(y * z).sum() for y, z in zip(ol.forward(a[0], a[1], a[2], a[3], x["ss"], a[4]), (do, df))]
+        diff = (sum(f(up)) - sum(f(dn))) / (2 * h)
+        got = float((to_f64(grads[i]).reshape(u.shape) * u).sum())
+        tol = (2.0 ** -7 + 2.0 ** -8 if dt == "bf16" and i < 4 else F32U) * (mag[name] * np.abs(u)).sum() + 1e-5
+        assert abs(diff - got) <= tol, name
+
+
+def test_far_offsets(cuda_ok):
+    """Element offsets past 2^31: the last sequences of a packed batch of 2^24 token-heads."""
+    import kimi_delta_attention_30_b200 as kda
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    H, d, tail = 256, 128, (130, 1, 140)
+    n = 66000
+    cu = [0] + [n - sum(tail)]
+    for t in tail:
+        cu.append(cu[-1] + t)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda: torch.empty(1, n, H, d, dtype=torch.bfloat16, device="cuda").normal_(0, 0.09, generator=g)
+    q, k, v = mk(), mk(), mk()
+    la = torch.empty(1, n, H, dtype=torch.bfloat16, device="cuda").uniform_(-0.2, 0, generator=g)
+    o, fs = kda.linear_chunk_fwd(q, k, v, la, cu_seqlens=cu)
+    a = cu[1]
+    heads = [0, 100, 255]
+    pick = lambda t: to_f64(t[0, a:][:, heads])
+    ss = np.concatenate([[0], np.cumsum(tail)])
+    o_ref, f_ref = ol.forward(pick(q), pick(k), pick(v), pick(la), ss)
+    o_abs, f_abs = ol.forward(np.abs(pick(q)), np.abs(pick(k)), np.abs(pick(v)), pick(la), ss)
+    close("o", o[0, a:][:, heads], o_ref, (F32U + 2.0 ** -8) * o_abs + 2.0 ** -8 * np.abs(o_ref))
+    close("state", fs[1:, heads], f_ref, F32U * f_abs)
