@@ -513,6 +513,11 @@ KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void
                                         const int32_t* cu_seqlens_host, int n_seqs, int B, int T, int H, int dk,
                                         int dv, void* o, float* final_state, void* workspace,
                                         size_t workspace_bytes, void* stream);
+/* Device-side status of the last kda_linear_chunk_fwd call that used `workspace`
+ * with these sizes, as kda_chunk_fwd_device_status (synchronises `stream`). */
+KDA_API kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda_dtype dtype,
+                                                      const int32_t* cu_seqlens_host, int n_seqs, int B, int T,
+                                                      int H, int dk, int dv, void* stream);
 
 /*
  * Gradients of sum(d_o * o) + sum(d_final_state * final_state) for the call

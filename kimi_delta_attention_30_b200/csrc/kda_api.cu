@@ -124,9 +124,13 @@ kda_status make_plan(int B, int T, int H, int dk, int dv, int C, const int32_t* 
     if (H <= 0 || B < 0 || T < 0) return KDA_ERR_SHAPE;
     if (!((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return KDA_ERR_SHAPE;
     if (C != 64 && C != 128) return KDA_ERR_CHUNK;
+    return plan_sequences(B, T, C, cu, n_seqs, p);
+}
+
+kda_status plan_sequences(int B, int T, int C, const int32_t* cu, int n_seqs, Plan& p) {
     if (cu == nullptr) {
         p.n_seqs = B;
-        long long ncps = (T + C - 1) / C;
+        long long ncps = ((long long)T + C - 1) / C;
         if ((long long)B * ncps > 0x7fffffffLL || (long long)B * T > 0x7fffffffLL) return KDA_ERR_SHAPE;
         p.n_chunks = (int)(B * ncps);
         p.total_tokens = (long long)B * T;
@@ -143,7 +147,7 @@ kda_status make_plan(int B, int T, int H, int dk, int dv, int C, const int32_t* 
         if (cu[s + 1] < cu[s]) return KDA_ERR_SEQLENS;
         int len = cu[s + 1] - cu[s];
         p.natural[s] = SeqInfo{cu[s], len, (int)chunks, s};
-        chunks += (len + C - 1) / C;
+        chunks += ((long long)len + C - 1) / C;
     }
     if (chunks > 0x7fffffffLL) return KDA_ERR_SHAPE;
     p.n_chunks = (int)chunks;

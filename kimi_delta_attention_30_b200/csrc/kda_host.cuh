@@ -26,6 +26,9 @@ struct Plan {
 
 kda_status make_plan(int B, int T, int H, int dk, int dv, int C, const int32_t* cu, int n_seqs, Plan& p);
 
+// The same for checked sizes and chunks of any length C.
+kda_status plan_sequences(int B, int T, int C, const int32_t* cu, int n_seqs, Plan& p);
+
 // Bytes of the sequence tables and the chunk table at the start of a workspace.
 size_t table_bytes(const Plan& p);
 // The per-chunk table follows the two sequence tables.

@@ -47,4 +47,18 @@ cudaError_t launch_lin_simt_bwd(kda_dtype dtype, const void* q, const void* k, c
 cudaError_t launch_lin_decode(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,
                               float* state, int N, int H, int dk, int dv, void* o, cudaStream_t stream);
 
+// ---- tensor-core path (bf16, 128 x 128): 128-token chunks, walked in segments ------
+constexpr int kLinTcChunk = 128;
+
+// `segs` / `smap` number segments of segs.C tokens as the CUDA-core path numbers chunks.
+// With `split` the segments' own sums come first (seg_state [segments, H, dk, dv], seg_gam
+// [segments, H]) and are chained into start states.  BV: value columns a block, 128 or 64.
+cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init_state,
+                              void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
+                              int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
+                              float* seg_gam, int* err, cudaStream_t stream);
+// end = start (or 0) for n sequences without tokens from rank `first` of smap on
+cudaError_t launch_lin_empty_states(const float* start, float* end, const SeqMap& smap, int first, int n, int H,
+                                    cudaStream_t stream);
+
 }  // namespace kda

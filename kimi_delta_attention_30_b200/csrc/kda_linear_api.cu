@@ -23,6 +23,79 @@ LinLayout simt_layout(const Plan& p, int H, int dk, int dv, bool bwd) {
     return L;
 }
 
+bool use_tc(kda_dtype dtype, int dk, int dv) { return dtype == KDA_BF16 && dk == 128 && dv == 128; }
+
+// How the tensor-core walk is cut: segments of seg_chunks chunks, value columns a block.
+struct Cut {
+    int seg_chunks = 1;
+    int BV = 128;
+    bool split = false;
+};
+
+constexpr int kSms = 148;
+
+// Microseconds a chunk of 128 tokens takes a block (one block an SM): all 128 value
+// columns, half of them, and the state alone; and the launches that a split adds.
+constexpr double kWalk128 = 1.75, kWalk64 = 1.35, kStateOnly = 1.1, kSplitCost = 8.0;
+
+// The cut with the least estimated time.  A sequence's chunks follow one another, so with
+// few (sequence, head) pairs most SMs would idle: two blocks of 64 value columns a pair
+// repeat the scores and the weighted keys, and segments read k and v twice.
+Cut choose_cut(const Plan& chunks, int H) {
+    long long longest = 0, total = chunks.n_chunks;
+    if (chunks.varlen)
+        for (const SeqInfo& q : chunks.natural) longest = std::max<long long>(longest, (q.len + kLinTcChunk - 1) / kLinTcChunk);
+    else
+        longest = chunks.n_seqs ? total / chunks.n_seqs : 0;
+    Cut best;
+    if (longest == 0) return best;
+    best.seg_chunks = (int)longest;
+    const double work = (double)total * H / kSms;
+    double t = std::max((double)longest, work) * kWalk128;
+    const double t64 = std::max((double)longest, 2 * work) * kWalk64;
+    if (t64 < t) {
+        t = t64;
+        best.BV = 64;
+    }
+    for (int m = 1; m <= 8; ++m) {
+        const long long len = std::max<long long>(4, (long long)(total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
+        if (len >= longest) continue;
+        long long segs = 0;
+        if (chunks.varlen)
+            for (const SeqInfo& q : chunks.natural) segs += ((q.len + kLinTcChunk - 1) / kLinTcChunk + len - 1) / len;
+        else
+            segs = (longest + len - 1) / len * chunks.n_seqs;
+        const double waves = (double)((segs * H + kSms - 1) / kSms);
+        const double first = (double)(((segs - chunks.n_seqs) * H + kSms - 1) / kSms);
+        const double ts = len * (waves * kWalk128 + first * kStateOnly) + kSplitCost;
+        if (ts < t) {
+            t = ts;
+            best = Cut{(int)len, 128, true};
+        }
+    }
+    return best;
+}
+
+struct TcLayout {
+    Cut cut;
+    Plan segs;          // segments as chunks
+    size_t err, state, gam, total;
+};
+
+kda_status tc_layout(const Plan& chunks, const int32_t* cu, int n_seqs, int B, int T, int H, TcLayout& L) {
+    L.cut = choose_cut(chunks, H);
+    const kda_status st = plan_sequences(B, T, L.cut.seg_chunks * kLinTcChunk, cu, n_seqs, L.segs);
+    if (st != KDA_OK) return st;
+    if ((long long)L.segs.n_chunks * H * 2 > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    const size_t n = L.cut.split ? (size_t)L.segs.n_chunks * H : 0;
+    size_t o = table_bytes(L.segs);
+    L.err = o; o += kAlign;
+    L.state = o; o = align_up(o + n * 128 * 128 * sizeof(float));
+    L.gam = o; o = align_up(o + n * sizeof(float));
+    L.total = o;
+    return KDA_OK;
+}
+
 kda_status check_decay(kda_decay decay) {
     return decay == KDA_DECAY_TOKEN || decay == KDA_DECAY_HEAD ? KDA_OK : KDA_ERR_SHAPE;
 }
@@ -30,11 +103,11 @@ kda_status check_decay(kda_decay decay) {
 // The checks that the chunk calls share; fills the plan.  Grids put heads on y and
 // sequence-heads on x.
 kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_seqs, int B, int T, int H, int dk,
-                    int dv, Plan& p) {
+                    int dv, int C, Plan& p) {
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
     kda_status st = check_decay(decay);
     if (st != KDA_OK) return st;
-    st = make_plan(B, T, H, dk, dv, kLinSimtChunk, cu, n_seqs, p);
+    st = make_plan(B, T, H, dk, dv, C, cu, n_seqs, p);
     if (st != KDA_OK) return st;
     if (H > 65535 || (long long)p.n_seqs * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
     return KDA_OK;
@@ -84,8 +157,16 @@ size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, 
     size_t n = 0;
     guarded([&] {
         Plan p;
-        const kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, p);
-        if (st == KDA_OK) n = simt_layout(p, H, dk, dv, false).total;
+        const bool tc = use_tc(dtype, dk, dv);
+        kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                 tc ? kLinTcChunk : kLinSimtChunk, p);
+        if (st != KDA_OK) return st;
+        if (!tc) {
+            n = simt_layout(p, H, dk, dv, false).total;
+            return st;
+        }
+        TcLayout L;
+        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) == KDA_OK) n = L.total;
         return st;
     });
     return n;
@@ -97,13 +178,37 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
                                 size_t workspace_bytes, void* stream) {
     return guarded([&]() -> kda_status {
         Plan p;
-        kda_status st = plan_for(decay, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, p);
+        const bool tc = use_tc(dtype, dk, dv);
+        kda_status st = plan_for(decay, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                 tc ? kLinTcChunk : kLinSimtChunk, p);
         if (st != KDA_OK) return st;
         if (p.total_tokens > 0 && (!q || !k || !v || !log_alpha || !o)) return KDA_ERR_NULL;
         if (!workspace) return KDA_ERR_WORKSPACE;
         if (!all_aligned({q, k, v, log_alpha, (const void*)init_state, (const void*)o, (const void*)final_state}) ||
             ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
+        const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
+        if (tc) {
+            TcLayout L;
+            if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) != KDA_OK) return st;
+            if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+            if ((st = check_device()) != KDA_OK) return st;
+            if (p.n_seqs == 0) return KDA_OK;
+            cudaStream_t s = (cudaStream_t)stream;
+            char* ws = (char*)workspace;
+            ChunkMap segs;
+            SeqMap smap;
+            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws, s, segs, smap)) != KDA_OK) return st;
+            int empty = p.total_tokens == 0 ? p.n_seqs : 0;
+            if (p.varlen && p.total_tokens > 0)
+                for (const SeqInfo& q1 : p.natural) empty += q1.len == 0;
+            cudaError_t e = launch_lin_empty_states(init_state, final_state, smap, p.n_seqs - empty, empty, H, s);
+            if (e == cudaSuccess && p.total_tokens > 0)
+                e = launch_lin_tc_fwd(q, k, v, dec, init_state, o, final_state, segs, smap, L.segs.n_chunks, p.n_seqs,
+                                      L.cut.split, L.cut.BV, p.total_tokens, H, (float*)(ws + L.state),
+                                      (float*)(ws + L.gam), (int*)(ws + L.err), s);
+            return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        }
         const LinLayout L = simt_layout(p, H, dk, dv, false);
         if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
         if ((st = check_device()) != KDA_OK) return st;
@@ -114,11 +219,26 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         SeqMap smap;
         if ((st = make_maps(p, T, kLinSimtChunk, ws, s, cmap, smap)) != KDA_OK) return st;
         const LinSimtWorkspace w{(float*)(ws + L.S), nullptr, (float*)(ws + L.gam)};
-        const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
         return launch_lin_simt_fwd(dtype, q, k, v, dec, init_state, o, final_state, cmap, smap, p.n_chunks, p.n_seqs,
                                    H, dk, dv, w, s) == cudaSuccess
                    ? KDA_OK
                    : KDA_ERR_CUDA;
+    });
+}
+
+kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda_dtype dtype, const int32_t* cu_seqlens_host,
+                                              int n_seqs, int B, int T, int H, int dk, int dv, void* stream) {
+    return guarded([&]() -> kda_status {
+        Plan p;
+        const bool tc = use_tc(dtype, dk, dv);
+        kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                 tc ? kLinTcChunk : kLinSimtChunk, p);
+        if (st != KDA_OK) return st;
+        if (!workspace) return KDA_ERR_NULL;
+        if (!tc || p.total_tokens == 0) return KDA_OK;   // nothing waited
+        TcLayout L;
+        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) != KDA_OK) return st;
+        return read_error_word(workspace, L.err, stream);
     });
 }
 
@@ -127,7 +247,8 @@ size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, 
     size_t n = 0;
     guarded([&] {
         Plan p;
-        const kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, p);
+        const kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                       kLinSimtChunk, p);
         if (st == KDA_OK) n = simt_layout(p, H, dk, dv, true).total;
         return st;
     });
@@ -141,7 +262,8 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                                 void* workspace, size_t workspace_bytes, void* stream) {
     return guarded([&]() -> kda_status {
         Plan p;
-        kda_status st = plan_for(decay, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, p);
+        kda_status st = plan_for(decay, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                       kLinSimtChunk, p);
         if (st != KDA_OK) return st;
         if (p.total_tokens > 0 && (!q || !k || !v || !log_alpha || !d_o || !dq || !dk_out || !dv_out ||
                                    (decay == KDA_DECAY_TOKEN && !dlog_alpha)))

@@ -1,0 +1,620 @@
+// Linear attention with one decay a head on the tensor cores (bf16, d_k = d_v = 128).
+//
+// A block walks the 128-token chunks of one (segment, head, BV value columns) with the
+// state in fp32 registers.  For a chunk with start state S (g: inclusive sum of its log
+// decays, D_ij = e^{g_i - g_j} for j <= i):
+//   A = Q K^T                      fp32 in tensor memory
+//   P = A . D                      rounded to bf16, back into tensor memory as an A operand
+//   O = P V + e^{g} (Q S)          S read as a bf16 copy
+//   U = (e^{g_C - g} K)^T V        the weighted keys as a bf16 pair (two products)
+//   S <- e^{g_C} S + U             fp32
+// The only roundings to 8 bits are P and the copy of S that the queries read, both of the
+// kind that o itself takes when it is stored; the state sees 16-bit operands, since its
+// errors would be carried from chunk to chunk and it is returned in fp32.
+//
+// Roles: 8 warps do the elementwise work (warp w: rows 32 (w % 4) + lane, column half w / 4),
+// one thread issues the products, one the loads, one warp forms the decays.  Products of
+// chunk n + 1 that need no state (Q K^T) are issued before chunk n's state is finished, and
+// the tiles of chunk n + 1 are loaded meanwhile: five 32 KB slots hold Q, K, V in turn (Q's
+// slot is free first and takes the next V).  The low parts of the weighted keys and the
+// state's copy share one buffer, since the product that reads one ends before the other is
+// written.  Rows past a sequence's end are loaded with the box (they belong to the next
+// sequence); K's are weighted with zero, V's are cleared, Q's only reach rows of o that are
+// not stored.
+#include <algorithm>
+
+#include "kda_linear_tc.cuh"
+
+namespace kda {
+namespace lintc {
+
+bool make_map(CUtensorMap* map, const void* base, long long tokens, int H) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (Encode)fn;
+    }();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)H * kD * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kT}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int kCompute = 256;              // threads of the elementwise warps
+constexpr int kWalkThreads = kCompute + 96;
+
+// whether segment `idx` of sequence `seq` is its last
+__device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int idx) {
+    const int len = segs.seqs ? segs.seqs[seq].len : segs.T;
+    return idx == (len + segs.C - 1) / segs.C - 1;
+}
+
+// ---- outputs ------------------------------------------------------------------------
+constexpr int kSlots = 5;
+constexpr uint32_t kOffSK = kSlots * kTile;            // state copy, or low parts of the weighted keys
+constexpr uint32_t kOffGates = kOffSK + kTile;
+constexpr uint32_t kOffBars = kOffGates + 2 * sizeof(Gates);
+constexpr uint32_t kWalkSmem = kOffBars + 256;
+static_assert(kWalkSmem <= 232448, "shared memory per block");
+
+enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady, kQsDone, kKReady, kODone, kUDone, kSReady,
+               kGFull, kGEmpty = kGFull + 2, kDrain = kGEmpty + 2, kWalkBars };
+
+template <int BV>
+__global__ void __launch_bounds__(kWalkThreads, 1)
+lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+         const __grid_constant__ CUtensorMap mv, LinDecay dec, ChunkMap segs, int H,
+         const float* __restrict__ init_state, const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
+         float* __restrict__ final_state, int* __restrict__ err) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBars);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kWalkBars);   // tensor-memory base, abort
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0 && blockIdx.x == 0 && seg_start == nullptr) *err = 0;   // first kernel of the call
+    if (smem_u32(sm) & 1023u) {
+        if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
+        return;
+    }
+    const int vt = (int)(blockIdx.x % NV), h = (int)(blockIdx.x / NV % H), seg = (int)(blockIdx.x / NV / H);
+    const int j0 = vt * BV;
+    int seq, tok0, len, idx;
+    segs.locate(seg, seq, tok0, len, idx);
+    const int nch = (len + kT - 1) / kT;
+
+    if (tid == 0) {
+        for (int i = 0; i < kWalkBars; ++i)
+            mbar_init(&bars[i], i == kPReady || i == kKReady || i == kSReady || i == kGEmpty || i == kGEmpty + 1
+                                    ? kCompute
+                                    : 1);
+        mbar_init_fence();
+        flags[1] = 0u;
+    }
+    if (warp == 8) {
+        tmem_alloc(&flags[0], 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = flags[0];
+    const uint32_t tA = tbase, tU = tbase + 128, tPV = tbase + 256, tQS = tbase + 384;
+    const Abort ab{&flags[1], err};
+    auto slot = [&](int i) { return sm + (uint32_t)(i % kSlots) * kTile; };   // tile i: Q 3 n, K 3 n + 1, V 3 n + 2
+    auto full = [&](int i) { return &bars[kFull + i % kSlots]; };
+    auto full_par = [&](int i) { return (uint32_t)(i / kSlots) & 1u; };
+    Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
+    uint8_t* sk = sm + kOffSK;
+
+    if (warp == 9) {
+        if (lane == 0) {   // loads
+            int i = 0;
+            bool ok = true;
+            for (; ok && i < 3 * nch; ++i) {
+                if (i >= kSlots) ok = wait_or_abort(&bars[kEmpty + i % kSlots], (full_par(i) ^ 1u), ab);
+                if (!ok) break;
+                const int t = tok0 + (i / 3) * kT, kind = i % 3;
+                const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
+                uint8_t* dst = slot(i);
+                if (kind < 2 || BV == 128) {
+                    mbar_arrive_expect_tx(full(i), kTile);
+                    tma_box(dst, m, 0, h, t, full(i));
+                    tma_box(dst + kBlock, m, 64, h, t, full(i));
+                } else {
+                    mbar_arrive_expect_tx(full(i), kBlock);
+                    tma_box(dst, m, j0, h, t, full(i));
+                }
+            }
+            if (!ok)   // given up: the copies in flight land before the block ends
+                for (int j = max(0, i - kSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
+        }
+    } else if (warp == 10) {   // decays
+        float x[4], y[4];
+        load_gates(x, dec, tok0, min(kT, len), H, h, lane);
+        for (int n = 0; n < nch; ++n) {
+            if (n + 1 < nch) load_gates(y, dec, (long long)tok0 + (n + 1) * kT, min(kT, len - (n + 1) * kT), H, h, lane);
+            if (n >= 2 && !wait_or_abort(&bars[kGEmpty + (n & 1)], ((uint32_t)(n >> 1) & 1u) ^ 1u, ab)) break;
+            make_gates(&gates[n & 1], x, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kGFull + (n & 1)]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = y[u];
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {   // products
+            constexpr uint32_t iS = idesc_bf16_f32(128, 128), iB = idesc_bf16_f32_bmn(128, BV),
+                               iU = idesc_amn_bmn(128, BV);
+            auto scores = [&](int n) {
+                if (!wait_or_abort(full(3 * n), full_par(3 * n), ab) ||
+                    !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
+                    return false;
+                const uint32_t a = smem_u32(slot(3 * n)), b = smem_u32(slot(3 * n + 1));
+#pragma unroll
+                for (int s = 0; s < kD / 16; ++s)
+                    mma_bf16(tA, sw128_desc_k(a, kT, s), sw128_desc_k(b, kT, s), iS, s > 0);
+                mma_commit(&bars[kScores]);
+                return true;
+            };
+            bool ok = nch > 0 && scores(0);
+            for (int n = 0; ok && n < nch; ++n) {
+                const uint32_t par = (uint32_t)n & 1u;
+                const uint32_t q = smem_u32(slot(3 * n)), k = smem_u32(slot(3 * n + 1)), v = smem_u32(slot(3 * n + 2));
+                // Q S
+                if (!(ok = wait_or_abort(&bars[kSReady], par, ab))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kD / 16; ++s)
+                    mma_bf16(tQS, sw128_desc_k(q, kT, s), mn_desc_k(smem_u32(sk), kD, s), iB, s > 0);
+                mma_commit(&bars[kQsDone]);
+                mma_commit(&bars[kEmpty + (3 * n) % kSlots]);
+                // P V
+                if (!(ok = wait_or_abort(&bars[kPReady], par, ab) &&
+                           wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)))
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s)
+                    mma_bf16_ta(tPV, tA + (s < 4 ? 8 * s : 64 + 8 * (s - 4)), mn_desc_k(v, kT, s), iB, s > 0);
+                mma_commit(&bars[kODone]);
+                // weighted K^T V, high then low parts
+                if (!(ok = wait_or_abort(&bars[kKReady], par, ab))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s)
+                    mma_bf16(tU, mn_desc_k(k, kT, s), mn_desc_k(v, kT, s), iU, s > 0);
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s)
+                    mma_bf16(tU, mn_desc_k(smem_u32(sk), kT, s), mn_desc_k(v, kT, s), iU, 1u);
+                mma_commit(&bars[kUDone]);
+                mma_commit(&bars[kEmpty + (3 * n + 1) % kSlots]);
+                mma_commit(&bars[kEmpty + (3 * n + 2) % kSlots]);
+                // the next chunk's scores, once P has been read
+                if (n + 1 < nch) ok = wait_or_abort(&bars[kODone], par, ab) && scores(n + 1);
+            }
+            if (!ok) {   // given up: products in flight end before the tensor memory is freed
+                mma_commit(&bars[kDrain]);
+                mbar_wait(&bars[kDrain], 0u);
+            }
+        }
+    } else {
+        const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
+        const uint32_t lanes = (uint32_t)(32 * sp) << 16;
+        float s[HB];   // state row `row`, columns j0 + HB hb + [0, HB)
+        {
+            const float* src = seg_start ? seg_start + ((size_t)seg * H + h) * kD * kD
+                               : init_state ? init_state + ((size_t)seq * H + h) * kD * kD
+                                            : nullptr;
+#pragma unroll
+            for (int j = 0; j < HB; j += 4) {
+                const float4 x = src ? *reinterpret_cast<const float4*>(src + (size_t)row * kD + j0 + HB * hb + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+            }
+        }
+        auto publish = [&]() {   // the state's bf16 copy, an MN-major B operand
+#pragma unroll
+            for (int j = 0; j < HB; j += 8) {
+                const uint4 w = make_uint4(pack_bf16(s[j], s[j + 1]), pack_bf16(s[j + 2], s[j + 3]),
+                                           pack_bf16(s[j + 4], s[j + 5]), pack_bf16(s[j + 6], s[j + 7]));
+                *reinterpret_cast<uint4*>(sk + mn_chunk(row, HB * hb + j, kD)) = w;
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(&bars[kSReady]);
+        };
+        publish();
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t par = (uint32_t)n & 1u;
+            const int live = min(kT, len - n * kT);
+            const Gates& G = gates[n & 1];
+            if (!wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab)) break;
+            if (live < kT) {
+                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
+                zero_rows(slot(3 * n + 2), BV / 64, live, tid);
+                fence_async_smem();
+            }
+            if (!wait_or_abort(&bars[kScores], par, ab)) break;
+            tc_fence_after();
+            {   // P: this thread's row, two blocks of 32 keys
+                const float er = G.erel[row], r2 = G.rel2[row];
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                    const int B = 2 * hb + bb;
+                    uint32_t w[16];
+                    if (B > sp) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = 0u;
+                    } else {
+                        float a[2][16];
+                        tmem_ld16(tA + lanes + 32 * B, a[0]);
+                        tmem_ld16(tA + lanes + 32 * B + 16, a[1]);
+                        tmem_ld_wait();
+                        if (B < sp) {
+                            const float f = er * G.fac[sp][B];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 c = *reinterpret_cast<const float4*>(&G.col[32 * B + e]);
+                                float* x = &a[e >> 4][e & 15];
+                                w[e / 2] = pack_bf16(x[0] * (f * c.x), x[1] * (f * c.y));
+                                w[e / 2 + 1] = pack_bf16(x[2] * (f * c.z), x[3] * (f * c.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 c = *reinterpret_cast<const float4*>(&G.rel2[32 * B + e]);
+                                float* x = &a[e >> 4][e & 15];
+                                const float y0 = e <= lane ? x[0] * ex2_approx(r2 - c.x) : 0.f;
+                                const float y1 = e + 1 <= lane ? x[1] * ex2_approx(r2 - c.y) : 0.f;
+                                const float y2 = e + 2 <= lane ? x[2] * ex2_approx(r2 - c.z) : 0.f;
+                                const float y3 = e + 3 <= lane ? x[3] * ex2_approx(r2 - c.w) : 0.f;
+                                w[e / 2] = pack_bf16(y0, y1);
+                                w[e / 2 + 1] = pack_bf16(y2, y3);
+                            }
+                        }
+                    }
+                    // over this warp's own columns of the scores, of which block 2 hb is read by now
+                    if (bb == 1) tmem_ld_wait();
+                    tmem_st16u(tA + lanes + 64 * hb + 16 * bb, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars[kPReady]);
+            }
+            // weighted keys: row tid % 128, channel block tid / 128
+            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) ||
+                !wait_or_abort(&bars[kQsDone], par, ab))
+                break;
+            {
+                const int r = tid & 127;
+                scale_split_row(slot(3 * n + 1), sk, r, tid >> 7, G.col[r] * G.end[r >> 5], r < live);
+                fence_async_smem();
+                mbar_arrive(&bars[kKReady]);
+            }
+            // o = P V + e^g (Q S)
+            if (!wait_or_abort(&bars[kODone], par, ab)) break;
+            tc_fence_after();
+            {
+                const float eg = G.erel[row] * G.start[sp];
+                __nv_bfloat16* dst = o + ((size_t)(tok0 + n * kT + row) * H + h) * kD + j0 + HB * hb;
+#pragma unroll
+                for (int g = 0; g < HB / 16; ++g) {
+                    float a[16], b[16];
+                    tmem_ld16(tPV + lanes + HB * hb + 16 * g, a);
+                    tmem_ld16(tQS + lanes + HB * hb + 16 * g, b);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) a[e] = fmaf(eg, b[e], a[e]);
+                    if (row < live) {
+                        reinterpret_cast<uint4*>(dst + 16 * g)[0] = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]),
+                                                                               pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+                        reinterpret_cast<uint4*>(dst + 16 * g)[1] =
+                            make_uint4(pack_bf16(a[8], a[9]), pack_bf16(a[10], a[11]), pack_bf16(a[12], a[13]),
+                                       pack_bf16(a[14], a[15]));
+                    }
+                }
+            }
+            // S <- e^{g_C} S + U
+            if (!wait_or_abort(&bars[kUDone], par, ab)) break;
+            tc_fence_after();
+            const float gam = G.gam;
+#pragma unroll
+            for (int g = 0; g < HB / 16; ++g) {
+                float a[16];
+                tmem_ld16(tU + lanes + HB * hb + 16 * g, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
+            }
+            mbar_arrive(&bars[kGEmpty + (n & 1)]);
+            if (n + 1 < nch) publish();
+        }
+        if (final_state && flags[1] == 0u && last_segment(segs, seq, idx)) {
+            float* dst = final_state + (((size_t)seq * H + h) * kD + row) * kD + j0 + HB * hb;
+#pragma unroll
+            for (int j = 0; j < HB; j += 4)
+                *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tbase, 512);
+}
+
+// ---- states ---------------------------------------------------------------------------
+// The state chain alone, S <- e^{g_C} S + (w A)^T B over the segment's chunks:
+//   forward A = K, B = V, w = e^{g_C - g};  REV (chunks from last to first) A = Q, B = d_o,
+//   w = e^{g}, S the gradient of the chunk's end state.
+// With seg_end: from zero, the segment's own sum and whole decay (of every segment that
+// another one follows in the chain).  With store: from start, the bf16 copy of S ahead of
+// each chunk as a 32 KB image [64-column block][row][128 bytes, swizzled].
+// The weighting of chunk n + 1 runs while the products of chunk n do: low parts and
+// accumulators are double buffered.
+constexpr int kStSlots = 4;
+constexpr uint32_t kStLo = kStSlots * kTile;
+constexpr uint32_t kStGates = kStLo + 2 * kTile;
+constexpr uint32_t kStBars = kStGates + 2 * sizeof(Gates);
+constexpr uint32_t kStSmem = kStBars + 256;
+static_assert(kStSmem <= 232448, "shared memory per block");
+enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSGFull = kSUDone + 2,
+             kSGEmpty = kSGFull + 2, kSDrain = kSGEmpty + 2, kStBarsN };
+
+template <bool REV>
+__global__ void __launch_bounds__(kWalkThreads, 1)
+lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, LinDecay dec, ChunkMap segs,
+          int H, const float* __restrict__ start, const float* __restrict__ seg_start, float* __restrict__ seg_end,
+          float* __restrict__ seg_gam, int* __restrict__ err) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0 && blockIdx.x == 0 && seg_start == nullptr) *err = 0;
+    if (smem_u32(sm) & 1023u) {
+        if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
+        return;
+    }
+    const int h = (int)(blockIdx.x % H), seg = (int)(blockIdx.x / H);
+    int seq, tok0, len, idx;
+    segs.locate(seg, seq, tok0, len, idx);
+    if (seg_end && (REV ? idx == 0 : last_segment(segs, seq, idx))) return;
+    const int nch = (len + kT - 1) / kT;
+    if (tid == 0) {
+        for (int i = 0; i < kStBarsN; ++i)
+            mbar_init(&bars[i], (i >= kSWReady && i < kSWReady + 2) || (i >= kSGEmpty && i < kSGEmpty + 2) ? kCompute : 1);
+        mbar_init_fence();
+        flags[1] = 0u;
+    }
+    if (warp == 8) {
+        tmem_alloc(&flags[0], 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = flags[0];
+    const Abort ab{&flags[1], err};
+    auto chunk = [&](int n) { return REV ? nch - 1 - n : n; };
+    auto slot = [&](int i) { return sm + (uint32_t)(i % kStSlots) * kTile; };   // tile i: A 2 n, B 2 n + 1
+    auto full = [&](int i) { return &bars[kSFull + i % kStSlots]; };
+    auto full_par = [&](int i) { return (uint32_t)(i / kStSlots) & 1u; };
+    Gates* gates = reinterpret_cast<Gates*>(sm + kStGates);
+
+    if (warp == 9) {
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            for (; i < 2 * nch; ++i) {
+                if (i >= kStSlots && !(ok = wait_or_abort(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab))) break;
+                const int t = tok0 + chunk(i / 2) * kT;
+                mbar_arrive_expect_tx(full(i), kTile);
+                tma_box(slot(i), i & 1 ? &mb : &ma, 0, h, t, full(i));
+                tma_box(slot(i) + kBlock, i & 1 ? &mb : &ma, 64, h, t, full(i));
+            }
+            if (!ok)
+                for (int j = max(0, i - kStSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
+        }
+    } else if (warp == 10) {
+        float x[4], y[4];
+        double whole = 0.0;   // log decay of the segment
+        load_gates(x, dec, (long long)tok0 + chunk(0) * kT, min(kT, len - chunk(0) * kT), H, h, lane);
+        for (int n = 0; n < nch; ++n) {
+            if (n + 1 < nch)
+                load_gates(y, dec, (long long)tok0 + chunk(n + 1) * kT, min(kT, len - chunk(n + 1) * kT), H, h, lane);
+            if (n >= 2 && !wait_or_abort(&bars[kSGEmpty + (n & 1)], ((uint32_t)(n >> 1) & 1u) ^ 1u, ab)) break;
+            make_gates(&gates[n & 1], x, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kSGFull + (n & 1)]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                whole += (double)x[u];
+                x[u] = y[u];
+            }
+        }
+        if (seg_end) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
+            if (lane == 0) seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            constexpr uint32_t iU = idesc_amn_bmn(128, 128);
+            bool ok = true;
+            for (int n = 0; n < nch; ++n) {
+                if (!(ok = wait_or_abort(&bars[kSWReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) &&
+                           wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab)))
+                    break;
+                tc_fence_after();
+                const uint32_t a = smem_u32(slot(2 * n)), b = smem_u32(slot(2 * n + 1));
+                const uint32_t lo = smem_u32(sm + kStLo) + (n & 1) * kTile, d = tbase + 128 * (n & 1);
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s)
+                    mma_bf16(d, mn_desc_k(a, kT, s), mn_desc_k(b, kT, s), iU, s > 0);
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s)
+                    mma_bf16(d, mn_desc_k(lo, kT, s), mn_desc_k(b, kT, s), iU, 1u);
+                mma_commit(&bars[kSUDone + (n & 1)]);
+                mma_commit(&bars[kSEmpty + (2 * n) % kStSlots]);
+                mma_commit(&bars[kSEmpty + (2 * n + 1) % kStSlots]);
+            }
+            if (!ok) {
+                mma_commit(&bars[kSDrain]);
+                mbar_wait(&bars[kSDrain], 0u);
+            }
+        }
+    } else {
+        const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
+        const uint32_t lanes = (uint32_t)(32 * sp) << 16;
+        float s[64];
+        {
+            const float* src = seg_end ? nullptr
+                               : seg_start ? seg_start + ((size_t)seg * H + h) * kD * kD
+                               : start ? start + ((size_t)seq * H + h) * kD * kD
+                                       : nullptr;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 x = src ? *reinterpret_cast<const float4*>(src + (size_t)row * kD + 64 * hb + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+            }
+        }
+        float gam = 0.f;
+        bool ok = true;
+        for (int n = 0; n <= nch; ++n) {
+            float next_gam = 0.f;
+            if (n < nch) {
+                const Gates& G = gates[n & 1];
+                const int live = min(kT, len - chunk(n) * kT);
+                if (!(ok = wait_or_abort(&bars[kSGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) &&
+                           wait_or_abort(full(2 * n), full_par(2 * n), ab)))
+                    break;
+                if (live < kT) {
+                    if (!(ok = wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab))) break;
+                    zero_rows(slot(2 * n + 1), 2, live, tid);
+                }
+                const int r = tid & 127;
+                const float w = REV ? G.erel[r] * G.start[r >> 5] : G.col[r] * G.end[r >> 5];
+                scale_split_row(slot(2 * n), sm + kStLo + (n & 1) * kTile, r, tid >> 7, w, r < live);
+                next_gam = G.gam;
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(&bars[kSWReady + (n & 1)]);
+                mbar_arrive(&bars[kSGEmpty + (n & 1)]);
+            }
+            if (n > 0) {
+                const int m = n - 1;
+                if (!(ok = wait_or_abort(&bars[kSUDone + (m & 1)], (uint32_t)(m >> 1) & 1u, ab))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float a[16];
+                    tmem_ld16(tbase + 128 * (m & 1) + lanes + 64 * hb + 16 * g, a);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
+                }
+            }
+            gam = next_gam;
+        }
+        if (ok && seg_end) {
+            float* dst = seg_end + (((size_t)seg * H + h) * kD + row) * kD + 64 * hb;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+                *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tbase, 256);
+}
+
+// start state of every segment from the segments' own sums, in place (as the chunk chain
+// of the CUDA-core path, with segments for chunks)
+template <bool REV>
+__global__ void __launch_bounds__(256) seg_chain(float* __restrict__ X, const float* __restrict__ gam,
+                                                 const float* __restrict__ start, SeqMap smap, int H) {
+    const SeqInfo sq = smap.get((int)blockIdx.x / H);
+    const int h = (int)blockIdx.x % H, e = (int)blockIdx.y * 256 + threadIdx.x;
+    const int n = (sq.len + smap.C - 1) / smap.C;
+    constexpr int E4 = kD * kD / 4;
+    float4* x4 = reinterpret_cast<float4*>(X);
+    float4 s = start ? reinterpret_cast<const float4*>(start)[((size_t)sq.seq * H + h) * E4 + e]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+        const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i : i)) * H + h;
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        float g = 0.f;
+        if (i + 1 < n) {   // nothing follows the last segment: its own sum was not formed
+            u = x4[unit * E4 + e];
+            g = gam[unit];
+        }
+        x4[unit * E4 + e] = s;
+        s.x = fmaf(g, s.x, u.x);
+        s.y = fmaf(g, s.y, u.y);
+        s.z = fmaf(g, s.z, u.z);
+        s.w = fmaf(g, s.w, u.w);
+    }
+}
+
+// states of sequences without tokens: the last `n_empty` of the longest-first order, or all
+__global__ void __launch_bounds__(256) empty_states(const float* __restrict__ start, float* __restrict__ end,
+                                                    SeqMap smap, int first, int H) {
+    const SeqInfo sq = smap.get(first + (int)blockIdx.x / H);
+    const size_t at = ((size_t)sq.seq * H + blockIdx.x % H) * (kD * kD / 4) + blockIdx.y * 256 + threadIdx.x;
+    reinterpret_cast<float4*>(end)[at] = start ? reinterpret_cast<const float4*>(start)[at]
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, uint32_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace
+}  // namespace lintc
+
+using namespace lintc;
+
+cudaError_t launch_lin_empty_states(const float* start, float* end, const SeqMap& smap, int first, int n, int H,
+                                    cudaStream_t s) {
+    if (n <= 0 || end == nullptr || end == start) return cudaSuccess;
+    empty_states<<<dim3((unsigned)n * H, kD * kD / 1024), 256, 0, s>>>(start, end, smap, first, H);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init_state,
+                              void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
+                              int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
+                              float* seg_gam, int* err, cudaStream_t s) {
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H))
+        return cudaErrorNotSupported;
+    cudaError_t e;
+    if (split) {
+        if ((e = allow_smem(lin_state<false>, kStSmem)) != cudaSuccess) return e;
+        lin_state<false><<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, dec, segs, H, nullptr, nullptr,
+                                                                            seg_state, seg_gam, err);
+        seg_chain<false><<<dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s>>>(seg_state, seg_gam, init_state,
+                                                                                   smap, H);
+    }
+    auto kern = BV == 128 ? lin_walk<128> : lin_walk<64>;
+    if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
+    kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
+        mq, mk, mv, dec, segs, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

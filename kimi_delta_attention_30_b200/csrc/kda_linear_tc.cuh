@@ -1,0 +1,193 @@
+// Building blocks shared by the tensor-core kernels of linear attention with one decay a
+// head: tensor maps over [tokens, H, 128] arrays, chunk gates, waits that can be given up.
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_linear.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace lintc {
+
+using namespace tc;
+
+constexpr int kT = 128;               // tokens a chunk
+constexpr int kD = 128;               // key and value width
+constexpr uint32_t kTile = 32768;     // a 128 x 128 bf16 tile: two 64-column blocks of 128 rows x 128 bytes
+constexpr uint32_t kBlock = 16384;
+
+// ---- tensor maps --------------------------------------------------------------------
+// A bf16 [tokens, H, 128] array as (channel, head, token), boxes of 64 channels x 1 head x
+// 128 tokens in the 128-byte swizzle that the matrix descriptors name; false if the driver
+// does not offer the call or rejects the array.
+bool make_map(CUtensorMap* map, const void* base, long long tokens, int H);
+
+// Box (channels x0 .. x0 + 63, head h, tokens t0 .. t0 + 127) -> 16 KB of shared memory.
+// Rows past the array's end read as zero.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x0, int h, int t0, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x0), "r"(h), "r"(t0), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds bf16 pairs, one row a lane.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__host__ __device__ constexpr uint32_t idesc_amn_bmn(int M, int N) {
+    return idesc_bf16_f32(M, N) | (1u << 15) | (1u << 16);
+}
+
+// 16 words (bf16 pairs) a lane into tensor memory
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* w) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+    tmem_st16(taddr, v);
+}
+
+// ---- waits ----------------------------------------------------------------------------
+// Every wait ends: after two seconds, or as soon as another role has given up, it returns
+// false and the caller leaves its loop.
+struct Abort {
+    uint32_t* flag;   // shared memory
+    int* err;         // the workspace's error word
+};
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Abort& A) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0u) {
+            if (*reinterpret_cast<volatile uint32_t*>(A.flag)) return false;
+            if (globaltimer_ns() - t0 > 2000000000ull) {
+                atomicCAS(A.err, 0, (int)KDA_ERR_TIMEOUT);
+                *reinterpret_cast<volatile uint32_t*>(A.flag) = 1u;
+                return false;
+            }
+        }
+    }
+}
+
+// ---- a chunk's decays -------------------------------------------------------------------
+// The 128 tokens are four blocks of 32.  With g the inclusive sum of log decays from the
+// chunk's start, every decay the kernels need is a product of numbers that are at most 1:
+//   e^{g_i}       = start[R] erel[i]               R the block of i
+//   e^{g_C - g_j} = end[B] col[j]                  B the block of j
+//   e^{g_i - g_j} = erel[i] fac[R][B] col[j]       B < R
+// with erel[i] = e^{g_i - (g before block R)}, col[j] = e^{(g at the end of block B) - g_j}.
+// Inside a block e^{g_i - g_j} = 2^{rel2[i] - rel2[j]}.  Sums run in fp64, so that resets
+// (-100 a token) do not blur the decays behind them.
+struct Gates {
+    float rel2[kT];      // log2 e (g_i - g before the block)
+    float erel[kT];
+    float col[kT];
+    float fac[4][4];
+    float start[4];
+    float end[4];
+    float gam;           // e^{g_C}
+    float pad[7];
+};
+static_assert(sizeof(Gates) == 1664, "gate buffer");
+
+// Four log decays a lane (tokens 4 lane + u), zero past `len`.
+template <typename Tin = __nv_bfloat16>
+__device__ __forceinline__ void load_gates(float (&x)[4], const LinDecay& dec, long long tok0, int len, int H, int h,
+                                           int lane) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int t = 4 * lane + u;
+        x[u] = t < len ? lin_log_decay<Tin>(dec, (size_t)(tok0 + t), H, h) : 0.f;
+    }
+}
+
+// One warp turns them into the chunk's gates.
+__device__ __forceinline__ void make_gates(Gates* G, const float (&x)[4], int lane) {
+    constexpr double kL2e = 1.4426950408889634074;
+    double p[4];
+    p[0] = (double)x[0] * kL2e;
+#pragma unroll
+    for (int u = 1; u < 4; ++u) p[u] = p[u - 1] + (double)x[u] * kL2e;
+    double incl = p[3];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    double before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0.0;
+    const int blk = lane >> 3;
+    double s = __shfl_sync(0xffffffffu, incl, (8 * blk + 31) & 31);   // end of the block before
+    if (blk == 0) s = 0.0;
+    const double e = __shfl_sync(0xffffffffu, incl, 8 * blk + 7);
+    const double all = __shfl_sync(0xffffffffu, incl, 31);
+    float4 r2, er, co;
+    float* r2p = &r2.x;
+    float* erp = &er.x;
+    float* cop = &co.x;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const double g = before + p[u];
+        r2p[u] = (float)(g - s);
+        erp[u] = ex2_approx((float)(g - s));
+        cop[u] = ex2_approx((float)(e - g));
+    }
+    reinterpret_cast<float4*>(G->rel2)[lane] = r2;
+    reinterpret_cast<float4*>(G->erel)[lane] = er;
+    reinterpret_cast<float4*>(G->col)[lane] = co;
+    const int R = (lane >> 2) & 3, B = lane & 3;
+    double rs = __shfl_sync(0xffffffffu, incl, (8 * R + 31) & 31);
+    const double be = __shfl_sync(0xffffffffu, incl, 8 * B + 7);
+    if (R == 0) rs = 0.0;
+    if (lane < 16) G->fac[R][B] = B < R ? ex2_approx((float)(rs - be)) : 0.f;
+    if (lane < 16 && B == 0) G->start[R] = ex2_approx((float)rs);
+    if (lane < 4) G->end[B] = ex2_approx((float)(all - be));
+    if (lane == 0) G->gam = ex2_approx((float)all);
+}
+
+// ---- the weighted rows as a bf16 pair ------------------------------------------------------
+// Thread (row, block) of 256 scales its 64 channels of the tile's row by w: the high parts
+// replace the row, the low parts go to `lo` (same layout).  hi + lo carries 16 bits.
+__device__ __forceinline__ void scale_split_row(uint8_t* tile, uint8_t* lo, int row, int blk, float w, bool live) {
+    uint8_t* src = tile + blk * kBlock + row * 128;
+    uint8_t* dst = lo + blk * kBlock + row * 128;
+    const float2 w2 = make_float2(w, w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t off = (uint32_t)((c ^ (row & 7)) << 4);
+        uint4 x = *reinterpret_cast<const uint4*>(src + off), y = make_uint4(0u, 0u, 0u, 0u);
+        if (live) {
+            uint32_t* xp = &x.x;
+            uint32_t* yp = &y.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = mul2(unpack_bf16x2(xp[i]), w2);
+                split2(v.x, v.y, xp[i], yp[i]);
+            }
+        } else {
+            x = y;   // rows past the chunk's end weigh nothing, whatever they hold
+        }
+        *reinterpret_cast<uint4*>(src + off) = x;
+        *reinterpret_cast<uint4*>(dst + off) = y;
+    }
+}
+
+// Rows >= len of a tile of `blocks` 64-column blocks set to zero by 256 threads.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int blocks, int len, int tid) {
+    for (int u = tid; u < blocks * (kT - len) * 8; u += 256) {
+        const int c = u & 7, r = len + (u >> 3) % (kT - len), b = (u >> 3) / (kT - len);
+        *reinterpret_cast<uint4*>(tile + b * kBlock + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+}  // namespace lintc
+}  // namespace kda

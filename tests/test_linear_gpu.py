@@ -13,7 +13,11 @@ off by at most u A.
   the fp32 part.  States see the weighted keys or queries as a bf16 pair (2^-16) and
   fp32 sums (2^-17 a chunk): u = 2^-15.
 * bf16 results are rounded once more: 2^-8 of the value.
-The same results are also held to the framework's parity bound on max |d| / rms.
+The same results are also held to the framework's parity bound on max |d| / rms.  For the
+tensor cores' bf16 results that bound gets 2^-8 max |value| / rms on top: a result that
+consists of one term (the first token behind a reset: o = (q . k) v) carries that term's
+one rounded operand whole, 2^-8 of the value, and the largest values are 5 to 6 rms here,
+2.1e-2 by themselves (measured 2.12e-2).
 """
 import numpy as np
 import pytest
@@ -80,6 +84,13 @@ def close(label, got, ref, bound):
     assert worst <= 1.0, f"{label}: {worst:.3f} of the bound"
 
 
+def parity_bound(dt, dk, dv, ref, name=""):
+    if not _tc(dt, dk, dv):
+        return TOL[dt]
+    roundings = 2 if name == "dlog_alpha" else 1
+    return TOL[dt] + roundings * 2.0 ** -8 * float(np.abs(ref).max() / np.sqrt(np.mean(ref ** 2)))
+
+
 def check_fwd(x, dt, dk, dv, o, fs, label):
     q, k, v, la, s0, _, _ = ref_args(x)
     o_ref, fs_ref = ol.forward(q, k, v, la, x["ss"], s0)
@@ -88,7 +99,8 @@ def check_fwd(x, dt, dk, dv, o, fs, label):
     u = F32U + (2.0 ** -8 if _tc(dt, dk, dv) else 0.0)
     if o_ref.size:
         close(label + " o", o, o_ref, u * o_abs + (2.0 ** -8 * np.abs(o_ref) if dt == "bf16" else 0.0))
-        assert parity(label + " o", to_f64(o).reshape(o_ref.shape), o_ref, TOL[dt], stored_as=dt) <= TOL[dt]
+        tol = parity_bound(dt, dk, dv, o_ref)
+        assert parity(label + " o", to_f64(o).reshape(o_ref.shape), o_ref, tol, stored_as=dt) <= tol
     if fs is not None:
         close(label + " state", fs, fs_ref, F32U * fs_abs)
         assert parity(label + " state", to_f64(fs), fs_ref, TOL["f32"]) <= TOL["f32"]
@@ -110,7 +122,7 @@ def check_bwd(x, dt, dk, dv, grads, label):
         if got.dtype == torch.bfloat16:
             b = b + 2.0 ** -8 * np.abs(ref[name])
         close(f"{label} {name}", got, ref[name], b)
-        tol = TOL["f32"] if name == "d_init_state" else TOL[dt]
+        tol = TOL["f32"] if name == "d_init_state" else parity_bound(dt, dk, dv, ref[name], name)
         assert parity(f"{label} {name}", to_f64(got).reshape(ref[name].shape), ref[name], tol,
                       stored_as="bf16" if got.dtype == torch.bfloat16 else None) <= tol
 
