@@ -12,15 +12,19 @@
 // kind that o itself takes when it is stored; the state sees 16-bit operands, since its
 // errors would be carried from chunk to chunk and it is returned in fp32.
 //
-// Roles: 8 warps do the elementwise work (warp w: rows 32 (w % 4) + lane, column half w / 4),
-// one thread issues the products, one the loads, one warp forms the decays.  Products of
-// chunk n + 1 that need no state (Q K^T) are issued before chunk n's state is finished, and
-// the tiles of chunk n + 1 are loaded meanwhile: five 32 KB slots hold Q, K, V in turn (Q's
-// slot is free first and takes the next V).  The low parts of the weighted keys and the
-// state's copy share one buffer, since the product that reads one ends before the other is
-// written.  Rows past a sequence's end are loaded with the box (they belong to the next
-// sequence); K's are weighted with zero, V's are cleared, Q's only reach rows of o that are
-// not stored.
+// Roles, each with its own barriers, so that they work on different chunks at once: 8 warps
+// form o and keep the state (warp w: rows 32 (w % 4) + lane, column half w / 4), 8 turn
+// scores into P and weight the keys, one issues the products, one the loads, one forms the
+// decays.  The state itself is off the critical path: U needs no state, so the chain from
+// chunk to chunk is one multiply-add and the copy for the next queries.  Products are issued
+// in the order P V, Q S, Q K^T of the next chunk, U: the first three run while the keys are
+// weighted (which waits for the last U to release the low parts' buffer), P of the next
+// chunk is formed while U runs.  Five 32 KB slots hold Q, K, V in turn (Q's slot is free
+// first and takes the next V).  A 128 x 128 x 16 product reads 8 KB in the 64 cycles it
+// takes, which is all that shared memory gives, so products, the loads' writes and the
+// weighting share 128 bytes a cycle.
+// Rows past a sequence's end are loaded with the box (they belong to the next sequence); K's
+// are weighted with zero, V's are cleared, Q's only reach rows of o that are not stored.
 #include <algorithm>
 
 #include "kda_linear_tc.cuh"
@@ -51,8 +55,7 @@ bool make_map(CUtensorMap* map, const void* base, long long tokens, int H) {
 
 namespace {
 
-constexpr int kCompute = 256;              // threads of the elementwise warps
-constexpr int kWalkThreads = kCompute + 96;
+constexpr int kWalkThreads = 640;   // warps 0-7 state (and o), 8-15 weights (and P), 16 products, 17 loads, 18 decays
 
 // whether segment `idx` of sequence `seq` is its last
 __device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int idx) {
@@ -62,13 +65,14 @@ __device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int 
 
 // ---- outputs ------------------------------------------------------------------------
 constexpr int kSlots = 5;
-constexpr uint32_t kOffSK = kSlots * kTile;            // state copy, or low parts of the weighted keys
-constexpr uint32_t kOffGates = kOffSK + kTile;
+constexpr uint32_t kOffLo = kSlots * kTile;            // low parts of the weighted keys
+constexpr uint32_t kOffS = kOffLo + kTile;             // the state's copy
+constexpr uint32_t kOffGates = kOffS + kTile;
 constexpr uint32_t kOffBars = kOffGates + 2 * sizeof(Gates);
 constexpr uint32_t kWalkSmem = kOffBars + 256;
 static_assert(kWalkSmem <= 232448, "shared memory per block");
 
-enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady, kQsDone, kKReady, kODone, kUDone, kSReady,
+enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady, kQsDone, kKReady, kODone, kORead, kUDone, kSReady,
                kGFull, kGEmpty = kGFull + 2, kDrain = kGEmpty + 2, kWalkBars };
 
 template <int BV>
@@ -81,7 +85,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kWalkBars);   // tensor-memory base, abort
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0 && blockIdx.x == 0 && seg_start == nullptr) *err = 0;   // first kernel of the call
     if (smem_u32(sm) & 1023u) {
         if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
@@ -94,14 +98,13 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const int nch = (len + kT - 1) / kT;
 
     if (tid == 0) {
-        for (int i = 0; i < kWalkBars; ++i)
-            mbar_init(&bars[i], i == kPReady || i == kKReady || i == kSReady || i == kGEmpty || i == kGEmpty + 1
-                                    ? kCompute
-                                    : 1);
+        for (int i = 0; i < kWalkBars; ++i)   // one arrival a warp
+            mbar_init(&bars[i], i == kPReady || i == kKReady || i == kSReady || i == kORead ? 8
+                                : i == kGEmpty || i == kGEmpty + 1 ? 16 : 1);
         mbar_init_fence();
         flags[1] = 0u;
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(&flags[0], 512);
         tmem_relinquish();
     }
@@ -115,101 +118,16 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     auto full = [&](int i) { return &bars[kFull + i % kSlots]; };
     auto full_par = [&](int i) { return (uint32_t)(i / kSlots) & 1u; };
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
-    uint8_t* sk = sm + kOffSK;
+    auto gates_full = [&](int n) { return wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
+    auto scores_done = [&](int n) { return wait_or_abort(&bars[kScores], (uint32_t)n & 1u, ab); };
+    const int sp = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * sp) << 16;
 
-    if (warp == 9) {
-        if (lane == 0) {   // loads
-            int i = 0;
-            bool ok = true;
-            for (; ok && i < 3 * nch; ++i) {
-                if (i >= kSlots) ok = wait_or_abort(&bars[kEmpty + i % kSlots], (full_par(i) ^ 1u), ab);
-                if (!ok) break;
-                const int t = tok0 + (i / 3) * kT, kind = i % 3;
-                const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
-                uint8_t* dst = slot(i);
-                if (kind < 2 || BV == 128) {
-                    mbar_arrive_expect_tx(full(i), kTile);
-                    tma_box(dst, m, 0, h, t, full(i));
-                    tma_box(dst + kBlock, m, 64, h, t, full(i));
-                } else {
-                    mbar_arrive_expect_tx(full(i), kBlock);
-                    tma_box(dst, m, j0, h, t, full(i));
-                }
-            }
-            if (!ok)   // given up: the copies in flight land before the block ends
-                for (int j = max(0, i - kSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
-        }
-    } else if (warp == 10) {   // decays
-        float x[4], y[4];
-        load_gates(x, dec, tok0, min(kT, len), H, h, lane);
-        for (int n = 0; n < nch; ++n) {
-            if (n + 1 < nch) load_gates(y, dec, (long long)tok0 + (n + 1) * kT, min(kT, len - (n + 1) * kT), H, h, lane);
-            if (n >= 2 && !wait_or_abort(&bars[kGEmpty + (n & 1)], ((uint32_t)(n >> 1) & 1u) ^ 1u, ab)) break;
-            make_gates(&gates[n & 1], x, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kGFull + (n & 1)]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = y[u];
-        }
-    } else if (warp == 8) {
-        if (lane == 0) {   // products
-            constexpr uint32_t iS = idesc_bf16_f32(128, 128), iB = idesc_bf16_f32_bmn(128, BV),
-                               iU = idesc_amn_bmn(128, BV);
-            auto scores = [&](int n) {
-                if (!wait_or_abort(full(3 * n), full_par(3 * n), ab) ||
-                    !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
-                    return false;
-                const uint32_t a = smem_u32(slot(3 * n)), b = smem_u32(slot(3 * n + 1));
-#pragma unroll
-                for (int s = 0; s < kD / 16; ++s)
-                    mma_bf16(tA, sw128_desc_k(a, kT, s), sw128_desc_k(b, kT, s), iS, s > 0);
-                mma_commit(&bars[kScores]);
-                return true;
-            };
-            bool ok = nch > 0 && scores(0);
-            for (int n = 0; ok && n < nch; ++n) {
-                const uint32_t par = (uint32_t)n & 1u;
-                const uint32_t q = smem_u32(slot(3 * n)), k = smem_u32(slot(3 * n + 1)), v = smem_u32(slot(3 * n + 2));
-                // Q S
-                if (!(ok = wait_or_abort(&bars[kSReady], par, ab))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < kD / 16; ++s)
-                    mma_bf16(tQS, sw128_desc_k(q, kT, s), mn_desc_k(smem_u32(sk), kD, s), iB, s > 0);
-                mma_commit(&bars[kQsDone]);
-                mma_commit(&bars[kEmpty + (3 * n) % kSlots]);
-                // P V
-                if (!(ok = wait_or_abort(&bars[kPReady], par, ab) &&
-                           wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)))
-                    break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s)
-                    mma_bf16_ta(tPV, tA + (s < 4 ? 8 * s : 64 + 8 * (s - 4)), mn_desc_k(v, kT, s), iB, s > 0);
-                mma_commit(&bars[kODone]);
-                // weighted K^T V, high then low parts
-                if (!(ok = wait_or_abort(&bars[kKReady], par, ab))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s)
-                    mma_bf16(tU, mn_desc_k(k, kT, s), mn_desc_k(v, kT, s), iU, s > 0);
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s)
-                    mma_bf16(tU, mn_desc_k(smem_u32(sk), kT, s), mn_desc_k(v, kT, s), iU, 1u);
-                mma_commit(&bars[kUDone]);
-                mma_commit(&bars[kEmpty + (3 * n + 1) % kSlots]);
-                mma_commit(&bars[kEmpty + (3 * n + 2) % kSlots]);
-                // the next chunk's scores, once P has been read
-                if (n + 1 < nch) ok = wait_or_abort(&bars[kODone], par, ab) && scores(n + 1);
-            }
-            if (!ok) {   // given up: products in flight end before the tensor memory is freed
-                mma_commit(&bars[kDrain]);
-                mbar_wait(&bars[kDrain], 0u);
-            }
-        }
-    } else {
-        const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
-        const uint32_t lanes = (uint32_t)(32 * sp) << 16;
+    // 96 registers a thread at launch, 20 warps: 8 x 120 + 8 x 96 + 4 x 40 of 20 x 96
+    if (warp >= 16) fewer_registers<40>();
+    if (warp < 8) {   // ---- o, and the state
+        more_registers<120>();
+        const int hb = warp >> 2, row = 32 * sp + lane;
         float s[HB];   // state row `row`, columns j0 + HB hb + [0, HB)
         {
             const float* src = seg_start ? seg_start + ((size_t)seg * H + h) * kD * kD
@@ -227,107 +145,38 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             for (int j = 0; j < HB; j += 8) {
                 const uint4 w = make_uint4(pack_bf16(s[j], s[j + 1]), pack_bf16(s[j + 2], s[j + 3]),
                                            pack_bf16(s[j + 4], s[j + 5]), pack_bf16(s[j + 6], s[j + 7]));
-                *reinterpret_cast<uint4*>(sk + mn_chunk(row, HB * hb + j, kD)) = w;
+                *reinterpret_cast<uint4*>(sm + kOffS + mn_chunk(row, HB * hb + j, kD)) = w;
             }
             fence_async_smem();
             tc_fence_before();
-            mbar_arrive(&bars[kSReady]);
+            warp_arrive(&bars[kSReady], lane);
         };
         publish();
+        bool ok = true;
         for (int n = 0; n < nch; ++n) {
             const uint32_t par = (uint32_t)n & 1u;
-            const int live = min(kT, len - n * kT);
-            const Gates& G = gates[n & 1];
-            if (!wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab)) break;
-            if (live < kT) {
-                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
-                zero_rows(slot(3 * n + 2), BV / 64, live, tid);
-                fence_async_smem();
-            }
-            if (!wait_or_abort(&bars[kScores], par, ab)) break;
-            tc_fence_after();
-            {   // P: this thread's row, two blocks of 32 keys
-                const float er = G.erel[row], r2 = G.rel2[row];
-#pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                    const int B = 2 * hb + bb;
-                    uint32_t w[16];
-                    if (B > sp) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = 0u;
-                    } else {
-                        float a[2][16];
-                        tmem_ld16(tA + lanes + 32 * B, a[0]);
-                        tmem_ld16(tA + lanes + 32 * B + 16, a[1]);
-                        tmem_ld_wait();
-                        if (B < sp) {
-                            const float f = er * G.fac[sp][B];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 c = *reinterpret_cast<const float4*>(&G.col[32 * B + e]);
-                                float* x = &a[e >> 4][e & 15];
-                                w[e / 2] = pack_bf16(x[0] * (f * c.x), x[1] * (f * c.y));
-                                w[e / 2 + 1] = pack_bf16(x[2] * (f * c.z), x[3] * (f * c.w));
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 c = *reinterpret_cast<const float4*>(&G.rel2[32 * B + e]);
-                                float* x = &a[e >> 4][e & 15];
-                                const float y0 = e <= lane ? x[0] * ex2_approx(r2 - c.x) : 0.f;
-                                const float y1 = e + 1 <= lane ? x[1] * ex2_approx(r2 - c.y) : 0.f;
-                                const float y2 = e + 2 <= lane ? x[2] * ex2_approx(r2 - c.z) : 0.f;
-                                const float y3 = e + 3 <= lane ? x[3] * ex2_approx(r2 - c.w) : 0.f;
-                                w[e / 2] = pack_bf16(y0, y1);
-                                w[e / 2 + 1] = pack_bf16(y2, y3);
-                            }
-                        }
-                    }
-                    // over this warp's own columns of the scores, of which block 2 hb is read by now
-                    if (bb == 1) tmem_ld_wait();
-                    tmem_st16u(tA + lanes + 64 * hb + 16 * bb, w);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&bars[kPReady]);
-            }
-            // weighted keys: row tid % 128, channel block tid / 128
-            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) ||
-                !wait_or_abort(&bars[kQsDone], par, ab))
-                break;
-            {
-                const int r = tid & 127;
-                scale_split_row(slot(3 * n + 1), sk, r, tid >> 7, G.col[r] * G.end[r >> 5], r < live);
-                fence_async_smem();
-                mbar_arrive(&bars[kKReady]);
-            }
+            if (!(ok = gates_full(n))) break;
+            const float gam = gates[n & 1].gam, eg = ex2_approx(gates[n & 1].rel2[row]) * gates[n & 1].start[sp];
+            warp_arrive(&bars[kGEmpty + (n & 1)], lane);
             // o = P V + e^g (Q S)
-            if (!wait_or_abort(&bars[kODone], par, ab)) break;
+            if (!(ok = wait_or_abort(&bars[kODone], par, ab) && wait_or_abort(&bars[kQsDone], par, ab))) break;
             tc_fence_after();
-            {
-                const float eg = G.erel[row] * G.start[sp];
-                __nv_bfloat16* dst = o + ((size_t)(tok0 + n * kT + row) * H + h) * kD + j0 + HB * hb;
+            __nv_bfloat16* dst = o + ((size_t)(tok0 + n * kT + row) * H + h) * kD + j0 + HB * hb;
+#pragma unroll 1
+            for (int g = 0; g < HB / 16; ++g) {
+                float a[16], b[16];
+                tmem_ld16(tPV + lanes + HB * hb + 16 * g, a);
+                tmem_ld16(tQS + lanes + HB * hb + 16 * g, b);
+                tmem_ld_wait();
+                uint32_t w[8];
 #pragma unroll
-                for (int g = 0; g < HB / 16; ++g) {
-                    float a[16], b[16];
-                    tmem_ld16(tPV + lanes + HB * hb + 16 * g, a);
-                    tmem_ld16(tQS + lanes + HB * hb + 16 * g, b);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) a[e] = fmaf(eg, b[e], a[e]);
-                    if (row < live) {
-                        reinterpret_cast<uint4*>(dst + 16 * g)[0] = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]),
-                                                                               pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
-                        reinterpret_cast<uint4*>(dst + 16 * g)[1] =
-                            make_uint4(pack_bf16(a[8], a[9]), pack_bf16(a[10], a[11]), pack_bf16(a[12], a[13]),
-                                       pack_bf16(a[14], a[15]));
-                    }
-                }
+                for (int e = 0; e < 16; e += 2) w[e / 2] = pack_bf16(fmaf(eg, b[e], a[e]), fmaf(eg, b[e + 1], a[e + 1]));
+                if (row < len - n * kT) store32(dst + 16 * g, w);
             }
-            // S <- e^{g_C} S + U
-            if (!wait_or_abort(&bars[kUDone], par, ab)) break;
+            tc_fence_before();
+            warp_arrive(&bars[kORead], lane);
+            if (!(ok = wait_or_abort(&bars[kUDone], par, ab))) break;
             tc_fence_after();
-            const float gam = G.gam;
 #pragma unroll
             for (int g = 0; g < HB / 16; ++g) {
                 float a[16];
@@ -336,21 +185,168 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
             }
-            mbar_arrive(&bars[kGEmpty + (n & 1)]);
-            if (n + 1 < nch) publish();
+            if (n + 1 < nch) {
+                // Q S of this chunk was issued before its U, which is done
+                publish();
+            }
         }
-        if (final_state && flags[1] == 0u && last_segment(segs, seq, idx)) {
+        if (final_state && ok && last_segment(segs, seq, idx)) {
             float* dst = final_state + (((size_t)seq * H + h) * kD + row) * kD + j0 + HB * hb;
 #pragma unroll
             for (int j = 0; j < HB; j += 4)
                 *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        }
+    } else if (warp < 16) {   // ---- P, and the weighted keys
+        const int hb = (warp >> 2) & 1, row = 32 * sp + lane, r = tid & 127;
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t par = (uint32_t)n & 1u;
+            const int live = min(kT, len - n * kT);
+            if (!gates_full(n)) break;
+            if (live < kT) {
+                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
+                zero_rows(slot(3 * n + 2), BV / 64, live, tid - 256, 256);
+                fence_async_smem();
+            }
+            const Gates& G = gates[n & 1];
+            const float r2 = G.rel2[row], er = ex2_approx(r2), wk = G.col[r] * G.end[r >> 5];
+            if (!scores_done(n)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int bb = 0; bb < 2; ++bb) {   // 32 keys at a time; P's words go over scores already read
+                const int B = 2 * hb + bb;
+                uint32_t w[16];
+                if (B > sp) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = 0u;
+                } else {
+                    float a[2][16];
+                    tmem_ld16(tA + lanes + 32 * B, a[0]);
+                    tmem_ld16(tA + lanes + 32 * B + 16, a[1]);
+                    tmem_ld_wait();
+                    if (B < sp) {
+                        const float f = er * G.fac[sp][B];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(&G.col[32 * B + e]);
+                            float* x = &a[e >> 4][e & 15];
+                            w[e / 2] = pack_bf16(x[0] * (f * c.x), x[1] * (f * c.y));
+                            w[e / 2 + 1] = pack_bf16(x[2] * (f * c.z), x[3] * (f * c.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(&G.rel2[32 * B + e]);
+                            float* x = &a[e >> 4][e & 15];
+                            const float y0 = e <= lane ? x[0] * ex2_approx(r2 - c.x) : 0.f;
+                            const float y1 = e + 1 <= lane ? x[1] * ex2_approx(r2 - c.y) : 0.f;
+                            const float y2 = e + 2 <= lane ? x[2] * ex2_approx(r2 - c.z) : 0.f;
+                            const float y3 = e + 3 <= lane ? x[3] * ex2_approx(r2 - c.w) : 0.f;
+                            w[e / 2] = pack_bf16(y0, y1);
+                            w[e / 2 + 1] = pack_bf16(y2, y3);
+                        }
+                    }
+                }
+                tmem_st16u(tA + lanes + 64 * hb + 16 * bb, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&bars[kPReady], lane);
+            warp_arrive(&bars[kGEmpty + (n & 1)], lane);
+            // the scores have read the keys, the last U the low parts
+            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) ||
+                (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)))
+                break;
+            scale_split_row(slot(3 * n + 1), sm + kOffLo, r, hb, wk, r < live);
+            fence_async_smem();
+            warp_arrive(&bars[kKReady], lane);
+        }
+    } else if (warp == 16) {   // ---- products
+        constexpr uint32_t iS = idesc_bf16_f32(128, 128), iB = idesc_bf16_f32_bmn(128, BV), iU = idesc_amn_bmn(128, BV);
+        const uint32_t lead = elect_lane();
+        const uint32_t base = smem_u32(sm), lo = base + kOffLo, st = base + kOffS;
+        auto commit = [&](int bar) {
+            if (lead) mma_commit(&bars[bar]);
+        };
+        auto scores = [&](int n) {
+            if (!wait_or_abort(full(3 * n), full_par(3 * n), ab) || !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
+                return false;
+            product<false, false>(tA, sw128_desc(base + (3 * n) % kSlots * kTile),
+                                  sw128_desc(base + (3 * n + 1) % kSlots * kTile), iS, false, lead);
+            commit(kScores);
+            return true;
+        };
+        bool ok = scores(0);
+        for (int n = 0; ok && n < nch; ++n) {
+            const uint32_t par = (uint32_t)n & 1u;
+            const uint32_t q = base + (3 * n) % kSlots * kTile, k = base + (3 * n + 1) % kSlots * kTile,
+                           v = base + (3 * n + 2) % kSlots * kTile;
+            // P V
+            if (!(ok = wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab) && wait_or_abort(&bars[kPReady], par, ab) &&
+                       (n == 0 || wait_or_abort(&bars[kORead], par ^ 1u, ab))))
+                break;
+            tc_fence_after();
+            const uint64_t dv = mn_desc_k(v, kT, 0);
+            product_ta(tPV, tA, dv, iB, lead);
+            commit(kODone);
+            // Q S
+            if (!(ok = wait_or_abort(&bars[kSReady], par, ab))) break;
+            tc_fence_after();
+            product<false, true>(tQS, sw128_desc(q), mn_desc_k(st, kD, 0), iB, false, lead);
+            commit(kQsDone);
+            commit(kEmpty + (3 * n) % kSlots);
+            // the next chunk's scores, once P has been read
+            if (n + 1 < nch && !(ok = wait_or_abort(&bars[kODone], par, ab) && scores(n + 1))) break;
+            // weighted K^T V, high then low parts
+            if (!(ok = wait_or_abort(&bars[kKReady], par, ab))) break;
+            tc_fence_after();
+            product<true, true>(tU, mn_desc_k(k, kT, 0), dv, iU, false, lead);
+            product<true, true>(tU, mn_desc_k(lo, kT, 0), dv, iU, true, lead);
+            commit(kUDone);
+            commit(kEmpty + (3 * n + 1) % kSlots);
+            commit(kEmpty + (3 * n + 2) % kSlots);
+        }
+        if (!ok) {   // given up: products in flight end before the tensor memory is freed
+            commit(kDrain);
+            mbar_wait(&bars[kDrain], 0u);
+        }
+    } else if (warp == 17) {
+        if (lane == 0) {   // ---- loads
+            int i = 0;
+            bool ok = true;
+            for (; i < 3 * nch; ++i) {
+                if (i >= kSlots && !(ok = wait_or_abort(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
+                const int t = tok0 + (i / 3) * kT, kind = i % 3;
+                const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
+                uint8_t* dst = slot(i);
+                if (kind < 2 || BV == 128) {
+                    mbar_arrive_expect_tx(full(i), kTile);
+                    tma_box(dst, m, 0, h, t, full(i));
+                    tma_box(dst + kBlock, m, 64, h, t, full(i));
+                } else {
+                    mbar_arrive_expect_tx(full(i), kBlock);
+                    tma_box(dst, m, j0, h, t, full(i));
+                }
+            }
+            if (!ok)   // given up: the copies in flight land before the block ends
+                for (int j = max(0, i - kSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
+        }
+    } else if (warp == 18) {   // ---- decays
+        float x[4], y[4];
+        load_gates(x, dec, tok0, min(kT, len), H, h, lane);
+        for (int n = 0; n < nch; ++n) {
+            if (n + 1 < nch) load_gates(y, dec, (long long)tok0 + (n + 1) * kT, min(kT, len - (n + 1) * kT), H, h, lane);
+            if (n >= 2 && !wait_or_abort(&bars[kGEmpty + (n & 1)], ((uint32_t)(n >> 1) & 1u) ^ 1u, ab)) break;
+            make_gates(&gates[n & 1], x, lane);
+            warp_arrive(&bars[kGFull + (n & 1)], lane);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = y[u];
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tbase, 512);
+    if (warp == 16) tmem_dealloc(tbase, 512);
 }
 
 // ---- states ---------------------------------------------------------------------------
@@ -358,29 +354,26 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 //   forward A = K, B = V, w = e^{g_C - g};  REV (chunks from last to first) A = Q, B = d_o,
 //   w = e^{g}, S the gradient of the chunk's end state.
 // With seg_end: from zero, the segment's own sum and whole decay (of every segment that
-// another one follows in the chain).  With store: from start, the bf16 copy of S ahead of
-// each chunk as a 32 KB image [64-column block][row][128 bytes, swizzled].
-// The weighting of chunk n + 1 runs while the products of chunk n do: low parts and
-// accumulators are double buffered.
+// another one follows in the chain).  Warps 0-7 keep the state, 8-15 weight the rows; low
+// parts and accumulators are double buffered, so both and the products overlap.
 constexpr int kStSlots = 4;
 constexpr uint32_t kStLo = kStSlots * kTile;
 constexpr uint32_t kStGates = kStLo + 2 * kTile;
 constexpr uint32_t kStBars = kStGates + 2 * sizeof(Gates);
 constexpr uint32_t kStSmem = kStBars + 256;
 static_assert(kStSmem <= 232448, "shared memory per block");
-enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSGFull = kSUDone + 2,
-             kSGEmpty = kSGFull + 2, kSDrain = kSGEmpty + 2, kStBarsN };
+enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSURead = kSUDone + 2,
+             kSGFull = kSURead + 2, kSGEmpty = kSGFull + 2, kSDrain = kSGEmpty + 2, kStBarsN };
 
 template <bool REV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, LinDecay dec, ChunkMap segs,
-          int H, const float* __restrict__ start, const float* __restrict__ seg_start, float* __restrict__ seg_end,
-          float* __restrict__ seg_gam, int* __restrict__ err) {
+          int H, float* __restrict__ seg_end, float* __restrict__ seg_gam, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0 && blockIdx.x == 0 && seg_start == nullptr) *err = 0;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    if (tid == 0 && blockIdx.x == 0) *err = 0;   // first kernel of the call
     if (smem_u32(sm) & 1023u) {
         if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
         return;
@@ -388,15 +381,16 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
     const int h = (int)(blockIdx.x % H), seg = (int)(blockIdx.x / H);
     int seq, tok0, len, idx;
     segs.locate(seg, seq, tok0, len, idx);
-    if (seg_end && (REV ? idx == 0 : last_segment(segs, seq, idx))) return;
+    if (REV ? idx == 0 : last_segment(segs, seq, idx)) return;   // nothing follows it
     const int nch = (len + kT - 1) / kT;
     if (tid == 0) {
         for (int i = 0; i < kStBarsN; ++i)
-            mbar_init(&bars[i], (i >= kSWReady && i < kSWReady + 2) || (i >= kSGEmpty && i < kSGEmpty + 2) ? kCompute : 1);
+            mbar_init(&bars[i], i >= kSWReady && i < kSWReady + 2 ? 8 : i >= kSURead && i < kSURead + 2 ? 8
+                                : i >= kSGEmpty && i < kSGEmpty + 2 ? 16 : 1);
         mbar_init_fence();
         flags[1] = 0u;
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(&flags[0], 256);
         tmem_relinquish();
     }
@@ -409,10 +403,87 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
     auto slot = [&](int i) { return sm + (uint32_t)(i % kStSlots) * kTile; };   // tile i: A 2 n, B 2 n + 1
     auto full = [&](int i) { return &bars[kSFull + i % kStSlots]; };
     auto full_par = [&](int i) { return (uint32_t)(i / kStSlots) & 1u; };
+    auto half_par = [&](int n) { return (uint32_t)(n >> 1) & 1u; };   // of barriers kept for chunks of either parity
     Gates* gates = reinterpret_cast<Gates*>(sm + kStGates);
 
-    if (warp == 9) {
-        if (lane == 0) {
+    if (warp >= 16) fewer_registers<40>();
+    if (warp < 8) {   // ---- the state
+        const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
+        const uint32_t lanes = (uint32_t)(32 * sp) << 16;
+        float s[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] = 0.f;
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            if (!(ok = wait_or_abort(&bars[kSGFull + (n & 1)], half_par(n), ab))) break;
+            const float gam = gates[n & 1].gam;
+            warp_arrive(&bars[kSGEmpty + (n & 1)], lane);
+            if (!(ok = wait_or_abort(&bars[kSUDone + (n & 1)], half_par(n), ab))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float a[16];
+                tmem_ld16(tbase + 128 * (n & 1) + lanes + 64 * hb + 16 * g, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
+            }
+            tc_fence_before();
+            warp_arrive(&bars[kSURead + (n & 1)], lane);
+        }
+        if (ok) {
+            float* dst = seg_end + (((size_t)seg * H + h) * kD + row) * kD + 64 * hb;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+                *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        }
+    } else if (warp < 16) {   // ---- weighted rows
+        more_registers<120>();
+        const int r = tid & 127, blk = (tid - 256) >> 7;
+        for (int n = 0; n < nch; ++n) {
+            const int live = min(kT, len - chunk(n) * kT);
+            if (!wait_or_abort(&bars[kSGFull + (n & 1)], half_par(n), ab)) break;
+            const Gates& G = gates[n & 1];
+            const float w = REV ? ex2_approx(G.rel2[r]) * G.start[r >> 5] : G.col[r] * G.end[r >> 5];
+            warp_arrive(&bars[kSGEmpty + (n & 1)], lane);
+            if (!wait_or_abort(full(2 * n), full_par(2 * n), ab) ||
+                (n >= 2 && !wait_or_abort(&bars[kSUDone + (n & 1)], half_par(n) ^ 1u, ab)))   // low parts are free
+                break;
+            if (live < kT) {
+                if (!wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab)) break;
+                zero_rows(slot(2 * n + 1), 2, live, tid - 256, 256);
+            }
+            scale_split_row(slot(2 * n), sm + kStLo + (n & 1) * kTile, r, blk, w, r < live);
+            fence_async_smem();
+            warp_arrive(&bars[kSWReady + (n & 1)], lane);
+        }
+    } else if (warp == 16) {   // ---- products
+        constexpr uint32_t iU = idesc_amn_bmn(128, 128);
+        const uint32_t lead = elect_lane(), base = smem_u32(sm);
+        auto commit = [&](int bar) {
+            if (lead) mma_commit(&bars[bar]);
+        };
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            if (!(ok = wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab) &&
+                       wait_or_abort(&bars[kSWReady + (n & 1)], half_par(n), ab) &&
+                       (n < 2 || wait_or_abort(&bars[kSURead + (n & 1)], half_par(n) ^ 1u, ab))))
+                break;
+            tc_fence_after();
+            const uint64_t b = mn_desc_k(base + (2 * n + 1) % kStSlots * kTile, kT, 0);
+            const uint32_t d = tbase + 128 * (n & 1);
+            product<true, true>(d, mn_desc_k(base + (2 * n) % kStSlots * kTile, kT, 0), b, iU, false, lead);
+            product<true, true>(d, mn_desc_k(base + kStLo + (n & 1) * kTile, kT, 0), b, iU, true, lead);
+            commit(kSUDone + (n & 1));
+            commit(kSEmpty + (2 * n) % kStSlots);
+            commit(kSEmpty + (2 * n + 1) % kStSlots);
+        }
+        if (!ok) {
+            commit(kSDrain);
+            mbar_wait(&bars[kSDrain], 0u);
+        }
+    } else if (warp == 17) {
+        if (lane == 0) {   // ---- loads
             int i = 0;
             bool ok = true;
             for (; i < 2 * nch; ++i) {
@@ -425,120 +496,31 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
             if (!ok)
                 for (int j = max(0, i - kStSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {   // ---- decays
         float x[4], y[4];
         double whole = 0.0;   // log decay of the segment
         load_gates(x, dec, (long long)tok0 + chunk(0) * kT, min(kT, len - chunk(0) * kT), H, h, lane);
         for (int n = 0; n < nch; ++n) {
             if (n + 1 < nch)
                 load_gates(y, dec, (long long)tok0 + chunk(n + 1) * kT, min(kT, len - chunk(n + 1) * kT), H, h, lane);
-            if (n >= 2 && !wait_or_abort(&bars[kSGEmpty + (n & 1)], ((uint32_t)(n >> 1) & 1u) ^ 1u, ab)) break;
+            if (n >= 2 && !wait_or_abort(&bars[kSGEmpty + (n & 1)], half_par(n) ^ 1u, ab)) break;
             make_gates(&gates[n & 1], x, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kSGFull + (n & 1)]);
+            warp_arrive(&bars[kSGFull + (n & 1)], lane);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 whole += (double)x[u];
                 x[u] = y[u];
             }
         }
-        if (seg_end) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
-            if (lane == 0) seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
-        }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            constexpr uint32_t iU = idesc_amn_bmn(128, 128);
-            bool ok = true;
-            for (int n = 0; n < nch; ++n) {
-                if (!(ok = wait_or_abort(&bars[kSWReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) &&
-                           wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab)))
-                    break;
-                tc_fence_after();
-                const uint32_t a = smem_u32(slot(2 * n)), b = smem_u32(slot(2 * n + 1));
-                const uint32_t lo = smem_u32(sm + kStLo) + (n & 1) * kTile, d = tbase + 128 * (n & 1);
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s)
-                    mma_bf16(d, mn_desc_k(a, kT, s), mn_desc_k(b, kT, s), iU, s > 0);
-#pragma unroll
-                for (int s = 0; s < kT / 16; ++s)
-                    mma_bf16(d, mn_desc_k(lo, kT, s), mn_desc_k(b, kT, s), iU, 1u);
-                mma_commit(&bars[kSUDone + (n & 1)]);
-                mma_commit(&bars[kSEmpty + (2 * n) % kStSlots]);
-                mma_commit(&bars[kSEmpty + (2 * n + 1) % kStSlots]);
-            }
-            if (!ok) {
-                mma_commit(&bars[kSDrain]);
-                mbar_wait(&bars[kSDrain], 0u);
-            }
-        }
-    } else {
-        const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
-        const uint32_t lanes = (uint32_t)(32 * sp) << 16;
-        float s[64];
-        {
-            const float* src = seg_end ? nullptr
-                               : seg_start ? seg_start + ((size_t)seg * H + h) * kD * kD
-                               : start ? start + ((size_t)seq * H + h) * kD * kD
-                                       : nullptr;
-#pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 x = src ? *reinterpret_cast<const float4*>(src + (size_t)row * kD + 64 * hb + j)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
-            }
-        }
-        float gam = 0.f;
-        bool ok = true;
-        for (int n = 0; n <= nch; ++n) {
-            float next_gam = 0.f;
-            if (n < nch) {
-                const Gates& G = gates[n & 1];
-                const int live = min(kT, len - chunk(n) * kT);
-                if (!(ok = wait_or_abort(&bars[kSGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) &&
-                           wait_or_abort(full(2 * n), full_par(2 * n), ab)))
-                    break;
-                if (live < kT) {
-                    if (!(ok = wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab))) break;
-                    zero_rows(slot(2 * n + 1), 2, live, tid);
-                }
-                const int r = tid & 127;
-                const float w = REV ? G.erel[r] * G.start[r >> 5] : G.col[r] * G.end[r >> 5];
-                scale_split_row(slot(2 * n), sm + kStLo + (n & 1) * kTile, r, tid >> 7, w, r < live);
-                next_gam = G.gam;
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(&bars[kSWReady + (n & 1)]);
-                mbar_arrive(&bars[kSGEmpty + (n & 1)]);
-            }
-            if (n > 0) {
-                const int m = n - 1;
-                if (!(ok = wait_or_abort(&bars[kSUDone + (m & 1)], (uint32_t)(m >> 1) & 1u, ab))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float a[16];
-                    tmem_ld16(tbase + 128 * (m & 1) + lanes + 64 * hb + 16 * g, a);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
-                }
-            }
-            gam = next_gam;
-        }
-        if (ok && seg_end) {
-            float* dst = seg_end + (((size_t)seg * H + h) * kD + row) * kD + 64 * hb;
-#pragma unroll
-            for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-        }
+        for (int off = 16; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
+        if (lane == 0) seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tbase, 256);
+    if (warp == 16) tmem_dealloc(tbase, 256);
 }
 
 // start state of every segment from the segments' own sums, in place (as the chunk chain
@@ -553,19 +535,32 @@ __global__ void __launch_bounds__(256) seg_chain(float* __restrict__ X, const fl
     float4* x4 = reinterpret_cast<float4*>(X);
     float4 s = start ? reinterpret_cast<const float4*>(start)[((size_t)sq.seq * H + h) * E4 + e]
                      : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-        const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i : i)) * H + h;
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        float g = 0.f;
-        if (i + 1 < n) {   // nothing follows the last segment: its own sum was not formed
-            u = x4[unit * E4 + e];
-            g = gam[unit];
+    constexpr int kAhead = 8;   // loads of that many segments stand before the first is used
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        float4 u[kAhead];
+        float g[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            u[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            g[j] = 0.f;
+            if (i + 1 < n) {   // nothing follows the last segment: its own sum was not formed
+                const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i : i)) * H + h;
+                u[j] = x4[unit * E4 + e];
+                g[j] = gam[unit];
+            }
         }
-        x4[unit * E4 + e] = s;
-        s.x = fmaf(g, s.x, u.x);
-        s.y = fmaf(g, s.y, u.y);
-        s.z = fmaf(g, s.z, u.z);
-        s.w = fmaf(g, s.w, u.w);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i < n) {
+                x4[((size_t)(sq.chunk0 + (REV ? n - 1 - i : i)) * H + h) * E4 + e] = s;
+                s.x = fmaf(g[j], s.x, u[j].x);
+                s.y = fmaf(g[j], s.y, u[j].y);
+                s.z = fmaf(g[j], s.z, u[j].z);
+                s.w = fmaf(g[j], s.w, u[j].w);
+            }
+        }
     }
 }
 
@@ -605,8 +600,8 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     cudaError_t e;
     if (split) {
         if ((e = allow_smem(lin_state<false>, kStSmem)) != cudaSuccess) return e;
-        lin_state<false><<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, dec, segs, H, nullptr, nullptr,
-                                                                            seg_state, seg_gam, err);
+        lin_state<false><<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, dec, segs, H, seg_state, seg_gam,
+                                                                            err);
         seg_chain<false><<<dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s>>>(seg_state, seg_gam, init_state,
                                                                                    smap, H);
     }

@@ -33,18 +33,56 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A holds bf16 pairs, one row a lane.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+
+// Products are issued by a whole warp whose elected lane (`lead`) carries the instruction:
+// control and descriptors then stay uniform for the warp.  A step of a rolled loop takes its
+// 64 cycles that way; the same loop under a branch of one lane took 100.
+__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+// A in tensor memory: bf16 pairs, one row a lane.
+__device__ __forceinline__ void mma_lead_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
 }
 
 __host__ __device__ constexpr uint32_t idesc_amn_bmn(int M, int N) {
     return idesc_bf16_f32(M, N) | (1u << 15) | (1u << 16);
+}
+
+// One product over K = 128 as eight steps of 16.  Kept as loops: the roles of a block run
+// different code at once, and what they run once a chunk has to stay small enough for the
+// instruction caches (unrolled code cost five times its issue time in fetches).
+// Descriptor steps, in 16-byte units: a K-major tile moves 32 bytes a step inside a
+// 64-column block and 16 KB to the next block, an MN-major tile 16 rows of 128 bytes.
+__device__ __forceinline__ uint64_t k_step(uint64_t desc, int s) { return desc + (uint64_t)((s >> 2) * 1024 + (s & 3) * 2); }
+__device__ __forceinline__ uint64_t mn_step(uint64_t desc, int s) { return desc + (uint64_t)(s * 128); }
+
+template <bool AMN, bool BMN>
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+#pragma unroll 1
+    for (int s = 0; s < 8; ++s)
+        mma_lead(d, AMN ? mn_step(a, s) : k_step(a, s), BMN ? mn_step(b, s) : k_step(b, s), idesc, add || s > 0, lead);
+}
+// A in tensor memory, 128 bf16 a row: 32 words from a on and 32 from a + 64 on
+__device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint64_t b_mn, uint32_t idesc, uint32_t lead) {
+#pragma unroll 1
+    for (int s = 0; s < 8; ++s) mma_lead_ta(d, a + 8 * s + 32 * (s >> 2), mn_step(b_mn, s), idesc, s > 0, lead);
 }
 
 // 16 words (bf16 pairs) a lane into tensor memory
@@ -88,16 +126,15 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
 // Inside a block e^{g_i - g_j} = 2^{rel2[i] - rel2[j]}.  Sums run in fp64, so that resets
 // (-100 a token) do not blur the decays behind them.
 struct Gates {
-    float rel2[kT];      // log2 e (g_i - g before the block)
-    float erel[kT];
+    float rel2[kT];      // log2 e (g_i - g before the block); erel is 2 to that
     float col[kT];
     float fac[4][4];
     float start[4];
     float end[4];
     float gam;           // e^{g_C}
-    float pad[7];
+    float pad[3];
 };
-static_assert(sizeof(Gates) == 1664, "gate buffer");
+static_assert(sizeof(Gates) == 1136, "gate buffer");
 
 // Four log decays a lane (tokens 4 lane + u), zero past `len`.
 template <typename Tin = __nv_bfloat16>
@@ -130,19 +167,16 @@ __device__ __forceinline__ void make_gates(Gates* G, const float (&x)[4], int la
     if (blk == 0) s = 0.0;
     const double e = __shfl_sync(0xffffffffu, incl, 8 * blk + 7);
     const double all = __shfl_sync(0xffffffffu, incl, 31);
-    float4 r2, er, co;
+    float4 r2, co;
     float* r2p = &r2.x;
-    float* erp = &er.x;
     float* cop = &co.x;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const double g = before + p[u];
         r2p[u] = (float)(g - s);
-        erp[u] = ex2_approx((float)(g - s));
         cop[u] = ex2_approx((float)(e - g));
     }
     reinterpret_cast<float4*>(G->rel2)[lane] = r2;
-    reinterpret_cast<float4*>(G->erel)[lane] = er;
     reinterpret_cast<float4*>(G->col)[lane] = co;
     const int R = (lane >> 2) & 3, B = lane & 3;
     double rs = __shfl_sync(0xffffffffu, incl, (8 * R + 31) & 31);
@@ -154,14 +188,37 @@ __device__ __forceinline__ void make_gates(Gates* G, const float (&x)[4], int la
     if (lane == 0) G->gam = ex2_approx((float)all);
 }
 
+// Registers a thread of this warpgroup holds from here on (all four warps call it).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One arrival for a warp, after everything its lanes wrote or read before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// 32 bytes a lane: a whole sector of its row
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // ---- the weighted rows as a bf16 pair ------------------------------------------------------
-// Thread (row, block) of 256 scales its 64 channels of the tile's row by w: the high parts
+// One thread scales 64 channels (column block blk) of the tile's row by w: the high parts
 // replace the row, the low parts go to `lo` (same layout).  hi + lo carries 16 bits.
 __device__ __forceinline__ void scale_split_row(uint8_t* tile, uint8_t* lo, int row, int blk, float w, bool live) {
     uint8_t* src = tile + blk * kBlock + row * 128;
     uint8_t* dst = lo + blk * kBlock + row * 128;
     const float2 w2 = make_float2(w, w);
-#pragma unroll
+#pragma unroll 4
     for (int c = 0; c < 8; ++c) {
         const uint32_t off = (uint32_t)((c ^ (row & 7)) << 4);
         uint4 x = *reinterpret_cast<const uint4*>(src + off), y = make_uint4(0u, 0u, 0u, 0u);
@@ -181,9 +238,9 @@ __device__ __forceinline__ void scale_split_row(uint8_t* tile, uint8_t* lo, int 
     }
 }
 
-// Rows >= len of a tile of `blocks` 64-column blocks set to zero by 256 threads.
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int blocks, int len, int tid) {
-    for (int u = tid; u < blocks * (kT - len) * 8; u += 256) {
+// Rows >= len of a tile of `blocks` 64-column blocks set to zero by `threads` threads.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int blocks, int len, int tid, int threads) {
+    for (int u = tid; u < blocks * (kT - len) * 8; u += threads) {
         const int c = u & 7, r = len + (u >> 3) % (kT - len), b = (u >> 3) / (kT - len);
         *reinterpret_cast<uint4*>(tile + b * kBlock + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
