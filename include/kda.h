@@ -538,6 +538,10 @@ KDA_API kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void
                                         int dv, const void* d_o, const float* d_final_state, void* dq, void* dk_out,
                                         void* dv_out, void* dlog_alpha, float* d_init_state, void* workspace,
                                         size_t workspace_bytes, void* stream);
+/* Device-side status of the last kda_linear_chunk_bwd call that used `workspace`. */
+KDA_API kda_status kda_linear_chunk_bwd_device_status(const void* workspace, kda_dtype dtype,
+                                                      const int32_t* cu_seqlens_host, int n_seqs, int B, int T,
+                                                      int H, int dk, int dv, void* stream);
 
 /*
  * One token for each of N sequences, the states updated in place (as

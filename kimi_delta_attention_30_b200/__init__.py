@@ -118,6 +118,8 @@ def _declare(lib):
     lib.kda_linear_chunk_fwd.restype = c_int
     lib.kda_linear_chunk_fwd_device_status.argtypes = [vp, c_int, i32p, c_int] + [c_int] * 5 + [vp]
     lib.kda_linear_chunk_fwd_device_status.restype = c_int
+    lib.kda_linear_chunk_bwd_device_status.argtypes = lib.kda_linear_chunk_fwd_device_status.argtypes
+    lib.kda_linear_chunk_bwd_device_status.restype = c_int
     lib.kda_linear_chunk_bwd_workspace_size.argtypes = [c_int] * 6 + [i32p, c_int]
     lib.kda_linear_chunk_bwd_workspace_size.restype = c_size
     lib.kda_linear_chunk_bwd.argtypes = [vp] * 4 + [c_int, c_int, vp, i32p, c_int] + [c_int] * 5 + [vp] * 7 + \
@@ -169,7 +171,7 @@ def exported_symbols():
             "kda_chunk_fwd_noalloc_device_status", "kda_chunk_segment_map", "kda_compose_states",
             "kda_set_test_wait_limit", "kda_chunk_fwd_host_buffer_size", "kda_chunk_fwd_host",
             "kda_chunk_fwd_host_device_status", "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
-            "kda_linear_chunk_fwd_device_status",
+            "kda_linear_chunk_fwd_device_status", "kda_linear_chunk_bwd_device_status",
             "kda_linear_chunk_bwd_workspace_size", "kda_linear_chunk_bwd", "kda_linear_decode_step",
             "kda_qk_norm_rope", "kda_qk_norm_rope_bwd_workspace_size", "kda_qk_norm_rope_bwd"]
 
@@ -750,13 +752,15 @@ def linear_workspace_size(B, T, H, dk, dv, dtype, cu_seqlens=None, backward: boo
     return int(f(B, T, H, dk, dv, d, cu, n))
 
 
-def linear_device_status(workspace, dtype, B, T, H, dk, dv, cu_seqlens=None, stream=None) -> int:
-    """As :func:`device_status`, for the last :func:`linear_chunk_fwd` call that
-    used ``workspace`` with these sizes."""
+def linear_device_status(workspace, dtype, B, T, H, dk, dv, cu_seqlens=None, backward: bool = False,
+                         stream=None) -> int:
+    """As :func:`device_status`, for the last :func:`linear_chunk_fwd` (or
+    :func:`linear_chunk_bwd`) call that used ``workspace`` with these sizes."""
     cu, n, _keep = _cu_arg(cu_seqlens)
     d = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    f = lib().kda_linear_chunk_bwd_device_status if backward else lib().kda_linear_chunk_fwd_device_status
     with _launch_on(workspace.device, stream) as (s, _):
-        st = lib().kda_linear_chunk_fwd_device_status(_ptr(workspace), d, cu, n, B, T, H, dk, dv, _stream_handle(s))
+        st = f(_ptr(workspace), d, cu, n, B, T, H, dk, dv, _stream_handle(s))
     if st not in (0, KDA_ERR_TIMEOUT):
         raise KdaError(st, "linear device status")
     return int(st)

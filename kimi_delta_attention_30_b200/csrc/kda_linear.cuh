@@ -57,6 +57,18 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
                               void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
                               int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
                               float* seg_gam, int* err, cudaStream_t stream);
+// Backward, two parts.  States: the bf16 images of every chunk's start state and of its end
+// state's gradient, [chunk image, H] x 32 KB, and d_init (seg_state and seg_gam hold both
+// directions, one behind the other).  Gradients: everything else, from the images.
+cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, const void* d_o, LinDecay dec,
+                                 const float* init_state, const float* d_final, float* d_init, const ChunkMap& segs,
+                                 const SeqMap& smap, int n_segs, int n_seqs, bool split, long long tokens, int H,
+                                 float* seg_state, float* seg_gam, uint8_t* images, uint8_t* d_images, int* err,
+                                 cudaStream_t stream);
+cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, const void* d_o, LinDecay dec, void* dq,
+                               void* dk, void* dv, void* dla, const ChunkMap& chunks, int n_chunks, long long tokens,
+                               int H, const uint8_t* images, const uint8_t* d_images, int* err, cudaStream_t stream);
+
 // end = start (or 0) for n sequences without tokens from rank `first` of smap on
 cudaError_t launch_lin_empty_states(const float* start, float* end, const SeqMap& smap, int first, int n, int H,
                                     cudaStream_t stream);

@@ -38,15 +38,27 @@ constexpr int kSms = 148;
 // columns, half of them, and the state alone; and the launches that a split adds.
 constexpr double kWalk128 = 1.75, kWalk64 = 1.35, kStateOnly = 1.1, kSplitCost = 8.0;
 
+long long longest_of(const Plan& chunks) {   // chunks of the longest sequence
+    long long longest = 0;
+    if (chunks.varlen)
+        for (const SeqInfo& q : chunks.natural) longest = std::max<long long>(longest, (q.len + kLinTcChunk - 1) / kLinTcChunk);
+    else
+        longest = chunks.n_seqs ? chunks.n_chunks / chunks.n_seqs : 0;
+    return longest;
+}
+
+long long segments_of(const Plan& chunks, long long longest, long long len) {   // of len chunks each
+    if (!chunks.varlen) return (longest + len - 1) / len * chunks.n_seqs;
+    long long segs = 0;
+    for (const SeqInfo& q : chunks.natural) segs += ((q.len + kLinTcChunk - 1) / kLinTcChunk + len - 1) / len;
+    return segs;
+}
+
 // The cut with the least estimated time.  A sequence's chunks follow one another, so with
 // few (sequence, head) pairs most SMs would idle: two blocks of 64 value columns a pair
 // repeat the scores and the weighted keys, and segments read k and v twice.
 Cut choose_cut(const Plan& chunks, int H) {
-    long long longest = 0, total = chunks.n_chunks;
-    if (chunks.varlen)
-        for (const SeqInfo& q : chunks.natural) longest = std::max<long long>(longest, (q.len + kLinTcChunk - 1) / kLinTcChunk);
-    else
-        longest = chunks.n_seqs ? total / chunks.n_seqs : 0;
+    const long long longest = longest_of(chunks), total = chunks.n_chunks;
     Cut best;
     if (longest == 0) return best;
     best.seg_chunks = (int)longest;
@@ -60,11 +72,7 @@ Cut choose_cut(const Plan& chunks, int H) {
     for (int m = 1; m <= 8; ++m) {
         const long long len = std::max<long long>(4, (long long)(total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
         if (len >= longest) continue;
-        long long segs = 0;
-        if (chunks.varlen)
-            for (const SeqInfo& q : chunks.natural) segs += ((q.len + kLinTcChunk - 1) / kLinTcChunk + len - 1) / len;
-        else
-            segs = (longest + len - 1) / len * chunks.n_seqs;
+        const long long segs = segments_of(chunks, longest, len);
         const double waves = (double)((segs * H + kSms - 1) / kSms);
         const double first = (double)(((segs - chunks.n_seqs) * H + kSms - 1) / kSms);
         const double ts = len * (waves * kWalk128 + first * kStateOnly) + kSplitCost;
@@ -76,24 +84,61 @@ Cut choose_cut(const Plan& chunks, int H) {
     return best;
 }
 
+// The same for the backward pass's state chains (both directions side by side, all value
+// columns): what a split saves in idle SMs against walking the chunks twice.
+Cut choose_state_cut(const Plan& chunks, int H) {
+    const long long total = chunks.n_chunks;
+    const long long longest = longest_of(chunks);
+    Cut best;
+    if (longest == 0) return best;
+    best.seg_chunks = (int)longest;
+    double t = std::max((double)longest, 2.0 * total * H / kSms) * kStateOnly;
+    for (int m = 1; m <= 8; ++m) {
+        const long long len = std::max<long long>(4, (2 * total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
+        if (len >= longest) continue;
+        const long long segs = segments_of(chunks, longest, len);
+        const double waves = (double)((2 * segs * H + kSms - 1) / kSms);
+        const double first = (double)((2 * (segs - chunks.n_seqs) * H + kSms - 1) / kSms);
+        const double ts = len * (waves + first) * kStateOnly + kSplitCost;
+        if (ts < t) {
+            t = ts;
+            best = Cut{(int)len, 128, true};
+        }
+    }
+    return best;
+}
+
 struct TcLayout {
     Cut cut;
     Plan segs;          // segments as chunks
-    size_t err, state, gam, total;
+    size_t seg_tables, err, state, gam, images, d_images, total;
 };
 
-kda_status tc_layout(const Plan& chunks, const int32_t* cu, int n_seqs, int B, int T, int H, TcLayout& L) {
-    L.cut = choose_cut(chunks, H);
+kda_status tc_layout(const Plan& chunks, const int32_t* cu, int n_seqs, int B, int T, int H, bool bwd, TcLayout& L) {
+    L.cut = bwd ? choose_state_cut(chunks, H) : choose_cut(chunks, H);
     const kda_status st = plan_sequences(B, T, L.cut.seg_chunks * kLinTcChunk, cu, n_seqs, L.segs);
     if (st != KDA_OK) return st;
-    if ((long long)L.segs.n_chunks * H * 2 > 0x7fffffffLL) return KDA_ERR_SHAPE;
-    const size_t n = L.cut.split ? (size_t)L.segs.n_chunks * H : 0;
-    size_t o = table_bytes(L.segs);
+    if ((long long)L.segs.n_chunks * H * 2 > 0x7fffffffLL || (long long)chunks.n_chunks * H > 0x7fffffffLL)
+        return KDA_ERR_SHAPE;
+    const size_t n = L.cut.split ? (size_t)L.segs.n_chunks * H * (bwd ? 2 : 1) : 0;
+    // a number a chunk image, one more a sequence (see image_of)
+    const size_t images = bwd ? (size_t)(chunks.total_tokens / kLinTcChunk + chunks.n_seqs + 1) * H * 32768 : 0;
+    size_t o = bwd ? table_bytes(chunks) : 0;
+    L.seg_tables = o; o += table_bytes(L.segs);
     L.err = o; o += kAlign;
     L.state = o; o = align_up(o + n * 128 * 128 * sizeof(float));
     L.gam = o; o = align_up(o + n * sizeof(float));
+    L.images = o; o += images;
+    L.d_images = o; o += images;
     L.total = o;
     return KDA_OK;
+}
+
+int empty_of(const Plan& p) {   // sequences without tokens: the last of the longest-first order
+    if (p.total_tokens == 0) return p.n_seqs;
+    int n = 0;
+    for (const SeqInfo& q : p.natural) n += q.len == 0;
+    return n;
 }
 
 kda_status check_decay(kda_decay decay) {
@@ -145,6 +190,21 @@ kda_status guarded(F&& f) {
     }
 }
 
+kda_status chunk_status(bool bwd, const void* workspace, kda_dtype dtype, const int32_t* cu, int n_seqs, int B, int T,
+                        int H, int dk, int dv, void* stream) {
+    return guarded([&]() -> kda_status {
+        Plan p;
+        const bool tc = use_tc(dtype, dk, dv);
+        kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu, n_seqs, B, T, H, dk, dv, tc ? kLinTcChunk : kLinSimtChunk, p);
+        if (st != KDA_OK) return st;
+        if (!workspace) return KDA_ERR_NULL;
+        if (!tc || p.total_tokens == 0) return KDA_OK;   // nothing waited
+        TcLayout L;
+        if ((st = tc_layout(p, cu, n_seqs, B, T, H, bwd, L)) != KDA_OK) return st;
+        return read_error_word(workspace, L.err, stream);
+    });
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -166,7 +226,7 @@ size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, 
             return st;
         }
         TcLayout L;
-        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) == KDA_OK) n = L.total;
+        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, false, L)) == KDA_OK) n = L.total;
         return st;
     });
     return n;
@@ -190,7 +250,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
         if (tc) {
             TcLayout L;
-            if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) != KDA_OK) return st;
+            if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, false, L)) != KDA_OK) return st;
             if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
             if ((st = check_device()) != KDA_OK) return st;
             if (p.n_seqs == 0) return KDA_OK;
@@ -199,9 +259,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
             ChunkMap segs;
             SeqMap smap;
             if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws, s, segs, smap)) != KDA_OK) return st;
-            int empty = p.total_tokens == 0 ? p.n_seqs : 0;
-            if (p.varlen && p.total_tokens > 0)
-                for (const SeqInfo& q1 : p.natural) empty += q1.len == 0;
+            const int empty = empty_of(p);
             cudaError_t e = launch_lin_empty_states(init_state, final_state, smap, p.n_seqs - empty, empty, H, s);
             if (e == cudaSuccess && p.total_tokens > 0)
                 e = launch_lin_tc_fwd(q, k, v, dec, init_state, o, final_state, segs, smap, L.segs.n_chunks, p.n_seqs,
@@ -228,18 +286,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
 
 kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda_dtype dtype, const int32_t* cu_seqlens_host,
                                               int n_seqs, int B, int T, int H, int dk, int dv, void* stream) {
-    return guarded([&]() -> kda_status {
-        Plan p;
-        const bool tc = use_tc(dtype, dk, dv);
-        kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
-                                 tc ? kLinTcChunk : kLinSimtChunk, p);
-        if (st != KDA_OK) return st;
-        if (!workspace) return KDA_ERR_NULL;
-        if (!tc || p.total_tokens == 0) return KDA_OK;   // nothing waited
-        TcLayout L;
-        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, L)) != KDA_OK) return st;
-        return read_error_word(workspace, L.err, stream);
-    });
+    return chunk_status(false, workspace, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, stream);
 }
 
 size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
@@ -247,9 +294,16 @@ size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, 
     size_t n = 0;
     guarded([&] {
         Plan p;
-        const kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
-                                       kLinSimtChunk, p);
-        if (st == KDA_OK) n = simt_layout(p, H, dk, dv, true).total;
+        const bool tc = use_tc(dtype, dk, dv);
+        kda_status st = plan_for(KDA_DECAY_TOKEN, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
+                                 tc ? kLinTcChunk : kLinSimtChunk, p);
+        if (st != KDA_OK) return st;
+        if (!tc) {
+            n = simt_layout(p, H, dk, dv, true).total;
+            return st;
+        }
+        TcLayout L;
+        if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, true, L)) == KDA_OK) n = L.total;
         return st;
     });
     return n;
@@ -262,8 +316,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                                 void* workspace, size_t workspace_bytes, void* stream) {
     return guarded([&]() -> kda_status {
         Plan p;
+        const bool tc = use_tc(dtype, dk, dv);
         kda_status st = plan_for(decay, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv,
-                                       kLinSimtChunk, p);
+                                 tc ? kLinTcChunk : kLinSimtChunk, p);
         if (st != KDA_OK) return st;
         if (p.total_tokens > 0 && (!q || !k || !v || !log_alpha || !d_o || !dq || !dk_out || !dv_out ||
                                    (decay == KDA_DECAY_TOKEN && !dlog_alpha)))
@@ -274,6 +329,33 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                           (const void*)d_init_state}) ||
             ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
+        const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
+        if (tc) {
+            TcLayout L;
+            if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, true, L)) != KDA_OK) return st;
+            if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+            if ((st = check_device()) != KDA_OK) return st;
+            if (p.n_seqs == 0) return KDA_OK;
+            cudaStream_t s = (cudaStream_t)stream;
+            char* ws = (char*)workspace;
+            ChunkMap segs, chunks;
+            SeqMap smap, cmap;
+            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws + L.seg_tables, s, segs, smap)) != KDA_OK ||
+                (st = make_maps(p, T, kLinTcChunk, ws, s, chunks, cmap)) != KDA_OK)
+                return st;
+            const int empty = empty_of(p);
+            cudaError_t e = launch_lin_empty_states(d_final_state, d_init_state, smap, p.n_seqs - empty, empty, H, s);
+            uint8_t *im = (uint8_t*)(ws + L.images), *dim = (uint8_t*)(ws + L.d_images);
+            int* err = (int*)(ws + L.err);
+            if (e == cudaSuccess && p.total_tokens > 0)
+                e = launch_lin_tc_states(q, k, v, d_o, dec, init_state, d_final_state, d_init_state, segs, smap,
+                                         L.segs.n_chunks, p.n_seqs, L.cut.split, p.total_tokens, H,
+                                         (float*)(ws + L.state), (float*)(ws + L.gam), im, dim, err, s);
+            if (e == cudaSuccess && p.total_tokens > 0)
+                e = launch_lin_tc_grad(q, k, v, d_o, dec, dq, dk_out, dv_out, dlog_alpha, chunks, p.n_chunks,
+                                       p.total_tokens, H, im, dim, err, s);
+            return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        }
         const LinLayout L = simt_layout(p, H, dk, dv, true);
         if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
         if ((st = check_device()) != KDA_OK) return st;
@@ -284,13 +366,17 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
         SeqMap smap;
         if ((st = make_maps(p, T, kLinSimtChunk, ws, s, cmap, smap)) != KDA_OK) return st;
         const LinSimtWorkspace w{(float*)(ws + L.S), (float*)(ws + L.dS), (float*)(ws + L.gam)};
-        const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
         return launch_lin_simt_bwd(dtype, q, k, v, dec, init_state, d_o, d_final_state, dq, dk_out, dv_out,
                                    dlog_alpha, d_init_state, cmap, smap, p.n_chunks, p.n_seqs, H, dk, dv, w, s) ==
                        cudaSuccess
                    ? KDA_OK
                    : KDA_ERR_CUDA;
     });
+}
+
+kda_status kda_linear_chunk_bwd_device_status(const void* workspace, kda_dtype dtype, const int32_t* cu_seqlens_host,
+                                              int n_seqs, int B, int T, int H, int dk, int dv, void* stream) {
+    return chunk_status(true, workspace, dtype, cu_seqlens_host, n_seqs, B, T, H, dk, dv, stream);
 }
 
 kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const void* log_alpha, kda_decay decay,

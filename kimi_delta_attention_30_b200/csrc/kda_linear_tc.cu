@@ -354,34 +354,50 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 //   forward A = K, B = V, w = e^{g_C - g};  REV (chunks from last to first) A = Q, B = d_o,
 //   w = e^{g}, S the gradient of the chunk's end state.
 // With seg_end: from zero, the segment's own sum and whole decay (of every segment that
-// another one follows in the chain).  Warps 0-7 keep the state, 8-15 weight the rows; low
-// parts and accumulators are double buffered, so both and the products overlap.
+// another one follows in the chain).  With images (backward pass): from start, S ahead of
+// each chunk as a bf16 operand image (image_of).  Warps 0-7 keep the state, 8-15 weight the
+// rows; low parts and accumulators are double buffered, so both and the products overlap.
+// One launch takes both directions (blocks from n_fwd on run in reverse).
+struct StateSide {
+    const float* start;       // [N, H, dk, dv] or null (zero)
+    const float* seg_start;   // [segments, H, dk, dv] or null
+    float* seg_end;           // [segments, H, dk, dv] (sums), or null
+    float* seg_gam;           // [segments, H]
+    uint8_t* images;          // [image, H] x 32 KB, or null
+    float* end;               // [N, H, dk, dv] or null: the state behind the last chunk walked
+};
 constexpr int kStSlots = 4;
 constexpr uint32_t kStLo = kStSlots * kTile;
-constexpr uint32_t kStGates = kStLo + 2 * kTile;
+constexpr uint32_t kStStage = kStLo + 2 * kTile;       // the state's image on its way out
+constexpr uint32_t kStGates = kStStage + kTile;
 constexpr uint32_t kStBars = kStGates + 2 * sizeof(Gates);
 constexpr uint32_t kStSmem = kStBars + 256;
 static_assert(kStSmem <= 232448, "shared memory per block");
 enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSURead = kSUDone + 2,
              kSGFull = kSURead + 2, kSGEmpty = kSGFull + 2, kSDrain = kSGEmpty + 2, kStBarsN };
 
-template <bool REV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
-lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, LinDecay dec, ChunkMap segs,
-          int H, float* __restrict__ seg_end, float* __restrict__ seg_gam, int* __restrict__ err) {
+lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+          const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, LinDecay dec, ChunkMap segs,
+          int H, int n_fwd, StateSide fwd, StateSide bwd, int clear_err, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    if (tid == 0 && blockIdx.x == 0) *err = 0;   // first kernel of the call
+    if (tid == 0 && blockIdx.x == 0 && clear_err) *err = 0;   // first kernel of the call
     if (smem_u32(sm) & 1023u) {
         if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
         return;
     }
-    const int h = (int)(blockIdx.x % H), seg = (int)(blockIdx.x / H);
+    const bool REV = (int)blockIdx.x >= n_fwd;
+    const int unit = (int)blockIdx.x - (REV ? n_fwd : 0);
+    const StateSide& A = REV ? bwd : fwd;
+    const CUtensorMap *ma = REV ? &mq : &mk, *mb = REV ? &mdo : &mv;
+    const int h = unit % H, seg = unit / H;
     int seq, tok0, len, idx;
     segs.locate(seg, seq, tok0, len, idx);
-    if (REV ? idx == 0 : last_segment(segs, seq, idx)) return;   // nothing follows it
+    const bool last = REV ? idx == 0 : last_segment(segs, seq, idx);
+    if (A.seg_end && last) return;   // nothing follows it
     const int nch = (len + kT - 1) / kT;
     if (tid == 0) {
         for (int i = 0; i < kStBarsN; ++i)
@@ -408,16 +424,44 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
 
     if (warp >= 16) fewer_registers<40>();
     if (warp < 8) {   // ---- the state
+        more_registers<120>();
         const int sp = warp & 3, hb = warp >> 2, row = 32 * sp + lane;
         const uint32_t lanes = (uint32_t)(32 * sp) << 16;
         float s[64];
+        {
+            const float* src = A.seg_end ? nullptr
+                               : A.seg_start ? A.seg_start + ((size_t)seg * H + h) * kD * kD
+                               : A.start ? A.start + ((size_t)seq * H + h) * kD * kD
+                                         : nullptr;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) s[j] = 0.f;
+            for (int j = 0; j < 64; j += 4) {
+                const float4 x = src ? *reinterpret_cast<const float4*>(src + (size_t)row * kD + 64 * hb + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+            }
+        }
+        const long long image0 = image_of(tok0 - idx * segs.C, seq) + (long long)idx * (segs.C / kT);
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             if (!(ok = wait_or_abort(&bars[kSGFull + (n & 1)], half_par(n), ab))) break;
             const float gam = gates[n & 1].gam;
             warp_arrive(&bars[kSGEmpty + (n & 1)], lane);
+            if (A.images) {   // this warp's 4 KB of the image: staged swizzled, copied out in one piece
+                uint8_t* stage = sm + kStStage + hb * kBlock + 32 * sp * 128;
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (row & 7)) << 4)) =
+                        make_uint4(pack_bf16(s[8 * c], s[8 * c + 1]), pack_bf16(s[8 * c + 2], s[8 * c + 3]),
+                                   pack_bf16(s[8 * c + 4], s[8 * c + 5]), pack_bf16(s[8 * c + 6], s[8 * c + 7]));
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_s2g(A.images + ((image0 + chunk(n)) * H + h) * kTile + hb * kBlock + 32 * sp * 128, stage, 4096);
+                    bulk_commit();
+                }
+            }
             if (!(ok = wait_or_abort(&bars[kSUDone + (n & 1)], half_par(n), ab))) break;
             tc_fence_after();
 #pragma unroll
@@ -431,14 +475,17 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
             tc_fence_before();
             warp_arrive(&bars[kSURead + (n & 1)], lane);
         }
-        if (ok) {
-            float* dst = seg_end + (((size_t)seg * H + h) * kD + row) * kD + 64 * hb;
+        if (lane == 0) bulk_wait_read_all();   // before the block's shared memory goes
+        float* to = A.seg_end ? A.seg_end + ((size_t)seg * H + h) * kD * kD
+                    : A.end && last ? A.end + ((size_t)seq * H + h) * kD * kD
+                                    : nullptr;
+        if (ok && to) {
+            float* dst = to + (size_t)row * kD + 64 * hb;
 #pragma unroll
             for (int j = 0; j < 64; j += 4)
                 *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         }
     } else if (warp < 16) {   // ---- weighted rows
-        more_registers<120>();
         const int r = tid & 127, blk = (tid - 256) >> 7;
         for (int n = 0; n < nch; ++n) {
             const int live = min(kT, len - chunk(n) * kT);
@@ -490,8 +537,8 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
                 if (i >= kStSlots && !(ok = wait_or_abort(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab))) break;
                 const int t = tok0 + chunk(i / 2) * kT;
                 mbar_arrive_expect_tx(full(i), kTile);
-                tma_box(slot(i), i & 1 ? &mb : &ma, 0, h, t, full(i));
-                tma_box(slot(i) + kBlock, i & 1 ? &mb : &ma, 64, h, t, full(i));
+                tma_box(slot(i), i & 1 ? mb : ma, 0, h, t, full(i));
+                tma_box(slot(i) + kBlock, i & 1 ? mb : ma, 64, h, t, full(i));
             }
             if (!ok)
                 for (int j = max(0, i - kStSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
@@ -514,7 +561,7 @@ lin_state(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtens
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
-        if (lane == 0) seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
+        if (lane == 0 && A.seg_end) A.seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
     }
     __syncwarp();
     tc_fence_before();
@@ -599,9 +646,10 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
         return cudaErrorNotSupported;
     cudaError_t e;
     if (split) {
-        if ((e = allow_smem(lin_state<false>, kStSmem)) != cudaSuccess) return e;
-        lin_state<false><<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, dec, segs, H, seg_state, seg_gam,
-                                                                            err);
+        if ((e = allow_smem(lin_state, kStSmem)) != cudaSuccess) return e;
+        const StateSide side{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
+        lin_state<<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, H, n_segs * H, side,
+                                                                     side, 1, err);
         seg_chain<false><<<dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s>>>(seg_state, seg_gam, init_state,
                                                                                    smap, H);
     }
@@ -609,6 +657,35 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
     kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
         mq, mk, mv, dec, segs, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
+    return cudaGetLastError();
+}
+
+// Backward, first part: the bf16 images of every chunk's start state and of the gradient of
+// its end state, and the initial state's gradient.
+cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, const void* d_o, LinDecay dec,
+                                 const float* init_state, const float* d_final, float* d_init, const ChunkMap& segs,
+                                 const SeqMap& smap, int n_segs, int n_seqs, bool split, long long tokens, int H,
+                                 float* seg_state, float* seg_gam, uint8_t* images, uint8_t* d_images, int* err,
+                                 cudaStream_t s) {
+    CUtensorMap mq, mk, mv, mdo;
+    if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
+        !make_map(&mdo, d_o, tokens, H))
+        return cudaErrorNotSupported;
+    cudaError_t e;
+    if ((e = allow_smem(lin_state, kStSmem)) != cudaSuccess) return e;
+    const int units = n_segs * H;
+    float *d_seg = seg_state + (size_t)units * kD * kD, *d_gam = seg_gam + units;
+    if (split) {
+        const StateSide f{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
+        const StateSide r{nullptr, nullptr, d_seg, d_gam, nullptr, nullptr};
+        lin_state<<<2u * units, kWalkThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, H, units, f, r, 1, err);
+        const dim3 grid((unsigned)n_seqs * H, kD * kD / 1024);
+        seg_chain<false><<<grid, 256, 0, s>>>(seg_state, seg_gam, init_state, smap, H);
+        seg_chain<true><<<grid, 256, 0, s>>>(d_seg, d_gam, d_final, smap, H);
+    }
+    const StateSide f{init_state, split ? seg_state : nullptr, nullptr, nullptr, images, nullptr};
+    const StateSide r{d_final, split ? d_seg : nullptr, nullptr, nullptr, d_images, d_init};
+    lin_state<<<2u * units, kWalkThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, H, units, f, r, !split, err);
     return cudaGetLastError();
 }
 

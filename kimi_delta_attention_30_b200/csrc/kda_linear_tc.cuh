@@ -23,6 +23,10 @@ constexpr uint32_t kBlock = 16384;
 // does not offer the call or rejects the array.
 bool make_map(CUtensorMap* map, const void* base, long long tokens, int H);
 
+// Number of a chunk's state image: chunks of different sequences never meet, since a sequence
+// that ends inside a block of 128 tokens leaves a number out (seq_tok0: its first token).
+__host__ __device__ __forceinline__ long long image_of(long long seq_tok0, long long seq) { return seq_tok0 / kT + seq; }
+
 // Box (channels x0 .. x0 + 63, head h, tokens t0 .. t0 + 127) -> 16 KB of shared memory.
 // Rows past the array's end read as zero.
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x0, int h, int t0, uint64_t* bar) {
