@@ -14,9 +14,11 @@
 // Eight products of 128^3 a chunk (4096 tensor cycles) against 288 KB of memory traffic
 // (6.6 us an SM at the measured copy rate): bound by memory as long as loads overlap the
 // work.  A block keeps one chunk in six 32 KB slots; a slot is loaded for the block's next
-// chunk as soon as its last product is done (Z's first, Q's last), and P and B replace S and
-// V, which nothing needs by then.  16 warps do the elementwise work: warp (R, B) owns rows
-// 32 R + lane and columns 32 B + [0, 32).
+// chunk as soon as nothing needs it.  P and B replace S and V.  The results leave through
+// slots too (dV Z's, dQ K's, dK Q's: free by then, and needed last by the next chunk), one box
+// a warp: stored from registers, a row a lane, they held the load/store pipe for 3000 cycles.
+// 16 warps do the elementwise work: warp (R, B) owns rows 32 R + lane and columns
+// 32 B + [0, 32).
 #include <algorithm>
 
 #include "kda_linear_tc.cuh"
@@ -25,7 +27,7 @@ namespace kda {
 namespace lintc {
 namespace {
 
-constexpr int kGradThreads = 608;   // warps 0-15 elementwise, 16 products, 17 loads, 18 decays
+constexpr int kGradThreads = 640;   // warps 0-15 elementwise, 16 products, 17 loads, 18 decays, 19 dlog_alpha
 enum Slot { kQ = 0, kK, kV, kDO, kS, kZ, kSlotsN };
 constexpr uint32_t kOffGates = kSlotsN * kTile;
 
@@ -43,8 +45,8 @@ constexpr uint32_t kOffBars = kOffSums + sizeof(GradSums);
 constexpr uint32_t kGradSmem = kOffBars + 256;
 static_assert(kOffBars % 8 == 0 && kGradSmem <= 232448, "shared memory per block");
 
-enum GradBar { kFull = 0, kFree = kSlotsN, kInter = 2 * kSlotsN, kKInter, kScores, kClean, kPReady, kDvDone, kDqDone, kDkDone,
-               kRead, kGFull, kGEmpty = kGFull + 2, kSumsFull = kGEmpty + 2, kSumsEmpty, kDrain, kGradBars };
+enum GradBar { kFull = 0, kFree = kSlotsN, kInter = 2 * kSlotsN, kKInter, kScores, kClean, kSRead, kPReady, kDvDone, kDqDone, kDkDone,
+               kRead, kGFull = kRead + 3, kGEmpty = kGFull + 2, kSumsFull = kGEmpty + 2, kSumsEmpty, kDrain, kGradBars };
 
 // lane l of the warp gets the sum over all lanes of v[l]
 __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
@@ -85,7 +87,9 @@ __device__ __forceinline__ float dot16(const float (&x)[16], const uint8_t* tile
 __global__ void __launch_bounds__(kGradThreads, 1)
 lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, LinDecay dec,
-            ChunkMap chunks, int n_units, int H, const uint8_t* __restrict__ s_images,
+            const __grid_constant__ CUtensorMap mdq, const __grid_constant__ CUtensorMap mdk,
+            const __grid_constant__ CUtensorMap mdv, ChunkMap chunks, int n_units, int H,
+            const uint8_t* __restrict__ s_images,
             const uint8_t* __restrict__ z_images, __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
             __nv_bfloat16* __restrict__ dv, __nv_bfloat16* __restrict__ dla, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -98,8 +102,11 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     if (tid == 0) {
         for (int i = 0; i < kGradBars; ++i)   // one arrival a warp
-            mbar_init(&bars[i], i == kClean || i == kPReady || i == kRead || i == kSumsFull || i == kGEmpty || i == kGEmpty + 1
-                                    ? 16 : 1);
+            mbar_init(&bars[i], i == kClean || i == kSRead || i == kPReady || (i >= kRead && i < kRead + 3) || i == kSumsFull
+                                    ? 16
+                                : i == kGEmpty || i == kGEmpty + 1                    ? 17   // and the dlog_alpha warp
+                                : i == kFree + kZ || i == kFree + kK || i == kFree + kQ ? 17   // results left, products done
+                                                                                        : 1);
         mbar_init_fence();
         flags[1] = 0u;
     }
@@ -130,25 +137,6 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             const int h = u % H;
             if (!wait_or_abort(&bars[kGFull + (it & 1)], (uint32_t)(it >> 1) & 1u, ab)) break;
             const Gates& G = gates[it & 1];
-            // <Z, S>, 1/16 of the tiles a warp
-            if (!wait_or_abort(&bars[kFull + kS], par, ab) || !wait_or_abort(&bars[kFull + kZ], par, ab)) break;
-            if (!wait_or_abort(&bars[kSumsEmpty], par ^ 1u, ab)) break;   // the last unit's sums are read
-            {
-                float z = 0.f;
-#pragma unroll 2
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t off = (uint32_t)(warp * 128 + i * 32 + lane) * 16;
-                    const uint4 x = *reinterpret_cast<const uint4*>(slot(kS) + off), y = *reinterpret_cast<const uint4*>(slot(kZ) + off);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        z = fmaf(bf16_lo(xs[e]), bf16_lo(ys[e]), z);
-                        z = fmaf(bf16_hi(xs[e]), bf16_hi(ys[e]), z);
-                    }
-                }
-                z = warp_sum(z);
-                if (lane == 0) sums.zs[warp] = z;
-            }
             if (len < kT) {   // rows of the next sequence: out of the sums over tokens
                 if (!wait_or_abort(&bars[kFull + kQ], par, ab) || !wait_or_abort(&bars[kFull + kK], par, ab) ||
                     !wait_or_abort(&bars[kFull + kDO], par, ab))
@@ -158,9 +146,9 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 zero_rows(slot(kDO), 2, len, tid, 512);
                 fence_async_smem();
             }
-            // S has been read here (P replaces it later), the rows are clean
             warp_arrive(&bars[kClean], lane);
             if (len < kT && !wait_or_abort(&bars[kClean], par, ab)) break;
+            if (!wait_or_abort(&bars[kSumsEmpty], par ^ 1u, ab)) break;   // the last unit's sums are read
             const float r2 = G.rel2[row], er = ex2_approx(r2), wq = er * G.start[R], wk = G.col[row] * G.end[R];
             // the states' parts of dQ and dK: scaled where they stand, and their dots
             if (!wait_or_abort(&bars[kFull + kQ], par, ab) || !wait_or_abort(&bars[kFull + kK], par, ab)) break;
@@ -185,8 +173,27 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 (side ? sums.b : sums.a)[B][row] = row < len ? dot : 0.f;
             }
             if (!ok) break;
-            // P, B and the sums of M
-            if (!wait_or_abort(&bars[kScores], par, ab)) break;
+            // <Z, S>, 1/16 of the tiles a warp
+            if (!wait_or_abort(&bars[kFull + kS], par, ab) || !wait_or_abort(&bars[kFull + kZ], par, ab)) break;
+            {
+                float z = 0.f;
+#pragma unroll 2
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t off = (uint32_t)(warp * 128 + i * 32 + lane) * 16;
+                    const uint4 x = *reinterpret_cast<const uint4*>(slot(kS) + off), y = *reinterpret_cast<const uint4*>(slot(kZ) + off);
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        z = fmaf(bf16_lo(xs[e]), bf16_lo(ys[e]), z);
+                        z = fmaf(bf16_hi(xs[e]), bf16_hi(ys[e]), z);
+                    }
+                }
+                z = warp_sum(z);
+                if (lane == 0) sums.zs[warp] = z;
+            }
+            warp_arrive(&bars[kSRead], lane);
+            // P, B and the sums of M; P replaces S, once every warp has read its part
+            if (!wait_or_abort(&bars[kScores], par, ab) || !wait_or_abort(&bars[kSRead], par, ab)) break;
             tc_fence_after();
             float m[32];
             if (B > R) {
@@ -205,19 +212,23 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                     tmem_ld16(tA + at + 16 * g, x);
                     tmem_ld16(tB + at + 16 * g, y);
                     tmem_ld_wait();
+                    if (B < R) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 c = *reinterpret_cast<const float4*>((B < R ? G.col : G.rel2) + 32 * B + 16 * g + e);
-                        const float cc[4] = {c.x, c.y, c.z, c.w};
+                        for (int e = 0; e < 16; ++e) {
+                            const float d = f * G.col[32 * B + 16 * g + e], p = in ? x[e] * d : 0.f;
+                            m[16 * g + e] = in ? p * y[e] : 0.f;
+                            x[e] = p;
+                            y[e] = in ? y[e] * d : 0.f;
+                        }
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = 16 * g + e + i;
-                            const bool keep = in && (B < R || j <= lane);
-                            const float d = B < R ? f * cc[i] : ex2_approx(r2 - cc[i]);
-                            const float p = keep ? x[e + i] * d : 0.f, b = keep ? y[e + i] * d : 0.f;
-                            m[j] = keep && (B < R || j < lane) ? p * y[e + i] : 0.f;
-                            x[e + i] = p;
-                            y[e + i] = b;
+                        for (int e = 0; e < 16; ++e) {
+                            const int j = 16 * g + e;
+                            const bool keep = in && j <= lane;
+                            const float d = ex2_approx(r2 - G.rel2[32 * B + j]), p = keep ? x[e] * d : 0.f;
+                            m[j] = keep && j < lane ? p * y[e] : 0.f;
+                            x[e] = p;
+                            y[e] = keep ? y[e] * d : 0.f;
                         }
                     }
 #pragma unroll
@@ -260,10 +271,13 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             warp_arrive(&bars[kGEmpty + (it & 1)], lane);
             // dV = w (K Z) + P^T dO, then dQ and dK
             const size_t base = ((size_t)(tok0 + row) * H + h) * kD + 32 * B;
+            const bool whole = 32 * R + 32 <= len;
 #pragma unroll 1
             for (int out = 0; out < 3; ++out) {
                 if (!(ok = wait_or_abort(&bars[kDvDone + out], par, ab))) break;
                 tc_fence_after();
+                const int through = out == 0 ? kZ : out == 1 ? kK : kQ;
+                uint8_t* stage = slot(through) + warp * 2048;
                 __nv_bfloat16* dst = (out == 0 ? dv : out == 1 ? dq : dk) + base;
 #pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
@@ -281,13 +295,35 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                     uint32_t w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-                    if (row < len) store32(dst + 16 * g, w);
+                    if (whole) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            *reinterpret_cast<uint4*>(stage + lane * 64 + (((2 * g + c) ^ ((lane >> 1) & 3)) << 4)) =
+                                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    } else if (row < len) {
+                        store32(dst + 16 * g, w);
+                    }
+                }
+                tc_fence_before();
+                warp_arrive(&bars[kRead + out], lane);   // the accumulator is free
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (whole) tma_store_box(out == 0 ? &mdv : out == 1 ? &mdq : &mdk, stage, 32 * B, h, tok0 + 32 * R);
+                    bulk_commit();
+                    if (out > 0) {   // the result before this one has left its slot
+                        bulk_wait_read_but1();
+                        mbar_arrive(&bars[kFree + (out == 1 ? kZ : kK)]);
+                    }
                 }
             }
             if (!ok) break;
-            tc_fence_before();
-            warp_arrive(&bars[kRead], lane);
+            if (lane == 0) {
+                bulk_wait_read_all();
+                mbar_arrive(&bars[kFree + kQ]);
+            }
         }
+        if (lane == 0) bulk_wait_read_all();
     } else if (warp == 16) {   // ---- products
         constexpr uint32_t iKK = idesc_bf16_f32(128, 128), iKM = idesc_bf16_f32_bmn(128, 128), iMM = idesc_amn_bmn(128, 128);
         const uint32_t lead = elect_lane(), base = smem_u32(sm);
@@ -300,15 +336,18 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         int it = 0;
         for (int u = first; u < n_units; u += step, ++it) {
             const uint32_t par = (uint32_t)it & 1u;
-            // the last unit's results have been read
-            if (it > 0 && !(ok = wait_or_abort(&bars[kRead], par ^ 1u, ab))) break;
+            // (each accumulator once the last unit's result has been read from it)
+            if (it > 0 && !(ok = wait_or_abort(&bars[kRead + 1], par ^ 1u, ab))) break;
             if (!(ok = wait_or_abort(&bars[kFull + kDO], par, ab) && wait_or_abort(&bars[kFull + kS], par, ab) &&
                        wait_or_abort(&bars[kClean], par, ab)))
                 break;
             tc_fence_after();
             product<false, false>(tQ, ktile(kDO), ktile(kS), iKK, false, lead);
             commit(kInter);
+            if (it > 0 && !(ok = wait_or_abort(&bars[kRead + 2], par ^ 1u, ab) && wait_or_abort(&bars[kRead], par ^ 1u, ab)))
+                break;
             if (!(ok = wait_or_abort(&bars[kFull + kV], par, ab) && wait_or_abort(&bars[kFull + kZ], par, ab))) break;
+            tc_fence_after();
             product<false, false>(tK, ktile(kV), ktile(kZ), iKK, false, lead);
             commit(kKInter);
             if (!(ok = wait_or_abort(&bars[kFull + kQ], par, ab) && wait_or_abort(&bars[kFull + kK], par, ab))) break;
@@ -338,7 +377,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         }
     } else if (warp == 17) {
         if (lane == 0) {   // ---- loads, in the order the slots are free and needed
-            constexpr int kOrder[kSlotsN] = {kZ, kS, kDO, kK, kV, kQ};
+            constexpr int kOrder[kSlotsN] = {kS, kDO, kV, kZ, kK, kQ};
             int it = 0, i = 0;
             bool ok = true;
             for (int u = first; ok && u < n_units; u += step, ++it) {
@@ -349,7 +388,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 const size_t image = (size_t)(image_of(tok0 - idx * kT, seq) + idx) * H + h;
                 for (i = 0; i < kSlotsN; ++i) {
                     const int k = kOrder[i];
-                    if (it > 0 && !(ok = wait_or_abort(&bars[kFree + k], par ^ 1u, ab))) break;
+                    if (it > 0 && !(ok = wait_or_abort_lane(&bars[kFree + k], par ^ 1u, ab))) break;
                     uint64_t* bar = &bars[kFull + k];
                     mbar_arrive_expect_tx(bar, kTile);
                     if (k == kS || k == kZ) {
@@ -367,34 +406,29 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 }
             }
         }
-    } else {   // ---- decays, and dlog_alpha from the sums
-        float x[4];
-        auto load = [&](int u) {
+    } else if (warp == 18) {   // ---- decays
+        float x[4], y[4];
+        auto load = [&](int u, float(&to)[4]) {
             int seq, tok0, len, idx;
             chunks.locate(u / H, seq, tok0, len, idx);
-            load_gates(x, dec, tok0, len, H, u % H, lane);
+            load_gates(to, dec, tok0, len, H, u % H, lane);
         };
-        float gam = 0.f, next_gam = 0.f;
-        auto make = [&](int i) {   // the gates of this block's unit number i, from x
-            if (i >= 2 && !wait_or_abort(&bars[kGEmpty + (i & 1)], ((uint32_t)(i >> 1) & 1u) ^ 1u, ab)) return false;
-            make_gates(&gates[i & 1], x, lane);
-            warp_arrive(&bars[kGFull + (i & 1)], lane);
-            next_gam = gates[i & 1].gam;
-            return true;
-        };
-        bool ok = true;
-        if (first < n_units) {
-            load(first);
-            ok = make(0);
-            if (first + step < n_units) load(first + step);
-        }
+        if (first < n_units) load(first, x);
         int it = 0;
-        for (int u = first; ok && u < n_units; u += step, ++it) {
-            gam = next_gam;
-            if (u + step < n_units) {   // the next unit's decays first, then this one's sums
-                if (!(ok = make(it + 1))) break;
-                if (u + 2 * step < n_units) load(u + 2 * step);
-            }
+        for (int u = first; u < n_units; u += step, ++it) {
+            if (u + step < n_units) load(u + step, y);
+            if (it >= 2 && !wait_or_abort(&bars[kGEmpty + (it & 1)], ((uint32_t)(it >> 1) & 1u) ^ 1u, ab)) break;
+            make_gates(&gates[it & 1], x, lane);
+            warp_arrive(&bars[kGFull + (it & 1)], lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = y[e];
+        }
+    } else {   // ---- dlog_alpha from the sums
+        int it = 0;
+        for (int u = first; u < n_units; u += step, ++it) {
+            if (!wait_or_abort(&bars[kGFull + (it & 1)], (uint32_t)(it >> 1) & 1u, ab)) break;
+            const float gam = gates[it & 1].gam;
+            warp_arrive(&bars[kGEmpty + (it & 1)], lane);
             if (!wait_or_abort(&bars[kSumsFull], (uint32_t)it & 1u, ab)) break;
             // tokens 4 lane + e; the block of 32 is lane / 8
             const int blk = lane >> 3, t0 = 4 * lane;
@@ -478,11 +512,15 @@ cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, cons
     if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
         !make_map(&mdo, d_o, tokens, H))
         return cudaErrorNotSupported;
+    CUtensorMap mdq, mdk, mdv;
+    if (!make_map(&mdq, dq, tokens, H, 32, 32) || !make_map(&mdk, dk, tokens, H, 32, 32) ||
+        !make_map(&mdv, dv, tokens, H, 32, 32))
+        return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(lin_grad_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
     if (e != cudaSuccess) return e;
     const int units = n_chunks * H;
     lin_grad_tc<<<std::min(units, 148), kGradThreads, kGradSmem, s>>>(
-        mq, mk, mv, mdo, dec, chunks, units, H, images, d_images, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk,
+        mq, mk, mv, mdo, dec, mdq, mdk, mdv, chunks, units, H, images, d_images, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk,
         (__nv_bfloat16*)dv, dec.per_head ? nullptr : (__nv_bfloat16*)dla, err);
     return cudaGetLastError();
 }

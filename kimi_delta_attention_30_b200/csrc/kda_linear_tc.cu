@@ -32,7 +32,7 @@
 namespace kda {
 namespace lintc {
 
-bool make_map(CUtensorMap* map, const void* base, long long tokens, int H) {
+bool make_map(CUtensorMap* map, const void* base, long long tokens, int H, int box_channels, int box_tokens) {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -47,9 +47,10 @@ bool make_map(CUtensorMap* map, const void* base, long long tokens, int H) {
     if (encode == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)H * kD * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kT}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)box_channels, 1, (cuuint32_t)box_tokens}, step[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -78,8 +79,8 @@ enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady, kQsDon
 template <int BV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-         const __grid_constant__ CUtensorMap mv, LinDecay dec, ChunkMap segs, int H,
-         const float* __restrict__ init_state, const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
+         const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, LinDecay dec, ChunkMap segs,
+         int H, const float* __restrict__ init_state, const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
          float* __restrict__ final_state, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
@@ -141,6 +142,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             }
         }
         auto publish = [&]() {   // the state's bf16 copy, an MN-major B operand
+            if (lane == 0) bulk_wait_read_all();   // o has left its buffer
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < HB; j += 8) {
                 const uint4 w = make_uint4(pack_bf16(s[j], s[j + 1]), pack_bf16(s[j + 2], s[j + 3]),
@@ -161,7 +164,13 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             // o = P V + e^g (Q S)
             if (!(ok = wait_or_abort(&bars[kODone], par, ab) && wait_or_abort(&bars[kQsDone], par, ab))) break;
             tc_fence_after();
+            // A lane's row in pieces of 32 bytes, straight to global memory, would cost the
+            // load/store pipe 32 cycles a store; so the rows go by way of shared memory: into
+            // the state's buffer, whose last reader is Q S (the copy takes one half of it when
+            // BV is 64), and out in one box a warp.  Warps with rows past the end store theirs.
+            const bool whole = 32 * sp + 32 <= len - n * kT;
             __nv_bfloat16* dst = o + ((size_t)(tok0 + n * kT + row) * H + h) * kD + j0 + HB * hb;
+            uint8_t* stage = sm + kOffS + (BV == 128 ? hb * kBlock + 32 * sp * 128 : kBlock + (4 * hb + sp) * 2048);
 #pragma unroll 1
             for (int g = 0; g < HB / 16; ++g) {
                 float a[16], b[16];
@@ -171,7 +180,22 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) w[e / 2] = pack_bf16(fmaf(eg, b[e], a[e]), fmaf(eg, b[e + 1], a[e + 1]));
-                if (row < len - n * kT) store32(dst + 16 * g, w);
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int x = BV == 128 ? (2 * g + c) ^ (lane & 7) : (2 * g + c) ^ ((lane >> 1) & 3);
+                        *reinterpret_cast<uint4*>(stage + lane * (BV == 128 ? 128 : 64) + x * 16) =
+                            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    }
+                } else if (row < len - n * kT) {
+                    store32(dst + 16 * g, w);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (whole && lane == 0) {
+                tma_store_box(&mo, stage, j0 + HB * hb, h, tok0 + n * kT + 32 * sp);
+                bulk_commit();
             }
             tc_fence_before();
             warp_arrive(&bars[kORead], lane);
@@ -190,6 +214,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                 publish();
             }
         }
+        if (lane == 0) bulk_wait_read_all();   // before the block's shared memory goes
         if (final_state && ok && last_segment(segs, seq, idx)) {
             float* dst = final_state + (((size_t)seq * H + h) * kD + row) * kD + j0 + HB * hb;
 #pragma unroll
@@ -314,7 +339,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             int i = 0;
             bool ok = true;
             for (; i < 3 * nch; ++i) {
-                if (i >= kSlots && !(ok = wait_or_abort(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
+                if (i >= kSlots && !(ok = wait_or_abort_lane(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
                 const int t = tok0 + (i / 3) * kT, kind = i % 3;
                 const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
                 uint8_t* dst = slot(i);
@@ -369,12 +394,13 @@ struct StateSide {
 constexpr int kStSlots = 4;
 constexpr uint32_t kStLo = kStSlots * kTile;
 constexpr uint32_t kStStage = kStLo + 2 * kTile;       // the state's image on its way out
+constexpr int kStGateBufs = 4;
 constexpr uint32_t kStGates = kStStage + kTile;
-constexpr uint32_t kStBars = kStGates + 2 * sizeof(Gates);
+constexpr uint32_t kStBars = kStGates + kStGateBufs * sizeof(Weights);
 constexpr uint32_t kStSmem = kStBars + 256;
 static_assert(kStSmem <= 232448, "shared memory per block");
 enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSURead = kSUDone + 2,
-             kSGFull = kSURead + 2, kSGEmpty = kSGFull + 2, kSDrain = kSGEmpty + 2, kStBarsN };
+             kSGFull = kSURead + 2, kSGEmpty = kSGFull + kStGateBufs, kSDrain = kSGEmpty + kStGateBufs, kStBarsN };
 
 __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -402,7 +428,7 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     if (tid == 0) {
         for (int i = 0; i < kStBarsN; ++i)
             mbar_init(&bars[i], i >= kSWReady && i < kSWReady + 2 ? 8 : i >= kSURead && i < kSURead + 2 ? 8
-                                : i >= kSGEmpty && i < kSGEmpty + 2 ? 16 : 1);
+                                : i >= kSGEmpty && i < kSGEmpty + kStGateBufs ? 16 : 1);
         mbar_init_fence();
         flags[1] = 0u;
     }
@@ -420,7 +446,10 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     auto full = [&](int i) { return &bars[kSFull + i % kStSlots]; };
     auto full_par = [&](int i) { return (uint32_t)(i / kStSlots) & 1u; };
     auto half_par = [&](int n) { return (uint32_t)(n >> 1) & 1u; };   // of barriers kept for chunks of either parity
-    Gates* gates = reinterpret_cast<Gates*>(sm + kStGates);
+    Weights* gates = reinterpret_cast<Weights*>(sm + kStGates);
+    auto gates_full = [&](int n) {
+        return wait_or_abort(&bars[kSGFull + n % kStGateBufs], (uint32_t)(n / kStGateBufs) & 1u, ab);
+    };
 
     if (warp >= 16) fewer_registers<40>();
     if (warp < 8) {   // ---- the state
@@ -443,9 +472,9 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         const long long image0 = image_of(tok0 - idx * segs.C, seq) + (long long)idx * (segs.C / kT);
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
-            if (!(ok = wait_or_abort(&bars[kSGFull + (n & 1)], half_par(n), ab))) break;
-            const float gam = gates[n & 1].gam;
-            warp_arrive(&bars[kSGEmpty + (n & 1)], lane);
+            if (!(ok = gates_full(n))) break;
+            const float gam = gates[n % kStGateBufs].gam;
+            warp_arrive(&bars[kSGEmpty + n % kStGateBufs], lane);
             if (A.images) {   // this warp's 4 KB of the image: staged swizzled, copied out in one piece
                 uint8_t* stage = sm + kStStage + hb * kBlock + 32 * sp * 128;
                 if (lane == 0) bulk_wait_read_all();
@@ -489,10 +518,9 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         const int r = tid & 127, blk = (tid - 256) >> 7;
         for (int n = 0; n < nch; ++n) {
             const int live = min(kT, len - chunk(n) * kT);
-            if (!wait_or_abort(&bars[kSGFull + (n & 1)], half_par(n), ab)) break;
-            const Gates& G = gates[n & 1];
-            const float w = REV ? ex2_approx(G.rel2[r]) * G.start[r >> 5] : G.col[r] * G.end[r >> 5];
-            warp_arrive(&bars[kSGEmpty + (n & 1)], lane);
+            if (!gates_full(n)) break;
+            const float w = gates[n % kStGateBufs].w[r];
+            warp_arrive(&bars[kSGEmpty + n % kStGateBufs], lane);
             if (!wait_or_abort(full(2 * n), full_par(2 * n), ab) ||
                 (n >= 2 && !wait_or_abort(&bars[kSUDone + (n & 1)], half_par(n) ^ 1u, ab)))   // low parts are free
                 break;
@@ -534,7 +562,7 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
             int i = 0;
             bool ok = true;
             for (; i < 2 * nch; ++i) {
-                if (i >= kStSlots && !(ok = wait_or_abort(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab))) break;
+                if (i >= kStSlots && !(ok = wait_or_abort_lane(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab))) break;
                 const int t = tok0 + chunk(i / 2) * kT;
                 mbar_arrive_expect_tx(full(i), kTile);
                 tma_box(slot(i), i & 1 ? mb : ma, 0, h, t, full(i));
@@ -545,23 +573,20 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         }
     } else if (warp == 18) {   // ---- decays
         float x[4], y[4];
-        double whole = 0.0;   // log decay of the segment
+        long long whole = 0;   // log decay of the segment
         load_gates(x, dec, (long long)tok0 + chunk(0) * kT, min(kT, len - chunk(0) * kT), H, h, lane);
         for (int n = 0; n < nch; ++n) {
             if (n + 1 < nch)
                 load_gates(y, dec, (long long)tok0 + chunk(n + 1) * kT, min(kT, len - chunk(n + 1) * kT), H, h, lane);
-            if (n >= 2 && !wait_or_abort(&bars[kSGEmpty + (n & 1)], half_par(n) ^ 1u, ab)) break;
-            make_gates(&gates[n & 1], x, lane);
-            warp_arrive(&bars[kSGFull + (n & 1)], lane);
+            if (n >= kStGateBufs &&
+                !wait_or_abort(&bars[kSGEmpty + n % kStGateBufs], ((uint32_t)(n / kStGateBufs) & 1u) ^ 1u, ab))
+                break;
+            whole += make_weights(&gates[n % kStGateBufs], x, REV, lane);
+            warp_arrive(&bars[kSGFull + n % kStGateBufs], lane);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                whole += (double)x[u];
-                x[u] = y[u];
-            }
+            for (int u = 0; u < 4; ++u) x[u] = y[u];
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, off);
-        if (lane == 0 && A.seg_end) A.seg_gam[(size_t)seg * H + h] = ex2_approx((float)(whole * 1.4426950408889634074));
+        if (lane == 0 && A.seg_end) A.seg_gam[(size_t)seg * H + h] = ex2_approx(from_fixed(whole));
     }
     __syncwarp();
     tc_fence_before();
@@ -641,8 +666,9 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
                               void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
                               int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
                               float* seg_gam, int* err, cudaStream_t s) {
-    CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H))
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
+        !make_map(&mo, o, tokens, H, BV / 2, 32))
         return cudaErrorNotSupported;
     cudaError_t e;
     if (split) {
@@ -656,7 +682,7 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     auto kern = BV == 128 ? lin_walk<128> : lin_walk<64>;
     if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
     kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
-        mq, mk, mv, dec, segs, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
+        mq, mk, mv, mo, dec, segs, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
     return cudaGetLastError();
 }
 
