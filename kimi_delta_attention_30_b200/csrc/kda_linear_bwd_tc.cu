@@ -129,7 +129,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     if (warp < 16) {   // ---- elementwise
         const int R = warp & 3, B = warp >> 2, row = 32 * R + lane;
         const uint32_t at = ((uint32_t)(32 * R) << 16) + 32 * B;   // this warp's lanes and columns
-        int it = 0;
+        int it = 0, tails = 0;   // units so far, and those with rows to clear
         for (int u = first; u < n_units; u += step, ++it) {
             const uint32_t par = (uint32_t)it & 1u;
             int seq, tok0, len, idx;
@@ -145,9 +145,9 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 zero_rows(slot(kK), 2, len, tid, 512);
                 zero_rows(slot(kDO), 2, len, tid, 512);
                 fence_async_smem();
+                warp_arrive(&bars[kClean], lane);
+                if (!wait_or_abort(&bars[kClean], (uint32_t)tails++ & 1u, ab)) break;
             }
-            warp_arrive(&bars[kClean], lane);
-            if (len < kT && !wait_or_abort(&bars[kClean], par, ab)) break;
             if (!wait_or_abort(&bars[kSumsEmpty], par ^ 1u, ab)) break;   // the last unit's sums are read
             const float r2 = G.rel2[row], er = ex2_approx(r2), wq = er * G.start[R], wk = G.col[row] * G.end[R];
             // the states' parts of dQ and dK: scaled where they stand, and their dots
@@ -333,13 +333,15 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         auto ktile = [&](int i) { return sw128_desc(base + (uint32_t)i * kTile); };
         auto mtile = [&](int i) { return mn_desc_k(base + (uint32_t)i * kTile, kT, 0); };
         bool ok = true;
-        int it = 0;
+        int it = 0, tails = 0;
         for (int u = first; u < n_units; u += step, ++it) {
             const uint32_t par = (uint32_t)it & 1u;
+            int seq, tok0, len, idx;
+            chunks.locate(u / H, seq, tok0, len, idx);
             // (each accumulator once the last unit's result has been read from it)
             if (it > 0 && !(ok = wait_or_abort(&bars[kRead + 1], par ^ 1u, ab))) break;
             if (!(ok = wait_or_abort(&bars[kFull + kDO], par, ab) && wait_or_abort(&bars[kFull + kS], par, ab) &&
-                       wait_or_abort(&bars[kClean], par, ab)))
+                       (len == kT || wait_or_abort(&bars[kClean], (uint32_t)tails++ & 1u, ab))))
                 break;
             tc_fence_after();
             product<false, false>(tQ, ktile(kDO), ktile(kS), iKK, false, lead);
