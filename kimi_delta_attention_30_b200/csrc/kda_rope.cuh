@@ -21,14 +21,14 @@ struct NormRopeArgs {
     long long T;
     int Hq, Hk, rot;
     float eps;
-    int groups;                 // forward: warps that share a token's heads
+    int groups, per;            // warps that share a token's heads, and heads each
 };
 
-int norm_rope_bwd_blocks(long long T);
+int norm_rope_bwd_blocks();
 cudaError_t launch_norm_rope(kda_dtype dtype, kda_dtype wdtype, NormRopeArgs A, int d, bool interleaved,
                              cudaStream_t stream);
-// partial: fp32 [norm_rope_bwd_blocks(T)][2][d]
-cudaError_t launch_norm_rope_bwd(kda_dtype dtype, kda_dtype wdtype, const NormRopeArgs& A, int d, bool interleaved,
+// partial: fp32 [norm_rope_bwd_blocks()][2][d]
+cudaError_t launch_norm_rope_bwd(kda_dtype dtype, kda_dtype wdtype, NormRopeArgs A, int d, bool interleaved,
                                  float* partial, void* dwq, void* dwk, cudaStream_t stream);
 
 }  // namespace kda

@@ -86,7 +86,7 @@ kda_status kda_qk_norm_rope(const kda_rows* q, const kda_rows* k, const void* q_
 
 size_t kda_qk_norm_rope_bwd_workspace_size(long long T, int Hq, int Hk, int d, int rot) {
     if (check_sizes(KDA_F32, KDA_F32, T, Hq, Hk, d, rot, 0.f) != KDA_OK) return 0;
-    return align_up((size_t)(T > 0 ? norm_rope_bwd_blocks(T) : 1) * 2 * d * sizeof(float));
+    return align_up((size_t)norm_rope_bwd_blocks() * 2 * d * sizeof(float));
 }
 
 kda_status kda_qk_norm_rope_bwd(const kda_rows* q, const kda_rows* k, const void* q_weight, const void* k_weight,
@@ -128,7 +128,6 @@ kda_status kda_qk_norm_rope_bwd(const kda_rows* q, const kda_rows* k, const void
     A.Hk = Hk;
     A.rot = rot;
     A.eps = eps;
-    A.groups = 1;
     return launch_norm_rope_bwd(dtype, weight_dtype, A, d, interleaved != 0, (float*)workspace, dq_weight, dk_weight,
                                 (cudaStream_t)stream) == cudaSuccess
                ? KDA_OK
