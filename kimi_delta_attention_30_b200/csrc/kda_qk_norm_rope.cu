@@ -106,10 +106,10 @@ struct Freq {
     }
 };
 
-// cos and sin of the lane's eight pairs; (1, 0) where the lane does not rotate
+// cos and sin of the token's pairs, for the warp
 template <int D>
-__device__ __forceinline__ void rotations(const NormRopeArgs& A, int position, const Freq<D>& F, const Lane& L, int lane,
-                                          float2* cs, float2 (&co)[4], float2 (&si)[4]) {
+__device__ __forceinline__ void rotations(const NormRopeArgs& A, int position, const Freq<D>& F, int lane, float2* cs) {
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < Freq<D>::N; ++i) {
         if (lane + 32 * i < A.rot / 2) {
@@ -120,18 +120,16 @@ __device__ __forceinline__ void rotations(const NormRopeArgs& A, int position, c
         }
     }
     __syncwarp();
+}
+
+// those of the lane's eight pairs; (1, 0) where the lane does not rotate
+__device__ __forceinline__ void lane_rotation(const float2* cs, const Lane& L, float2 (&co)[4], float2 (&si)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (L.turns) {
-            const float4 x = *reinterpret_cast<const float4*>(&cs[L.pair + 2 * i]);
-            co[i] = make_float2(x.x, x.z);
-            si[i] = make_float2(x.y, x.w);
-        } else {
-            co[i] = make_float2(1.f, 1.f);
-            si[i] = make_float2(0.f, 0.f);
-        }
+        const float4 x = L.turns ? *reinterpret_cast<const float4*>(&cs[L.pair + 2 * i]) : make_float4(1.f, 0.f, 1.f, 0.f);
+        co[i] = make_float2(x.x, x.z);
+        si[i] = make_float2(x.y, x.w);
     }
-    __syncwarp();
 }
 
 // sum over the lanes that share a row
@@ -185,46 +183,93 @@ __device__ __forceinline__ void unsort_pairs(float2 (&a)[4], float2 (&b)[4]) {
     }
 }
 
+// A warp's steps in order: its (token, part of the heads) pairs, queries before keys, ROWS
+// heads at a time.  The loads of the next step, whatever token it belongs to, stand before
+// the current step's arithmetic.
+struct Walk {
+    long long tok, tok_step;
+    int grp, grp_step, side, h, e;   // heads h .. h + ROWS - 1 of the side, below e
+    bool new_tok, new_side;
+
+    __device__ __forceinline__ bool enter(const NormRopeArgs& A) {   // the first step of the current pair
+        if (tok >= A.T) return false;
+        const int h0 = grp * A.per, h1 = min(A.Hq + A.Hk, h0 + A.per);
+        side = h0 < A.Hq ? 0 : 1;
+        h = side ? h0 - A.Hq : h0;
+        e = side ? h1 - A.Hq : min(h1, A.Hq);
+        new_tok = new_side = true;
+        return true;
+    }
+    __device__ __forceinline__ bool start(const NormRopeArgs& A, long long first, long long step) {
+        tok = first / A.groups;
+        grp = (int)(first - tok * A.groups);
+        tok_step = step / A.groups;
+        grp_step = (int)(step - tok_step * A.groups);
+        return enter(A);
+    }
+    template <int ROWS>
+    __device__ __forceinline__ bool next(const NormRopeArgs& A) {
+        new_tok = new_side = false;
+        h += ROWS;
+        if (h < e) return true;
+        const int h1 = min(A.Hq + A.Hk, grp * A.per + A.per);
+        if (side == 0 && h1 > A.Hq) {
+            side = 1;
+            h = 0;
+            e = h1 - A.Hq;
+            new_side = true;
+            return true;
+        }
+        tok += tok_step;
+        grp += grp_step;
+        if (grp >= A.groups) {
+            grp -= A.groups;
+            ++tok;
+        }
+        return enter(A);
+    }
+};
+
 template <typename Tin, typename Tw, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd(const __grid_constant__ NormRopeArgs A) {
+__global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_fwd(const __grid_constant__ NormRopeArgs A) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;   // lanes a row, rows a warp at a time
     __shared__ __align__(16) float2 cs[kWarps][D / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
     const Lane L = lane_of(l, A.rot, INTER);
+    Walk W;
+    bool more = W.start(A, (long long)blockIdx.x * kWarps + warp, (long long)gridDim.x * kWarps);
+    if (!more) return;
+    Raw8<Tin> ra, rb;
+    int position = 0;
+    auto load = [&]() {
+        const NormRopeSide& X = W.side ? A.k : A.q;
+        const Tin* p = reinterpret_cast<const Tin*>(X.in) + W.tok * X.in_tok + (long long)min(W.h + sub, W.e - 1) * X.in_head;
+        ra.load(p + L.c0);
+        rb.load(p + L.c1);
+        if (W.new_tok && A.rot > 0) position = A.positions[W.tok];
+    };
+    load();
     Freq<D> F;
     F.load(A, lane);
-    const int heads = A.Hq + A.Hk;
-    const long long tasks = A.T * A.groups, step = (long long)gridDim.x * kWarps;
-    for (long long task = (long long)blockIdx.x * kWarps + warp; task < tasks; task += step) {
-        const long long tok = task / A.groups;
-        const int h0 = (int)(task - tok * A.groups) * A.per, h1 = min(heads, h0 + A.per);
-        const int position = A.rot > 0 ? A.positions[tok] : 0;
-        float2 co[4], si[4];
-        bool turned = false;
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {   // queries, then keys
-            const int base = side ? A.Hq : 0;
-            const int b = (side ? max(h0, A.Hq) : h0) - base, e = (side ? h1 : min(h1, A.Hq)) - base;
-            if (b >= e) continue;
-            const NormRopeSide& X = side ? A.k : A.q;
-            const Tin* in = reinterpret_cast<const Tin*>(X.in) + tok * X.in_tok;
-            Tin* out = reinterpret_cast<Tin*>(X.out) + tok * X.out_tok;
-            Raw8<Tin> ra, rb;
-            auto load = [&](int h) {
-                const Tin* p = in + (long long)min(h + sub, e - 1) * X.in_head;
-                ra.load(p + L.c0);
-                rb.load(p + L.c1);
-            };
-            load(b);
-            if (!turned) {
-                rotations<D>(A, position, F, L, lane, cs[warp], co, si);
-                turned = true;
-            }
-            // the rotation of the weighted row: a' = ca a - sb b, b' = cb b + sa a
-            float2 w0[4], w1[4], ca[4], cb[4], sa[4], sb[4];
-            weights8<Tw>(X.w, L.c0, w0);
-            weights8<Tw>(X.w, L.c1, w1);
+    float2 ca[4], cb[4], sa[4], sb[4];   // the rotation of the weighted row: a' = ca a + sb b, b' = cb b + sa a
+    while (more) {
+        float2 x[4], y[4];
+        ra.get(x);
+        rb.get(y);
+        const bool live = W.h + sub < W.e, new_tok = W.new_tok, new_side = W.new_side;
+        const int pos = position;
+        const NormRopeSide& X = W.side ? A.k : A.q;
+        Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
+        const void* weight = X.w;
+        more = W.next<ROWS>(A);
+        if (more) load();
+        if (new_tok) rotations<D>(A, pos, F, lane, cs[warp]);
+        if (new_side) {
+            float2 w0[4], w1[4], co[4], si[4];
+            weights8<Tw>(weight, L.c0, w0);
+            weights8<Tw>(weight, L.c1, w1);
             sort_pairs<INTER>(w0, w1);
+            lane_rotation(cs[warp], L, co, si);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ca[i] = mul2(co[i], w0[i]);
@@ -232,30 +277,23 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd(const __grid_constant_
                 sa[i] = mul2(si[i], w0[i]);
                 sb[i] = neg2(mul2(si[i], w1[i]));
             }
-            for (int h = b; h < e; h += ROWS) {
-                float2 x[4], y[4];
-                ra.get(x);
-                rb.get(y);
-                if (h + ROWS < e) load(h + ROWS);
-                sort_pairs<INTER>(x, y);
-                float2 ss = make_float2(0.f, 0.f);
+        }
+        sort_pairs<INTER>(x, y);
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ss = fma2(x[i], x[i], fma2(y[i], y[i], ss));
-                const float r1 = rms_scale(row_sum<LANES>(ss.x + ss.y), D, A.eps);
-                const float2 r = make_float2(r1, r1);
-                float2 u[4], v[4];
+        for (int i = 0; i < 4; ++i) ss = fma2(x[i], x[i], fma2(y[i], y[i], ss));
+        const float r1 = rms_scale(row_sum<LANES>(ss.x + ss.y), D, A.eps);
+        const float2 r = make_float2(r1, r1);
+        float2 u[4], v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u[i] = mul2(fma2(ca[i], x[i], mul2(sb[i], y[i])), r);
-                    v[i] = mul2(fma2(cb[i], y[i], mul2(sa[i], x[i])), r);
-                }
-                unsort_pairs<INTER>(u, v);
-                if (h + sub < e) {
-                    Tin* d = out + (long long)(h + sub) * X.out_head;
-                    store8(d + L.c0, u);
-                    store8(d + L.c1, v);
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            u[i] = mul2(fma2(ca[i], x[i], mul2(sb[i], y[i])), r);
+            v[i] = mul2(fma2(cb[i], y[i], mul2(sa[i], x[i])), r);
+        }
+        unsort_pairs<INTER>(u, v);
+        if (live) {
+            store8(d + L.c0, u);
+            store8(d + L.c1, v);
         }
     }
 }
@@ -263,109 +301,117 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd(const __grid_constant_
 // Backward: the weight gradients are summed in registers over a lane's rows, then over the
 // block in a fixed order, and written as one partial row per block ([grid][2][D] fp32); the
 // second kernel adds the partial rows in order, so the result does not depend on timing.
+// dw: sum over rows of (rotated gradient) x r; a lane sums one side at a time and adds it to
+// the side's shared-memory row of its own at the end of the side's steps of a token.
 template <typename Tin, typename Tw, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd(const __grid_constant__ NormRopeArgs A,
-                                                          float* __restrict__ partial) {
+__global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_bwd(const __grid_constant__ NormRopeArgs A,
+                                                                                   float* __restrict__ partial) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;
     __shared__ __align__(16) float2 cs[kWarps][D / 2];
-    __shared__ __align__(16) float acc[kWarps * ROWS][D];
+    __shared__ __align__(16) float acc[2][kWarps * ROWS][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
     const Lane L = lane_of(l, A.rot, INTER);
+    float2 g0[4], g1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g0[i] = g1[i] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        store8(&acc[side][warp * ROWS + sub][L.c0], g0);
+        store8(&acc[side][warp * ROWS + sub][L.c1], g1);
+    }
+    Walk W;
+    bool more = W.start(A, (long long)blockIdx.x * kWarps + warp, (long long)gridDim.x * kWarps);
+    Raw8<Tin> ra, rb, da, db;
+    int position = 0;
+    auto load = [&]() {
+        const NormRopeSide& X = W.side ? A.k : A.q;
+        const int hh = min(W.h + sub, W.e - 1);
+        const Tin* p = reinterpret_cast<const Tin*>(X.in) + W.tok * X.in_tok + (long long)hh * X.in_head;
+        const Tin* q = reinterpret_cast<const Tin*>(X.dy) + W.tok * X.dy_tok + (long long)hh * X.dy_head;
+        ra.load(p + L.c0);
+        rb.load(p + L.c1);
+        da.load(q + L.c0);
+        db.load(q + L.c1);
+        if (W.new_tok && A.rot > 0) position = A.positions[W.tok];
+    };
+    if (more) load();
     Freq<D> F;
     F.load(A, lane);
-    float2 g0[2][4], g1[2][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) g0[0][i] = g0[1][i] = g1[0][i] = g1[1][i] = make_float2(0.f, 0.f);
-    const int heads = A.Hq + A.Hk;
-    const long long tasks = A.T * A.groups, step = (long long)gridDim.x * kWarps;
-    for (long long task = (long long)blockIdx.x * kWarps + warp; task < tasks; task += step) {
-        const long long tok = task / A.groups;
-        const int h0 = (int)(task - tok * A.groups) * A.per, h1 = min(heads, h0 + A.per);
-        const int position = A.rot > 0 ? A.positions[tok] : 0;
-        float2 co[4], si[4];
-        bool turned = false;
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int base = side ? A.Hq : 0;
-            const int b = (side ? max(h0, A.Hq) : h0) - base, e = (side ? h1 : min(h1, A.Hq)) - base;
-            if (b >= e) continue;
-            const NormRopeSide& X = side ? A.k : A.q;
-            const Tin* in = reinterpret_cast<const Tin*>(X.in) + tok * X.in_tok;
-            const Tin* dy = reinterpret_cast<const Tin*>(X.dy) + tok * X.dy_tok;
-            Tin* out = reinterpret_cast<Tin*>(X.out) + tok * X.out_tok;
-            Raw8<Tin> ra, rb, da, db;
-            auto load = [&](int h) {
-                const int hh = min(h + sub, e - 1);
-                const Tin *p = in + (long long)hh * X.in_head, *q = dy + (long long)hh * X.dy_head;
-                ra.load(p + L.c0);
-                rb.load(p + L.c1);
-                da.load(q + L.c0);
-                db.load(q + L.c1);
-            };
-            load(b);
-            if (!turned) {
-                rotations<D>(A, position, F, L, lane, cs[warp], co, si);
-                turned = true;
-            }
-            float2 w0[4], w1[4];
-            weights8<Tw>(X.w, L.c0, w0);
-            weights8<Tw>(X.w, L.c1, w1);
+    float2 co[4], si[4], w0[4], w1[4];
+    while (more) {
+        float2 x[4], y[4], u[4], v[4];
+        ra.get(x);
+        rb.get(y);
+        da.get(u);
+        db.get(v);
+        const bool live = W.h + sub < W.e, new_tok = W.new_tok, new_side = W.new_side;
+        const int pos = position, side = W.side;
+        const NormRopeSide& X = side ? A.k : A.q;
+        Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
+        const void* weight = X.w;
+        more = W.next<ROWS>(A);
+        if (more) load();
+        if (new_tok) rotations<D>(A, pos, F, lane, cs[warp]);
+        if (new_side) {
+            weights8<Tw>(weight, L.c0, w0);
+            weights8<Tw>(weight, L.c1, w1);
             sort_pairs<INTER>(w0, w1);
-#pragma unroll 1
-            for (int h = b; h < e; h += ROWS) {
-                float2 x[4], y[4], u[4], v[4];
-                ra.get(x);
-                rb.get(y);
-                da.get(u);
-                db.get(v);
-                if (h + ROWS < e) load(h + ROWS);
-                sort_pairs<INTER>(x, y);
-                sort_pairs<INTER>(u, v);
-                float2 ss = make_float2(0.f, 0.f), hx = ss;
+            lane_rotation(cs[warp], L, co, si);
+        }
+        sort_pairs<INTER>(x, y);
+        sort_pairs<INTER>(u, v);
+        float2 ss = make_float2(0.f, 0.f), hx = ss;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {   // the gradient turns back
-                    const float2 g = fma2(co[i], u[i], mul2(si[i], v[i]));
-                    v[i] = fma2(co[i], v[i], neg2(mul2(si[i], u[i])));
-                    u[i] = g;
-                    ss = fma2(x[i], x[i], fma2(y[i], y[i], ss));
-                    hx = fma2(mul2(u[i], w0[i]), x[i], fma2(mul2(v[i], w1[i]), y[i], hx));
-                }
-                const bool live = h + sub < e;
-                const float r1 = rms_scale(row_sum<LANES>(ss.x + ss.y), D, A.eps);
-                const float m1 = -row_sum<LANES>(hx.x + hx.y) * r1 * r1 * (1.f / D);
-                const float2 r = make_float2(r1, r1), m = make_float2(m1, m1);
-                const float2 rl = live ? r : make_float2(0.f, 0.f);
+        for (int i = 0; i < 4; ++i) {   // the gradient turns back
+            const float2 g = fma2(co[i], u[i], mul2(si[i], v[i]));
+            v[i] = fma2(co[i], v[i], neg2(mul2(si[i], u[i])));
+            u[i] = g;
+            ss = fma2(x[i], x[i], fma2(y[i], y[i], ss));
+            hx = fma2(mul2(u[i], w0[i]), x[i], fma2(mul2(v[i], w1[i]), y[i], hx));
+        }
+        const float r1 = rms_scale(row_sum<LANES>(ss.x + ss.y), D, A.eps);
+        const float m1 = -row_sum<LANES>(hx.x + hx.y) * r1 * r1 * (1.f / D);
+        const float2 r = make_float2(r1, r1), m = make_float2(m1, m1);
+        const float2 rl = live ? r : make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 xr = mul2(x[i], rl), yr = mul2(y[i], rl);
-                    g0[side][i] = fma2(u[i], xr, g0[side][i]);
-                    g1[side][i] = fma2(v[i], yr, g1[side][i]);
-                    u[i] = fma2(mul2(u[i], w0[i]), r, mul2(xr, m));
-                    v[i] = fma2(mul2(v[i], w1[i]), r, mul2(yr, m));
-                }
-                unsort_pairs<INTER>(u, v);
-                if (live) {
-                    Tin* d = out + (long long)(h + sub) * X.out_head;
-                    store8(d + L.c0, u);
-                    store8(d + L.c1, v);
-                }
+        for (int i = 0; i < 4; ++i) {
+            const float2 xr = mul2(x[i], rl), yr = mul2(y[i], rl);
+            g0[i] = fma2(u[i], xr, g0[i]);
+            g1[i] = fma2(v[i], yr, g1[i]);
+            u[i] = fma2(mul2(u[i], w0[i]), r, mul2(xr, m));
+            v[i] = fma2(mul2(v[i], w1[i]), r, mul2(yr, m));
+        }
+        unsort_pairs<INTER>(u, v);
+        if (live) {
+            store8(d + L.c0, u);
+            store8(d + L.c1, v);
+        }
+        if (!more || W.new_side) {   // the side's last step
+            float4* s0 = reinterpret_cast<float4*>(&acc[side][warp * ROWS + sub][L.c0]);
+            float4* s1 = reinterpret_cast<float4*>(&acc[side][warp * ROWS + sub][L.c1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 p = s0[i], q = s1[i];
+                s0[i] = make_float4(p.x + g0[2 * i].x, p.y + g0[2 * i].y, p.z + g0[2 * i + 1].x, p.w + g0[2 * i + 1].y);
+                s1[i] = make_float4(q.x + g1[2 * i].x, q.y + g1[2 * i].y, q.z + g1[2 * i + 1].x, q.w + g1[2 * i + 1].y);
+                g0[2 * i] = g0[2 * i + 1] = g1[2 * i] = g1[2 * i + 1] = make_float2(0.f, 0.f);
             }
         }
     }
     if (partial == nullptr) return;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        unsort_pairs<INTER>(g0[side], g1[side]);
-        __syncthreads();
-        store8(&acc[warp * ROWS + sub][L.c0], g0[side]);
-        store8(&acc[warp * ROWS + sub][L.c1], g1[side]);
-        __syncthreads();
-        for (int c = threadIdx.x; c < D; c += kThreads) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < kWarps * ROWS; ++i) s += acc[i][c];
-            partial[((size_t)blockIdx.x * 2 + side) * D + c] = s;
+    // a neighbour rotation's sums stand sorted: channel 2 i of vector p at p's i-th half, 2 i + 1 at the other's
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+        const int side = c / D, ch = c % D;
+        int at = ch;
+        if (INTER) {
+            const int p = ch / 16, k = ch % 16;                  // lane p holds channels 16 p .. 16 p + 15
+            at = 16 * p + (k & 1) * 8 + k / 2;                   // evens of both vectors, then odds
         }
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps * ROWS; ++i) s += acc[side][i][at];
+        partial[((size_t)blockIdx.x * 2 + side) * D + ch] = s;
     }
 }
 
@@ -434,7 +480,7 @@ void split_heads(NormRopeArgs& A, int d, int warps) {
     A.groups = (heads + A.per - 1) / A.per;
 }
 
-constexpr int kFwdBlocks = 148 * 8, kBwdBlocks = 148 * 4;
+constexpr int kFwdBlocks = 148 * 5, kBwdBlocks = 148 * 4;   // what fits at once
 
 }  // namespace
 
