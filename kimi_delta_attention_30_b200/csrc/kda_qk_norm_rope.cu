@@ -12,8 +12,9 @@
 // (or a part of them when there are few tokens), four or eight rows at a time: d / 16 lanes
 // share a row, and a lane holds the two 8-channel vectors that rotate with each other
 // (halves: vectors p and p + rot / 16; neighbours: vectors 2 p and 2 p + 1), so a rotation
-// needs no exchange between lanes and loads are 16 bytes.  The next rows' loads stand before
-// the current rows' arithmetic.
+// needs no exchange between lanes and loads are 16 bytes.  Loads run several steps ahead,
+// across tokens and sides, through shared memory (asynchronous copies that the lane which
+// made them reads).
 //
 // The rotations of a token are formed once, two pairs a lane, and exchanged through shared
 // memory.  Angles are taken in turns in 64-bit fixed point: with f = inv_freq / (2 pi) as a
@@ -33,31 +34,43 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
-// Eight channels as they stand in memory.
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(float2 (&x)[4]) const {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// Eight channels as they stand in memory: 16-byte pieces, copied asynchronously into shared
+// memory by the lane that will read them (so a step needs no barrier), `pitch` bytes apart.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T> constexpr int pieces8() { return 8 * (int)sizeof(T) / 16; }
+constexpr int kPiece = 32 * 16;   // one 16-byte piece of every lane
+
+template <typename T>
+__device__ __forceinline__ void copy8(uint32_t dst, const T* src) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-    }
-};
-template <> struct Raw8<float> {
-    float4 v[2];
-    __device__ __forceinline__ void load(const float* p) {
-        v[0] = reinterpret_cast<const float4*>(p)[0];
-        v[1] = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void get(float2 (&x)[4]) const {
+    for (int i = 0; i < pieces8<T>(); ++i) copy16(dst + i * kPiece, src + i * (16 / (int)sizeof(T)));
+}
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[2 * i] = make_float2(v[i].x, v[i].y);
-            x[2 * i + 1] = make_float2(v[i].z, v[i].w);
-        }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ void get8(const uint8_t* src, float2 (&x)[4]) {
+    if constexpr (sizeof(T) == 2) {
+        unpack8(*reinterpret_cast<const uint4*>(src), x);
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + kPiece);
+        x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
     }
-};
+}
 __device__ __forceinline__ void store8(float* p, const float2 (&x)[4]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
@@ -150,9 +163,14 @@ __device__ __forceinline__ void weights8(const void* w, int c, float2 (&x)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = make_float2(1.f, 1.f);
     } else {
-        Raw8<Tw> r;
-        r.load(reinterpret_cast<const Tw*>(w) + c);
-        r.get(x);
+        const Tw* p = reinterpret_cast<const Tw*>(w) + c;
+        if constexpr (sizeof(Tw) == 2) {
+            unpack8(*reinterpret_cast<const uint4*>(p), x);
+        } else {
+            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+            x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+            x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
+        }
     }
 }
 
@@ -184,8 +202,7 @@ __device__ __forceinline__ void unsort_pairs(float2 (&a)[4], float2 (&b)[4]) {
 }
 
 // A warp's steps in order: its (token, part of the heads) pairs, queries before keys, ROWS
-// heads at a time.  The loads of the next step, whatever token it belongs to, stand before
-// the current step's arithmetic.
+// heads at a time.
 struct Walk {
     long long tok, tok_step;
     int grp, grp_step, side, h, e;   // heads h .. h + ROWS - 1 of the side, below e
@@ -230,46 +247,61 @@ struct Walk {
     }
 };
 
+// Steps in flight, the current one among them.
+template <typename Tin> constexpr int kDepth() { return sizeof(Tin) == 2 ? 5 : 4; }
+constexpr int kPos = 16;   // bytes behind a stage's pieces: the token's position
+
+template <typename Tin, int VECS> constexpr int stage_bytes() { return VECS * pieces8<Tin>() * kPiece + kPos; }
+
 template <typename Tin, typename Tw, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_fwd(const __grid_constant__ NormRopeArgs A) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;   // lanes a row, rows a warp at a time
-    __shared__ __align__(16) float2 cs[kWarps][D / 2];
+    constexpr int DEPTH = kDepth<Tin>(), BYTES = stage_bytes<Tin, 2>(), VEC = pieces8<Tin>() * kPiece;
+    extern __shared__ __align__(16) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+    uint8_t* stages = sm + warp * (DEPTH * BYTES + D / 2 * 8);
+    float2* cs = reinterpret_cast<float2*>(stages + DEPTH * BYTES);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(stages) + lane * 16;
     const Lane L = lane_of(l, A.rot, INTER);
-    Walk W;
+    Walk W, ahead;
     bool more = W.start(A, (long long)blockIdx.x * kWarps + warp, (long long)gridDim.x * kWarps);
     if (!more) return;
-    Raw8<Tin> ra, rb;
-    int position = 0;
-    auto load = [&]() {
-        const NormRopeSide& X = W.side ? A.k : A.q;
-        const Tin* p = reinterpret_cast<const Tin*>(X.in) + W.tok * X.in_tok + (long long)min(W.h + sub, W.e - 1) * X.in_head;
-        ra.load(p + L.c0);
-        rb.load(p + L.c1);
-        if (W.new_tok && A.rot > 0) position = A.positions[W.tok];
+    ahead = W;
+    bool any = true;
+    auto load = [&](int s) {   // the steps ahead into stage s, one group a step (empty behind the last)
+        if (any) {
+            const NormRopeSide& X = ahead.side ? A.k : A.q;
+            const Tin* p = reinterpret_cast<const Tin*>(X.in) + ahead.tok * X.in_tok +
+                           (long long)min(ahead.h + sub, ahead.e - 1) * X.in_head;
+            copy8(to + s * BYTES, p + L.c0);
+            copy8(to + s * BYTES + VEC, p + L.c1);
+            if (ahead.new_tok && A.rot > 0) copy4(to + s * BYTES + 2 * VEC - lane * 16, A.positions + ahead.tok);
+            any = ahead.next<ROWS>(A);
+        }
+        copies_done();
     };
-    load();
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) load(s);
     Freq<D> F;
     F.load(A, lane);
     float2 ca[4], cb[4], sa[4], sb[4];   // the rotation of the weighted row: a' = ca a + sb b, b' = cb b + sa a
+    int stage = 0;
     while (more) {
+        wait_copies<DEPTH - 2>();
+        const uint8_t* from = stages + stage * BYTES;
         float2 x[4], y[4];
-        ra.get(x);
-        rb.get(y);
-        const bool live = W.h + sub < W.e, new_tok = W.new_tok, new_side = W.new_side;
-        const int pos = position;
+        get8<Tin>(from + lane * 16, x);
+        get8<Tin>(from + VEC + lane * 16, y);
         const NormRopeSide& X = W.side ? A.k : A.q;
-        Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
-        const void* weight = X.w;
-        more = W.next<ROWS>(A);
-        if (more) load();
-        if (new_tok) rotations<D>(A, pos, F, lane, cs[warp]);
-        if (new_side) {
+        if (W.new_tok) rotations<D>(A, *reinterpret_cast<const int*>(from + 2 * VEC), F, lane, cs);
+        load(stage == 0 ? DEPTH - 1 : stage - 1);   // the stage before this one: read a step ago
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
+        if (W.new_side) {
             float2 w0[4], w1[4], co[4], si[4];
-            weights8<Tw>(weight, L.c0, w0);
-            weights8<Tw>(weight, L.c1, w1);
+            weights8<Tw>(X.w, L.c0, w0);
+            weights8<Tw>(X.w, L.c1, w1);
             sort_pairs<INTER>(w0, w1);
-            lane_rotation(cs[warp], L, co, si);
+            lane_rotation(cs, L, co, si);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ca[i] = mul2(co[i], w0[i]);
@@ -291,10 +323,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_
             v[i] = mul2(fma2(cb[i], y[i], mul2(sa[i], x[i])), r);
         }
         unsort_pairs<INTER>(u, v);
-        if (live) {
+        if (W.h + sub < W.e) {
+            Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
             store8(d + L.c0, u);
             store8(d + L.c1, v);
         }
+        more = W.next<ROWS>(A);
     }
 }
 
@@ -303,61 +337,74 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_
 // second kernel adds the partial rows in order, so the result does not depend on timing.
 // dw: sum over rows of (rotated gradient) x r; a lane sums one side at a time and adds it to
 // the side's shared-memory row of its own at the end of the side's steps of a token.
+template <typename Tin> constexpr int kBwdDepth() { return sizeof(Tin) == 2 ? 4 : 3; }
+
 template <typename Tin, typename Tw, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_bwd(const __grid_constant__ NormRopeArgs A,
                                                                                    float* __restrict__ partial) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;
-    __shared__ __align__(16) float2 cs[kWarps][D / 2];
-    __shared__ __align__(16) float acc[2][kWarps * ROWS][D];
+    constexpr int DEPTH = kBwdDepth<Tin>(), BYTES = stage_bytes<Tin, 4>(), VEC = pieces8<Tin>() * kPiece;
+    extern __shared__ __align__(16) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+    float* acc = reinterpret_cast<float*>(sm);   // [2][kWarps * ROWS][D]
+    uint8_t* stages = sm + 2 * kWarps * ROWS * D * 4 + warp * (DEPTH * BYTES + D / 2 * 8);
+    float2* cs = reinterpret_cast<float2*>(stages + DEPTH * BYTES);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(stages) + lane * 16;
     const Lane L = lane_of(l, A.rot, INTER);
+    auto mine = [&](int side) { return acc + ((side * kWarps + warp) * ROWS + sub) * D; };
     float2 g0[4], g1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) g0[i] = g1[i] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-        store8(&acc[side][warp * ROWS + sub][L.c0], g0);
-        store8(&acc[side][warp * ROWS + sub][L.c1], g1);
+        store8(mine(side) + L.c0, g0);
+        store8(mine(side) + L.c1, g1);
     }
-    Walk W;
+    Walk W, ahead;
     bool more = W.start(A, (long long)blockIdx.x * kWarps + warp, (long long)gridDim.x * kWarps);
-    Raw8<Tin> ra, rb, da, db;
-    int position = 0;
-    auto load = [&]() {
-        const NormRopeSide& X = W.side ? A.k : A.q;
-        const int hh = min(W.h + sub, W.e - 1);
-        const Tin* p = reinterpret_cast<const Tin*>(X.in) + W.tok * X.in_tok + (long long)hh * X.in_head;
-        const Tin* q = reinterpret_cast<const Tin*>(X.dy) + W.tok * X.dy_tok + (long long)hh * X.dy_head;
-        ra.load(p + L.c0);
-        rb.load(p + L.c1);
-        da.load(q + L.c0);
-        db.load(q + L.c1);
-        if (W.new_tok && A.rot > 0) position = A.positions[W.tok];
+    ahead = W;
+    bool any = more;
+    auto load = [&](int s) {
+        if (any) {
+            const NormRopeSide& X = ahead.side ? A.k : A.q;
+            const int hh = min(ahead.h + sub, ahead.e - 1);
+            const Tin* p = reinterpret_cast<const Tin*>(X.in) + ahead.tok * X.in_tok + (long long)hh * X.in_head;
+            const Tin* q = reinterpret_cast<const Tin*>(X.dy) + ahead.tok * X.dy_tok + (long long)hh * X.dy_head;
+            copy8(to + s * BYTES, p + L.c0);
+            copy8(to + s * BYTES + VEC, p + L.c1);
+            copy8(to + s * BYTES + 2 * VEC, q + L.c0);
+            copy8(to + s * BYTES + 3 * VEC, q + L.c1);
+            if (ahead.new_tok && A.rot > 0) copy4(to + s * BYTES + 4 * VEC - lane * 16, A.positions + ahead.tok);
+            any = ahead.next<ROWS>(A);
+        }
+        copies_done();
     };
-    if (more) load();
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) load(s);
     Freq<D> F;
     F.load(A, lane);
     float2 co[4], si[4], w0[4], w1[4];
+    int stage = 0;
     while (more) {
+        wait_copies<DEPTH - 2>();
+        const uint8_t* from = stages + stage * BYTES;
         float2 x[4], y[4], u[4], v[4];
-        ra.get(x);
-        rb.get(y);
-        da.get(u);
-        db.get(v);
-        const bool live = W.h + sub < W.e, new_tok = W.new_tok, new_side = W.new_side;
-        const int pos = position, side = W.side;
+        get8<Tin>(from + lane * 16, x);
+        get8<Tin>(from + VEC + lane * 16, y);
+        get8<Tin>(from + 2 * VEC + lane * 16, u);
+        get8<Tin>(from + 3 * VEC + lane * 16, v);
+        const int side = W.side;
         const NormRopeSide& X = side ? A.k : A.q;
-        Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
-        const void* weight = X.w;
-        more = W.next<ROWS>(A);
-        if (more) load();
-        if (new_tok) rotations<D>(A, pos, F, lane, cs[warp]);
-        if (new_side) {
-            weights8<Tw>(weight, L.c0, w0);
-            weights8<Tw>(weight, L.c1, w1);
+        if (W.new_tok) rotations<D>(A, *reinterpret_cast<const int*>(from + 4 * VEC), F, lane, cs);
+        load(stage == 0 ? DEPTH - 1 : stage - 1);
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
+        if (W.new_side) {
+            weights8<Tw>(X.w, L.c0, w0);
+            weights8<Tw>(X.w, L.c1, w1);
             sort_pairs<INTER>(w0, w1);
-            lane_rotation(cs[warp], L, co, si);
+            lane_rotation(cs, L, co, si);
         }
+        const bool live = W.h + sub < W.e;
         sort_pairs<INTER>(x, y);
         sort_pairs<INTER>(u, v);
         float2 ss = make_float2(0.f, 0.f), hx = ss;
@@ -383,12 +430,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_
         }
         unsort_pairs<INTER>(u, v);
         if (live) {
+            Tin* d = reinterpret_cast<Tin*>(X.out) + W.tok * X.out_tok + (long long)(W.h + sub) * X.out_head;
             store8(d + L.c0, u);
             store8(d + L.c1, v);
         }
+        more = W.next<ROWS>(A);
         if (!more || W.new_side) {   // the side's last step
-            float4* s0 = reinterpret_cast<float4*>(&acc[side][warp * ROWS + sub][L.c0]);
-            float4* s1 = reinterpret_cast<float4*>(&acc[side][warp * ROWS + sub][L.c1]);
+            float4 *s0 = reinterpret_cast<float4*>(mine(side) + L.c0), *s1 = reinterpret_cast<float4*>(mine(side) + L.c1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float4 p = s0[i], q = s1[i];
@@ -410,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_
         }
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps * ROWS; ++i) s += acc[side][i][at];
+        for (int i = 0; i < kWarps * ROWS; ++i) s += acc[(side * kWarps * ROWS + i) * D + at];
         partial[((size_t)blockIdx.x * 2 + side) * D + ch] = s;
     }
 }
@@ -438,13 +486,19 @@ __global__ void __launch_bounds__(1024) norm_rope_dw(const float* __restrict__ p
 template <typename Tin, typename Tw, int D>
 cudaError_t run(const NormRopeArgs& A, bool inter, bool bwd, float* partial, int blocks, void* dwq, void* dwk,
                 cudaStream_t s) {
+    constexpr int ROWS = 512 / D, CS = D / 2 * 8;
     if (!bwd) {
-        if (inter) norm_rope_fwd<Tin, Tw, D, true><<<blocks, kThreads, 0, s>>>(A);
-        else norm_rope_fwd<Tin, Tw, D, false><<<blocks, kThreads, 0, s>>>(A);
+        auto kern = inter ? norm_rope_fwd<Tin, Tw, D, true> : norm_rope_fwd<Tin, Tw, D, false>;
+        constexpr int smem = kWarps * (kDepth<Tin>() * stage_bytes<Tin, 2>() + CS);
+        static_assert(smem <= 48 * 1024, "the default limit");
+        kern<<<blocks, kThreads, smem, s>>>(A);
     } else {
         const bool dw = dwq != nullptr || dwk != nullptr;
-        if (inter) norm_rope_bwd<Tin, Tw, D, true><<<blocks, kThreads, 0, s>>>(A, dw ? partial : nullptr);
-        else norm_rope_bwd<Tin, Tw, D, false><<<blocks, kThreads, 0, s>>>(A, dw ? partial : nullptr);
+        auto kern = inter ? norm_rope_bwd<Tin, Tw, D, true> : norm_rope_bwd<Tin, Tw, D, false>;
+        constexpr int smem = 2 * kWarps * ROWS * D * 4 + kWarps * (kBwdDepth<Tin>() * stage_bytes<Tin, 4>() + CS);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<blocks, kThreads, smem, s>>>(A, dw ? partial : nullptr);
         if (dw) norm_rope_dw<Tw, D><<<dim3(D / 32, 2), 1024, 0, s>>>(partial, blocks, dwq, dwk);
     }
     return cudaGetLastError();
