@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 import threading
 
@@ -150,7 +151,7 @@ def lib():
         if _lib is None:
             try:
                 from . import build as _build
-                if _build._stale():
+                if _build._stale() or _build._binding_stale():
                     _build.build()
             except Exception as exc:  # noqa: BLE001 - report any build problem
                 if not os.path.exists(LIB_PATH):
@@ -656,91 +657,32 @@ def decode_step(q, k, v, log_alpha, beta, state, o=None, stream=None, prep: int 
 DECAY_TOKEN, DECAY_HEAD = 0, 1
 
 # The calls below are short on the GPU (a decode step of one sequence takes 3 us), so their
-# marshalling avoids what costs microseconds on the host: context managers, stream and
-# device objects, ctypes wrappers around integers.
+# tensors are marshalled by a compiled module (csrc/torch_binding.cpp) instead of ctypes: the
+# same checks in Python took 6 to 28 us a call.
+_torch_binding = None
 
 
-def _need(name, t, dtype, shape, dev):
-    """A contiguous CUDA tensor of this dtype, shape and device index, or None."""
-    if t is None:
-        return None
-    if t.get_device() != dev or not t.is_cuda:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _binding():
+    global _torch_binding
+    if _torch_binding is None:
+        lib()                                   # builds both when stale; the module links libkda.so
+        try:
+            mod = importlib.import_module("._torch_binding", __name__)
+        except ImportError as exc:
+            raise RuntimeError(f"cannot load _torch_binding.so: {exc}") from exc
+        mod.set_errors(KdaError, torch.OutOfMemoryError)
+        _torch_binding = mod
+    return _torch_binding
 
 
-def _device_of(name, t, dtypes=_DTYPES):
-    if t.dtype not in dtypes:
-        raise ValueError(f"unsupported dtype {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    return t.get_device()
+def _offsets(cu_seqlens):
+    if cu_seqlens is None or type(cu_seqlens) in (list, tuple):
+        return cu_seqlens
+    return np.asarray(cu_seqlens).tolist()
 
 
-class _On:
-    """The device and stream of one call: ``raw`` is the stream's handle; tensors
-    allocated by the wrapper are recorded on a stream that is not the device's
-    current one."""
-    __slots__ = ("dev", "stream", "raw")
-
-    def __init__(self, dev, stream):
-        self.dev = dev
-        cur = torch._C._cuda_getCurrentRawStream(dev)
-        if stream is None or stream.cuda_stream == cur:
-            if stream is not None and stream.device.index != dev:
-                raise ValueError(f"stream belongs to {stream.device}, the call runs on cuda:{dev}")
-            self.raw, self.stream = cur, None
-        else:
-            if stream.device.index != dev:
-                raise ValueError(f"stream belongs to {stream.device}, the call runs on cuda:{dev}")
-            self.raw, self.stream = stream.cuda_stream, stream
-
-    def call(self, what, fn, *args, allocated=()):
-        if torch._C._cuda_getDevice() == self.dev:
-            st = fn(*args, self.raw)
-        else:
-            with torch.cuda.device(self.dev):
-                st = fn(*args, self.raw)
-        if self.stream is not None:
-            for t in allocated:
-                if t is not None:
-                    t.record_stream(self.stream)
-        if st != 0:
-            raise KdaError(st, what)
-
-
-def _scratch(workspace, need, like, dev):
-    """(pointer, bytes, tensor) of the given workspace, or of a new one."""
-    if workspace is None:
-        workspace = like.new_empty(max(int(need()), 256), dtype=torch.uint8)
-        return workspace.data_ptr(), workspace.numel(), workspace
-    return (_need("workspace", workspace, workspace.dtype, None, dev), workspace.numel() * workspace.element_size(),
-            None)
-
-
-def _linear_args(q, k, v, log_alpha, cu_seqlens):
-    dt = q.dtype
-    dev = _device_of("q", q)
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and v must have 4 dimensions [B, T, H, d]")
-    shape = q.shape
-    B, T, H, dk = shape
-    dv = v.shape[3]
-    ptrs = (_need("q", q, dt, None, dev), _need("k", k, dt, shape, dev), _need("v", v, dt, (B, T, H, dv), dev))
-    if log_alpha.dim() == 1:
-        decay, la = DECAY_HEAD, _need("log_alpha", log_alpha, torch.float32, (H,), dev)
-    else:
-        decay, la = DECAY_TOKEN, _need("log_alpha", log_alpha, dt, (B, T, H), dev)
-    cu, n_seqs, keep = _cu_arg(cu_seqlens)
-    return dt, dev, (B, T, H, dk, dv), ptrs + (la, decay, _DTYPES[dt]), cu, n_seqs, keep, (n_seqs if cu_seqlens is not None else B)
+def _stream(stream):
+    return None if stream is None else (stream.cuda_stream, stream.stream_id, stream.device_index, stream.device_type)
 
 
 def linear_workspace_size(B, T, H, dk, dv, dtype, cu_seqlens=None, backward: bool = False) -> int:
@@ -776,26 +718,9 @@ def linear_chunk_fwd(q, k, v, log_alpha, init_state=None, cu_seqlens=None, outpu
     contiguous, on one CUDA device.  ``log_alpha`` is ``[B, T, H]`` in that
     dtype, or ``[H]`` fp32 for a fixed decay a head.  ``init_state``,
     ``cu_seqlens`` and the results as :func:`chunk_fwd`."""
-    L = _lib or lib()
-    dt, dev, sizes, head, cu, n_seqs, _keep, N = _linear_args(q, k, v, log_alpha, cu_seqlens)
-    state_shape = (N, sizes[2], sizes[3], sizes[4])
-    init = _need("init_state", init_state, torch.float32, state_shape, dev)
-    on = _On(dev, stream)
-    made = []
-    if o is None:
-        o = torch.empty_like(v)
-        made.append(o)
-    if final_state is None and output_final_state:
-        final_state = q.new_empty(state_shape, dtype=torch.float32)
-        made.append(final_state)
-    po = _need("o", o, dt, v.shape, dev)
-    pf = _need("final_state", final_state, torch.float32, state_shape, dev)
-    pw, wb, tw = _scratch(workspace, lambda: L.kda_linear_chunk_fwd_workspace_size(*sizes, _DTYPES[dt], cu, n_seqs), q,
-                          dev)
-    made.append(tw)
-    on.call("kda_linear_chunk_fwd", L.kda_linear_chunk_fwd, *head, init, cu, n_seqs, *sizes, po, pf, pw, wb,
-            allocated=made)
-    return o, final_state
+    return (_torch_binding or _binding()).linear_chunk_fwd(
+        q, k, v, log_alpha, init_state, _offsets(cu_seqlens), output_final_state, o, final_state, workspace,
+        _stream(stream))
 
 
 def linear_chunk_bwd(q, k, v, log_alpha, d_o, init_state=None, d_final_state=None, cu_seqlens=None,
@@ -805,29 +730,10 @@ def linear_chunk_bwd(q, k, v, log_alpha, d_o, init_state=None, d_final_state=Non
     dlog_alpha, d_init_state)``; ``dlog_alpha`` is None for a fixed decay a head
     (``[H]``), ``d_init_state`` fp32 ``[N, H, dk, dv]`` or None.  ``grads`` may
     pass preallocated outputs in that order."""
-    L = _lib or lib()
-    dt, dev, sizes, head, cu, n_seqs, _keep, N = _linear_args(q, k, v, log_alpha, cu_seqlens)
-    state_shape = (N, sizes[2], sizes[3], sizes[4])
-    init = _need("init_state", init_state, torch.float32, state_shape, dev)
-    pdo = _need("d_o", d_o, dt, v.shape, dev)
-    pdf = _need("d_final_state", d_final_state, torch.float32, state_shape, dev)
-    on = _On(dev, stream)
-    made = []
-    if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
-                 torch.empty_like(log_alpha) if log_alpha.dim() != 1 else None,
-                 q.new_empty(state_shape, dtype=torch.float32) if need_d_init_state else None)
-        made.extend(grads)
-    dq, dk_, dv_, dla, dinit = grads
-    out = (_need("dq", dq, dt, q.shape, dev), _need("dk", dk_, dt, k.shape, dev), _need("dv", dv_, dt, v.shape, dev),
-           _need("dlog_alpha", dla, log_alpha.dtype, log_alpha.shape, dev),
-           _need("d_init_state", dinit, torch.float32, state_shape, dev))
-    pw, wb, tw = _scratch(workspace, lambda: L.kda_linear_chunk_bwd_workspace_size(*sizes, _DTYPES[dt], cu, n_seqs), q,
-                          dev)
-    made.append(tw)
-    on.call("kda_linear_chunk_bwd", L.kda_linear_chunk_bwd, *head, init, cu, n_seqs, *sizes, pdo, pdf, *out, pw, wb,
-            allocated=made)
-    return dq, dk_, dv_, dla, dinit
+    given = grads is not None
+    return (_torch_binding or _binding()).linear_chunk_bwd(
+        q, k, v, log_alpha, d_o, init_state, d_final_state, _offsets(cu_seqlens), need_d_init_state,
+        *(grads if given else (None,) * 5), given, workspace, _stream(stream))
 
 
 def linear_decode_step(q, k, v, log_alpha, state, o=None, stream=None):
@@ -835,88 +741,7 @@ def linear_decode_step(q, k, v, log_alpha, state, o=None, stream=None):
     (``kda_linear_decode_step``); ``state`` ``[N, H, dk, dv]`` fp32 is updated in
     place.  q, k ``[N, H, dk]``, v ``[N, H, dv]``, log_alpha ``[N, H]`` or ``[H]``
     fp32.  Returns o ``[N, H, dv]``."""
-    L = _lib or lib()
-    dt = q.dtype
-    dev = _device_of("q", q)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and v must have 3 dimensions [N, H, d]")
-    shape = q.shape
-    N, H, dk = shape
-    dv = v.shape[2]
-    pq, pk, pv = _need("q", q, dt, None, dev), _need("k", k, dt, shape, dev), _need("v", v, dt, (N, H, dv), dev)
-    if log_alpha.dim() == 1:
-        decay, la = DECAY_HEAD, _need("log_alpha", log_alpha, torch.float32, (H,), dev)
-    else:
-        decay, la = DECAY_TOKEN, _need("log_alpha", log_alpha, dt, (N, H), dev)
-    ps = _need("state", state, torch.float32, (N, H, dk, dv), dev)
-    on = _On(dev, stream)
-    made = ()
-    if o is None:
-        o = torch.empty_like(v)
-        made = (o,)
-    po = _need("o", o, dt, v.shape, dev)
-    on.call("kda_linear_decode_step", L.kda_linear_decode_step, pq, pk, pv, la, decay, _DTYPES[dt], ps, N, H, dk, dv, po,
-            allocated=made)
-    return o
-
-
-def _rows(name, t, dt, dev, shape=None):
-    """``t`` ``[..., H, d]`` as a kda_rows of its tokens: any strides that let the
-    leading dimensions be walked with one step."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
-    if t.dtype != dt:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
-    size = t.shape
-    if len(size) < 2:
-        raise ValueError(f"{name} must have shape [..., H, d]")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        d = size[-1]
-        return _Rows(t.data_ptr(), size[-2] * d, d)
-    step = t.stride()
-    if step[-1] != 1 and size[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if t.numel() == 0:
-        return _Rows(None, 0, 0)
-    token = None
-    for n, st in zip(reversed(size[:-2]), reversed(step[:-2])):   # from the innermost out
-        if n > 1:
-            if token is not None and st != token * walked:
-                raise ValueError(f"{name}'s token dimensions must be walkable with one stride")
-            token, walked = (st, n) if token is None else (token, walked * n)
-    # a stride that no step is made along is taken as that of packed heads
-    head = step[-2] if size[-2] > 1 else size[-1]
-    return _Rows(t.data_ptr(), size[-2] * head if token is None else token, head)
-
-
-def _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
-    dt = q.dtype
-    dev = _device_of("q", q)
-    rq, rk = _rows("q", q, dt, dev), _rows("k", k, dt, dev)
-    lead = q.shape[:-2]
-    Hq, d = q.shape[-2:]
-    Hk = k.shape[-2]
-    if k.shape != lead + (Hk, d):
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(lead) + (Hk, d)}")
-    wdt = dt if q_weight is None and k_weight is None else (q_weight if q_weight is not None else k_weight).dtype
-    if wdt not in _DTYPES:
-        raise ValueError(f"unsupported weight dtype {wdt}")
-    wq, wk = _need("q_weight", q_weight, wdt, (d,), dev), _need("k_weight", k_weight, wdt, (d,), dev)
-    rot, pos, freq = 0, None, None
-    if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must have one dimension [rot / 2]")
-        freq = _need("inv_freq", inv_freq, torch.float32, None, dev)
-        rot = 2 * inv_freq.shape[0]
-        if positions is None:
-            raise ValueError("positions are required with inv_freq")
-        pos = _need("positions", positions, torch.int32, lead, dev)
-    args = (rq, rk, wq, wk, _DTYPES[wdt], pos, freq, _DTYPES[dt], lead.numel(), Hq, Hk, d, rot, eps, int(interleaved))
-    return dt, wdt, dev, args
+    return (_torch_binding or _binding()).linear_decode_step(q, k, v, log_alpha, state, o, _stream(stream))
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps: float = 1e-6,
@@ -932,19 +757,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     alone.  ``interleaved`` pairs channels (2 i, 2 i + 1) instead of
     (i, i + rot / 2).  Returns ``(q_out, k_out)``; ``q_out=q, k_out=k`` works in
     place."""
-    L = _lib or lib()
-    dt, _, dev, args = _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-    on = _On(dev, stream)
-    made = []
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-        made.append(q_out)
-    if k_out is None:
-        k_out = k.new_empty(k.shape)
-        made.append(k_out)
-    on.call("kda_qk_norm_rope", L.kda_qk_norm_rope, *args, _rows("q_out", q_out, dt, dev, q.shape),
-            _rows("k_out", k_out, dt, dev, k.shape), allocated=made)
-    return q_out, k_out
+    return (_torch_binding or _binding()).qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
+                                                       q_out, k_out, _stream(stream))
 
 
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, eps: float = 1e-6,
@@ -954,21 +768,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
     of its results.  Returns ``(dq, dk, dq_weight, dk_weight)``, the last two in
     the weights' dtype (None for a weight that is None, or without
     ``need_weight_grads``).  ``grads`` may pass preallocated outputs."""
-    L = _lib or lib()
-    dt, wdt, dev, args = _norm_rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-    gq, gk = _rows("d_q_out", d_q_out, dt, dev, q.shape), _rows("d_k_out", d_k_out, dt, dev, k.shape)
-    on = _On(dev, stream)
-    made = []
-    if grads is None:
-        grads = (q.new_empty(q.shape), k.new_empty(k.shape),
-                 *(torch.empty_like(w) if w is not None and need_weight_grads else None for w in (q_weight, k_weight)))
-        made.extend(grads)
-    dq, dk_, dwq, dwk = grads
-    d = q.shape[-1]
-    pwq, pwk = _need("dq_weight", dwq, wdt, (d,), dev), _need("dk_weight", dwk, wdt, (d,), dev)
-    T, Hq, Hk, _, rot = args[8:13]
-    pw, wb, tw = _scratch(workspace, lambda: L.kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d, rot), q, dev)
-    made.append(tw)
-    on.call("kda_qk_norm_rope_bwd", L.kda_qk_norm_rope_bwd, *args, gq, gk, _rows("dq", dq, dt, dev, q.shape),
-            _rows("dk", dk_, dt, dev, k.shape), pwq, pwk, pw, wb, allocated=made)
-    return dq, dk_, dwq, dwk
+    given = grads is not None
+    return (_torch_binding or _binding()).qk_norm_rope_bwd(
+        q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, d_q_out, d_k_out, need_weight_grads,
+        *(grads if given else (None,) * 4), given, workspace, _stream(stream))

@@ -1,4 +1,5 @@
-"""Build ``libkda.so`` (the C-ABI CUDA library) in-tree for sm_100a.
+"""Build ``libkda.so`` (the C-ABI CUDA library) in-tree for sm_100a, and
+``_torch_binding.so`` (torch tensors into the C ABI, host code) beside it.
 
 Usage: ``python -m kimi_delta_attention_30_b200.build [--force]``.
 Each ``csrc/*.cu`` is compiled by nvcc to an object under ``_build/`` (in
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 
 
 def nvcc() -> str:
@@ -53,6 +56,36 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(p) > t for p in [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the torch binding with g++ (links ``libkda.so`` beside it)."""
+    if not force and not _binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(cuda_lib_dir())
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           *(f"-isystem{p}" for p in ext.include_paths()), BINDING_SRC, "-o", tmp, "-L", PKG, "-l:libkda.so", "-L", libs, "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     cmd = [nvcc(), *FLAGS, *extra, "-c", src, "-o", obj]
@@ -66,6 +99,7 @@ def _compile(src: str, extra) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
+        build_binding()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = shlex.split(os.environ.get("KDA_NVCC_FLAGS", ""))
@@ -78,6 +112,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     if verbose:
         print(f"built {LIB}")
     return LIB
