@@ -31,6 +31,7 @@ struct LinSimtWorkspace {
     float* S;       // [chunks, H, dk, dv] each chunk's update, then its start state
     float* dS;      // [chunks, H, dk, dv] (backward) the same for the reversed chain: gradient of the end state
     float* gam;     // [chunks, H] a chunk's whole decay
+    float* parts;   // (backward) [chunks, H] x (3 x 64 + 1) what dlog_alpha is put together from
 };
 
 cudaError_t launch_lin_simt_fwd(kda_dtype dtype, const void* q, const void* k, const void* v, LinDecay dec,

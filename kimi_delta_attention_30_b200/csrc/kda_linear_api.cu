@@ -9,7 +9,7 @@ namespace kda {
 namespace {
 
 struct LinLayout {
-    size_t S, dS, gam, total;   // byte offsets in the workspace (SIMT path)
+    size_t S, dS, gam, parts, total;   // byte offsets in the workspace (SIMT path)
 };
 
 LinLayout simt_layout(const Plan& p, int H, int dk, int dv, bool bwd) {
@@ -19,6 +19,7 @@ LinLayout simt_layout(const Plan& p, int H, int dk, int dv, bool bwd) {
     L.S = o; o = align_up(o + ch * dk * dv * sizeof(float));
     L.dS = o; if (bwd) o = align_up(o + ch * dk * dv * sizeof(float));
     L.gam = o; o = align_up(o + ch * sizeof(float));
+    L.parts = o; if (bwd) o = align_up(o + ch * (3 * kLinSimtChunk + 1) * sizeof(float));
     L.total = std::max(o, kAlign);
     return L;
 }
@@ -276,7 +277,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         ChunkMap cmap;
         SeqMap smap;
         if ((st = make_maps(p, T, kLinSimtChunk, ws, s, cmap, smap)) != KDA_OK) return st;
-        const LinSimtWorkspace w{(float*)(ws + L.S), nullptr, (float*)(ws + L.gam)};
+        const LinSimtWorkspace w{(float*)(ws + L.S), nullptr, (float*)(ws + L.gam), nullptr};
         return launch_lin_simt_fwd(dtype, q, k, v, dec, init_state, o, final_state, cmap, smap, p.n_chunks, p.n_seqs,
                                    H, dk, dv, w, s) == cudaSuccess
                    ? KDA_OK
@@ -365,7 +366,8 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
         ChunkMap cmap;
         SeqMap smap;
         if ((st = make_maps(p, T, kLinSimtChunk, ws, s, cmap, smap)) != KDA_OK) return st;
-        const LinSimtWorkspace w{(float*)(ws + L.S), (float*)(ws + L.dS), (float*)(ws + L.gam)};
+        const LinSimtWorkspace w{(float*)(ws + L.S), (float*)(ws + L.dS), (float*)(ws + L.gam),
+                                 (float*)(ws + L.parts)};
         return launch_lin_simt_bwd(dtype, q, k, v, dec, init_state, d_o, d_final_state, dq, dk_out, dv_out,
                                    dlog_alpha, d_init_state, cmap, smap, p.n_chunks, p.n_seqs, H, dk, dv, w, s) ==
                        cudaSuccess

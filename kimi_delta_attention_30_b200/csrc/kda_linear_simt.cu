@@ -25,7 +25,12 @@
 //
 // Products are 64 x 64 register tiles (256 threads, 4 x 4 each) over operands in shared
 // memory, every operand read as 16-byte vectors where its layout allows; fp32 throughout,
-// as fp32 inputs ask for.  Decays are formed from g as a (hi, lo) pair.
+// as fp32 inputs ask for.  Shared-memory reads bound them (a 64^3 product takes 3.8 us a
+// block), so small problems are spread wider: while the blocks would not fill the machine,
+// sums and outputs use 16-row tiles (64 threads), and the backward always gives dq, dk and
+// dv of a chunk to three blocks, which costs the pair products twice (16 units of 64^3
+// instead of 13 at 64 x 128) and puts dlog_alpha's last sums into a kernel of its own.
+// Decays are formed from g as a (hi, lo) pair.
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -91,84 +96,120 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[4]) 
     x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-// 64 token rows of COLS columns from column c0 of a [tokens, H, D] array; rows past
-// `len` are zero (they belong to the next sequence).
-template <typename Tin, int COLS>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const Tin* __restrict__ src, size_t tok0, int len, int H,
+// ROWS token rows of COLS columns from column c0 of a [tokens, H, D] array; rows past `len`
+// are zero (they belong to the next sequence).  Eight loads a thread stand before the first
+// is stored: one at a time they are a round trip to memory each.
+template <typename Tin, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const Tin* __restrict__ src, long long tok0, int len, int H,
                                           int h, int D, int c0) {
-    constexpr int V = COLS / 4;
-    for (int u = threadIdx.x; u < kC * V; u += kThreads) {
-        const int r = u / V, c = (u % V) * 4;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < len) load_vec(src + ((tok0 + r) * (size_t)H + h) * D + c0 + c, x);
-        *reinterpret_cast<float4*>(dst + r * ld + c) = make_float4(x[0], x[1], x[2], x[3]);
+    constexpr int V = COLS / 4, N = ROWS * V / THREADS, BATCH = N < 8 ? N : 8;
+    static_assert(ROWS * V % THREADS == 0 && N % BATCH == 0, "tile");
+#pragma unroll 1
+    for (int n = 0; n < N; n += BATCH) {
+        float x[BATCH][4];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int u = (n + i) * THREADS + threadIdx.x, r = u / V, c = (u % V) * 4;
+            x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+            if (r < len) load_vec(src + ((size_t)(tok0 + r) * (size_t)H + h) * D + c0 + c, x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int u = (n + i) * THREADS + threadIdx.x;
+            *reinterpret_cast<float4*>(dst + u / V * ld + (u % V) * 4) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        }
     }
 }
 
+// ROWS x COLS of a matrix with `pitch` columns, fp32
+template <int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void load_tile(float* dst, int ld, const float* __restrict__ src, int pitch) {
+    load_rows<float, ROWS, COLS, THREADS>(dst, ld, src, 0, ROWS, 1, 0, pitch, 0);
+}
+
 // The chunk's inclusive cumulative log decay as (hi, lo), by the first warp; tokens past
-// `len` add nothing, so g stays at the last token's value there.
+// `len` add nothing, so g stays at the last token's value there.  Summed in 64-bit fixed
+// point (32 fractional bits of log_alpha; exact sums).
 template <typename Tin>
 __device__ __forceinline__ void chunk_decay(float* gh, float* gl, const LinDecay& dec, size_t tok0, int len, int H,
                                             int h) {
     if (threadIdx.x < 32) {
         const int t = 2 * threadIdx.x;
-        const double a = t < len ? (double)lin_log_decay<Tin>(dec, tok0 + t, H, h) : 0.0;
-        const double b = t + 1 < len ? (double)lin_log_decay<Tin>(dec, tok0 + t + 1, H, h) : 0.0;
-        double s = a + b;
+        const float x = t < len ? lin_log_decay<Tin>(dec, tok0 + t, H, h) : 0.f;
+        const float y = t + 1 < len ? lin_log_decay<Tin>(dec, tok0 + t + 1, H, h) : 0.f;
+        const long long a = __float2ll_rn(x * 4294967296.f), b = __float2ll_rn(y * 4294967296.f);
+        long long s = a + b;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, off);
-            if ((int)threadIdx.x >= off) s += y;
+            const long long z = __shfl_up_sync(0xffffffffu, s, off);
+            if ((int)threadIdx.x >= off) s += z;
         }
-        const double g0 = s - b;
-        gh[t] = (float)g0;
-        gl[t] = (float)(g0 - (double)gh[t]);
-        gh[t + 1] = (float)s;
-        gl[t + 1] = (float)(s - (double)gh[t + 1]);
+        const long long g[2] = {s - b, s};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float hi = __ll2float_rn(g[u]);
+            gh[t + u] = hi * (1.f / 4294967296.f);
+            gl[t + u] = __ll2float_rn(g[u] - __float2ll_rn(hi)) * (1.f / 4294967296.f);
+        }
     }
 }
 
-// ---- (1) each chunk's own sum: one 64 x 64 tile of the state a block ---------------
-// Forward: sum_j e^{g_C - g_j} a_j b_j^T (a = k, b = v); REV: sum_i e^{g_i} a_i b_i^T (q, d_o).
-template <typename Tin, bool REV>
-__global__ void __launch_bounds__(kThreads) lin_update(const Tin* __restrict__ a, const Tin* __restrict__ b,
-                                                       LinDecay dec, ChunkMap cmap, int H, int DK, int DV,
-                                                       float* __restrict__ U, float* __restrict__ gam) {
-    __shared__ __align__(16) float sa[kC * kLdP], sb[kC * kLdP];
+// ---- (1) each chunk's own sum: ROWS x 64 of the state a block ------------------------
+// Forward: sum_j e^{g_C - g_j} a_j b_j^T (a = k, b = v); reversed: sum_i e^{g_i} a_i b_i^T (q, d_o).
+template <typename Tin>
+struct UpdateSide {
+    const Tin *a, *b;
+    float* U;
+};
+template <typename Tin, int ROWS>
+__global__ void __launch_bounds__(ROWS * 4) lin_update(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, LinDecay dec,
+                                                       ChunkMap cmap, int H, int DK, int DV, float* __restrict__ gam) {
+    constexpr int LDA = ROWS + 4;
+    __shared__ __align__(16) float sa[kC * LDA], sb[kC * kLdP];
     __shared__ float gh[kC], gl[kC], w[kC];
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int nv = DV / 64, k0 = ((int)blockIdx.z / nv) * 64, v0 = ((int)blockIdx.z % nv) * 64;
+    const int nv = DV / 64, tiles = nv * (DK / ROWS), z = (int)blockIdx.z % tiles;
+    const bool REV = (int)blockIdx.z >= tiles;
+    const UpdateSide<Tin>& A = REV ? rev : fwd;
+    const int k0 = z / nv * ROWS, v0 = z % nv * 64;
+    load_rows<Tin, kC, ROWS, ROWS * 4>(sa, LDA, A.a, tok0, len, H, h, DK, k0);
+    load_rows<Tin, kC, 64, ROWS * 4>(sb, kLdP, A.b, tok0, len, H, h, DV, v0);
     chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
-    load_rows<Tin, 64>(sa, kLdP, a, tok0, len, H, h, DK, k0);
-    load_rows<Tin, 64>(sb, kLdP, b, tok0, len, H, h, DV, v0);
     __syncthreads();
     if (tid < kC)
         w[tid] = REV ? exp_g(gh[tid], gl[tid]) : exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
     __syncthreads();
-    for (int u = tid; u < kC * 16; u += kThreads) {
-        float4* p = reinterpret_cast<float4*>(sb + (u >> 4) * kLdP + (u & 15) * 4);
-        const float s = w[u >> 4];
+    for (int u = tid; u < kC * ROWS / 4; u += blockDim.x) {
+        float4* p = reinterpret_cast<float4*>(sa + u / (ROWS / 4) * LDA + u % (ROWS / 4) * 4);
+        const float s = w[u / (ROWS / 4)];
         *p = make_float4(p->x * s, p->y * s, p->z * s, p->w * s);
     }
     __syncthreads();
     float acc[4][4];
     clear(acc);
-    mm64<kC, true, false, false>(acc, sa, kLdP, sb, kLdP, ty, tx);
+    mm64<kC, true, false, false>(acc, sa, LDA, sb, kLdP, ty, tx);
     const size_t unit = (size_t)blockIdx.x * H + h;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<float4*>(U + (unit * DK + k0 + 4 * ty + r) * DV + v0 + 4 * tx) =
+        *reinterpret_cast<float4*>(A.U + (unit * DK + k0 + 4 * ty + r) * DV + v0 + 4 * tx) =
             make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     if (blockIdx.z == 0 && tid == 0) gam[unit] = exp_g(gh[kC - 1], gl[kC - 1]);
 }
 
 // ---- (2) the chain over chunks, in place: X[n] = state before chunk n (REV: behind it)
-template <bool REV>
-__global__ void __launch_bounds__(kThreads) lin_chain(float* __restrict__ X, const float* __restrict__ gam,
-                                                      const float* __restrict__ start, float* __restrict__ end,
+struct ChainSide {
+    float* X;
+    const float* start;
+    float* end;
+};
+__global__ void __launch_bounds__(kThreads) lin_chain(ChainSide fwd, ChainSide rev, const float* __restrict__ gam,
                                                       SeqMap smap, int H, int E4) {
+    const bool REV = blockIdx.z != 0;
+    float* X = REV ? rev.X : fwd.X;
+    const float* start = REV ? rev.start : fwd.start;
+    float* end = REV ? rev.end : fwd.end;
     const SeqInfo sq = smap.get((int)blockIdx.x / H);
     const int h = (int)blockIdx.x % H;
     const int e = (int)blockIdx.y * kThreads + threadIdx.x;
@@ -204,28 +245,29 @@ __global__ void __launch_bounds__(kThreads) lin_chain(float* __restrict__ X, con
     if (end) reinterpret_cast<float4*>(end)[sh] = s;
 }
 
-// ---- (3) outputs: 64 tokens x 64 value columns a block -----------------------------
-template <int DK> constexpr size_t out_smem() { return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * kLdP + DK * kLdP); }
+// ---- (3) outputs: ROWS tokens x 64 value columns a block -----------------------------
+template <int DK, int ROWS> constexpr size_t out_smem() {
+    return sizeof(float) * ((ROWS + kC) * (DK + 4) + (ROWS + kC) * kLdP + DK * kLdP);
+}
 
-template <typename Tin, int DK>
-__global__ void __launch_bounds__(kThreads) lin_out(const Tin* __restrict__ q, const Tin* __restrict__ k,
-                                                    const Tin* __restrict__ v, LinDecay dec, ChunkMap cmap, int H,
-                                                    int DV, const float* __restrict__ S, Tin* __restrict__ o) {
+template <typename Tin, int DK, int ROWS>
+__global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, const Tin* __restrict__ k,
+                                                    const Tin* __restrict__ v, LinDecay dec, ChunkMap cmap, int H, int DV,
+                                                    const float* __restrict__ S, Tin* __restrict__ o) {
     extern __shared__ __align__(16) float sm[];
     __shared__ float gh[kC], gl[kC];
     constexpr int LD = DK + 4;
-    float *sq = sm, *sk = sq + kC * LD, *sv = sk + kC * LD, *sp = sv + kC * kLdP, *ss = sp + kC * kLdP;
+    float *sq = sm, *sk = sq + ROWS * LD, *sv = sk + kC * LD, *sp = sv + kC * kLdP, *ss = sp + ROWS * kLdP;
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
-    const int h = blockIdx.y, v0 = blockIdx.z * 64, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int h = blockIdx.y, nv = DV / 64, v0 = (int)blockIdx.z % nv * 64, i0 = (int)blockIdx.z / nv * ROWS;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    if (i0 >= len) return;
+    load_rows<Tin, ROWS, DK, ROWS * 4>(sq, LD, q, (long long)tok0 + i0, len - i0, H, h, DK, 0);
+    load_rows<Tin, kC, DK, ROWS * 4>(sk, LD, k, tok0, len, H, h, DK, 0);
+    load_rows<Tin, kC, 64, ROWS * 4>(sv, kLdP, v, tok0, len, H, h, DV, v0);
+    load_tile<DK, 64, ROWS * 4>(ss, kLdP, S + ((size_t)blockIdx.x * H + h) * DK * DV + v0, DV);
     chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
-    load_rows<Tin, DK>(sq, LD, q, tok0, len, H, h, DK, 0);
-    load_rows<Tin, DK>(sk, LD, k, tok0, len, H, h, DK, 0);
-    load_rows<Tin, 64>(sv, kLdP, v, tok0, len, H, h, DV, v0);
-    const float* Sn = S + ((size_t)blockIdx.x * H + h) * DK * DV + v0;
-    for (int u = tid; u < DK * 16; u += kThreads)
-        *reinterpret_cast<float4*>(ss + (u >> 4) * kLdP + (u & 15) * 4) =
-            *reinterpret_cast<const float4*>(Sn + (size_t)(u >> 4) * DV + (u & 15) * 4);
     __syncthreads();
     float acc[4][4];
     clear(acc);
@@ -234,14 +276,14 @@ __global__ void __launch_bounds__(kThreads) lin_out(const Tin* __restrict__ q, c
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const int i = 4 * ty + r, j = tx + 16 * c;
-            sp[i * kLdP + j] = j <= i ? acc[r][c] * exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
+            const int i = i0 + 4 * ty + r, j = tx + 16 * c;
+            sp[(4 * ty + r) * kLdP + j] = j <= i ? acc[r][c] * exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
         }
     clear(acc);
     mm64<DK, false, false, false>(acc, sq, LD, ss, kLdP, ty, tx);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const float e = exp_g(gh[4 * ty + r], gl[4 * ty + r]);
+        const float e = exp_g(gh[i0 + 4 * ty + r], gl[i0 + 4 * ty + r]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] *= e;
     }
@@ -249,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) lin_out(const Tin* __restrict__ q, c
     mm64<kC, false, false, false>(acc, sp, kLdP, sv, kLdP, ty, tx);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int i = 4 * ty + r;
+        const int i = i0 + 4 * ty + r;
         if (i < len) {
             Tin* dst = o + ((size_t)(tok0 + i) * H + h) * DV + v0 + 4 * tx;
 #pragma unroll
@@ -258,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) lin_out(const Tin* __restrict__ q, c
     }
 }
 
-// ---- backward: one (chunk, head) a block -------------------------------------------
+// ---- backward: one (chunk, head) and one of dq, dk, dv a block ---------------------------
 template <int DK, int DV> constexpr size_t grad_smem() {
     constexpr int tile = (64 * (DV + 4) > DK * kLdP) ? 64 * (DV + 4) : DK * kLdP;
     return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * (DV + 4) + tile + 2 * kC * kLdP);
@@ -275,45 +317,59 @@ __device__ __forceinline__ void add_row_sums(float* dst, const float (&s)[4], in
     }
 }
 
+// What dlog_alpha is put together from, per unit = (chunk, head): a[i] = q_i . e^{g_i} (S d_o_i),
+// b[j] = k_j . e^{g_C - g_j} (dS' v_j), r[t] = sum over i >= t > j, e = e^{g_C} <dS', S>.
+struct DecayParts {
+    float *a, *b, *r, *e;   // [units, 64] each, e [units]
+};
+
 template <typename Tin, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, LinDecay dec,
          const Tin* __restrict__ d_o, ChunkMap cmap, int H, const float* __restrict__ S, const float* __restrict__ dS,
-         Tin* __restrict__ dq, Tin* __restrict__ dk, Tin* __restrict__ dv, Tin* __restrict__ dla) {
+         Tin* __restrict__ dq, Tin* __restrict__ dk, Tin* __restrict__ dv, DecayParts parts) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ float gh[kC], gl[kC], wq[kC], wk[kC], ra[kC], rb[kC], rx[kC], red[kThreads / 32];
+    __shared__ float gh[kC], gl[kC], w[kC], ra[kC], red[kThreads / 32];
     constexpr int LK = DK + 4, LV = DV + 4;
     float *sq = sm, *sk = sq + kC * LK, *sv = sk + kC * LK, *sd = sv + kC * LV;
     float *sp = sd + kC * LV, *sa = sp + kC * kLdP, *tile = sa + kC * kLdP;
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
-    const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int h = blockIdx.y, role = blockIdx.z, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;   // dq, dk, dv
     const size_t unit = (size_t)blockIdx.x * H + h;
     const float *Sn = S + unit * DK * DV, *dSn = dS + unit * DK * DV;
+    load_rows<Tin, kC, DK, kThreads>(sq, LK, q, tok0, len, H, h, DK, 0);
+    load_rows<Tin, kC, DK, kThreads>(sk, LK, k, tok0, len, H, h, DK, 0);
+    if (role < 2) load_rows<Tin, kC, DV, kThreads>(sv, LV, v, tok0, len, H, h, DV, 0);
+    load_rows<Tin, kC, DV, kThreads>(sd, LV, d_o, tok0, len, H, h, DV, 0);
     chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
-    load_rows<Tin, DK>(sq, LK, q, tok0, len, H, h, DK, 0);
-    load_rows<Tin, DK>(sk, LK, k, tok0, len, H, h, DK, 0);
-    load_rows<Tin, DV>(sv, LV, v, tok0, len, H, h, DV, 0);
-    load_rows<Tin, DV>(sd, LV, d_o, tok0, len, H, h, DV, 0);
-    float e = 0.f;   // <dS', S>
-    for (int u = tid; u < DK * DV / 4; u += kThreads) {
-        const float4 x = reinterpret_cast<const float4*>(Sn)[u], y = reinterpret_cast<const float4*>(dSn)[u];
-        e += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-    }
+    if (role == 2) {
+        float e = 0.f;   // <dS', S>
+#pragma unroll 8
+        for (int u = tid; u < DK * DV / 4; u += kThreads) {
+            const float4 x = reinterpret_cast<const float4*>(Sn)[u], y = reinterpret_cast<const float4*>(dSn)[u];
+            e += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
-    if ((tid & 31) == 0) red[tid >> 5] = e;
+        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+        if ((tid & 31) == 0) red[tid >> 5] = e;
+    }
     __syncthreads();
     if (tid < kC) {
-        wq[tid] = exp_g(gh[tid], gl[tid]);
-        wk[tid] = exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
-        ra[tid] = rb[tid] = 0.f;
+        w[tid] = role == 0 ? exp_g(gh[tid], gl[tid]) : exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
+        ra[tid] = 0.f;
+    }
+    if (role == 2 && tid == 0) {
+        float whole = 0.f;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) whole += red[i];
+        parts.e[unit] = whole * exp_g(gh[kC - 1], gl[kC - 1]);
     }
     float p[4][4], a[4][4];
     clear(p);
     clear(a);
-    mm64<DK, false, true, true>(p, sq, LK, sk, LK, ty, tx);
-    mm64<DV, false, true, true>(a, sd, LV, sv, LV, ty, tx);
+    if (role != 1) mm64<DK, false, true, true>(p, sq, LK, sk, LK, ty, tx);
+    if (role != 2) mm64<DV, false, true, true>(a, sd, LV, sv, LV, ty, tx);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -325,7 +381,7 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
             tile[i * kLdM + j] = j < i ? p[r][c] * a[r][c] * d : 0.f;
         }
     __syncthreads();
-    {   // rx[t] = sum of the pair products over i >= t > j, four threads a row, then four a column
+    if (role == 0) {   // r[t] = sum of the pair products over i >= t > j, four threads a row, then four a column
         const int i = tid >> 2, part = tid & 3;
         float* row = tile + i * kLdM + 16 * part;
         float run = 0.f;
@@ -348,29 +404,25 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
         for (int r = t + ((part - t) & 3); t > 0 && r < kC; r += 4) sum += tile[r * kLdM + t - 1];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (part == 0) rx[t] = sum;
+        if (part == 0) parts.r[unit * kC + t] = sum;
     }
-    for (int k0 = 0; k0 < DK; k0 += 64) {
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {   // dq from S and dA k, then dk from dS' and dA^T q
+    if (role < 2) {   // dq from S and dA k, or dk from dS' and dA^T q
+        const float* x = role ? sk : sq;
+        Tin* out = role ? dk : dq;
+        for (int k0 = 0; k0 < DK; k0 += 64) {
             __syncthreads();
-            const float* src = (side ? dSn : Sn) + (size_t)k0 * DV;
-            for (int u = tid; u < 64 * DV / 4; u += kThreads)
-                *reinterpret_cast<float4*>(tile + (u / (DV / 4)) * LV + (u % (DV / 4)) * 4) =
-                    reinterpret_cast<const float4*>(src)[u];
+            load_tile<64, DV, kThreads>(tile, LV, (role ? dSn : Sn) + (size_t)k0 * DV, DV);
             __syncthreads();
-            float s1[4];
             clear(p);
             clear(a);
-            if (side == 0) {
+            if (role == 0) {
                 mm64<DV, false, true, true>(p, sd, LV, tile, LV, ty, tx);
                 mm64<kC, false, false, true>(a, sa, kLdP, sk + k0, LK, ty, tx);
             } else {
                 mm64<DV, false, true, true>(p, sv, LV, tile, LV, ty, tx);
                 mm64<kC, true, false, true>(a, sa, kLdP, sq + k0, LK, ty, tx);
             }
-            const float *w = side ? wk : wq, *x = (side ? sk : sq) + k0;
-            Tin* out = side ? dk : dq;
+            float s1[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 4 * ty + r;
@@ -379,77 +431,102 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int j = tx + 16 * c;
-                    const float xi = x[i * LK + j], inter = wi * p[r][c];
-                    s1[r] = fmaf(xi, inter, s1[r]);
+                    const float inter = wi * p[r][c];
+                    s1[r] = fmaf(x[i * LK + k0 + j], inter, s1[r]);
                     if (i < len) out[((size_t)(tok0 + i) * H + h) * DK + k0 + j] = from_f32<Tin>(inter + a[r][c]);
                 }
             }
-            add_row_sums(side ? rb : ra, s1, ty, tx);
+            add_row_sums(ra, s1, ty, tx);
         }
-    }
-    for (int v0 = 0; v0 < DV; v0 += 64) {
         __syncthreads();
-        for (int u = tid; u < DK * 16; u += kThreads)
-            *reinterpret_cast<float4*>(tile + (u >> 4) * kLdP + (u & 15) * 4) =
-                *reinterpret_cast<const float4*>(dSn + (size_t)(u >> 4) * DV + v0 + (u & 15) * 4);
-        __syncthreads();
-        clear(p);
-        mm64<DK, false, false, false>(p, sk, LK, tile, kLdP, ty, tx);
+        if (tid < kC) (role ? parts.b : parts.a)[unit * kC + tid] = ra[tid];
+    } else {
+        for (int v0 = 0; v0 < DV; v0 += 64) {
+            __syncthreads();
+            load_tile<DK, 64, kThreads>(tile, kLdP, dSn + v0, DV);
+            __syncthreads();
+            clear(p);
+            mm64<DK, false, false, false>(p, sk, LK, tile, kLdP, ty, tx);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) p[r][c] *= wk[4 * ty + r];
-        mm64<kC, true, false, false>(p, sp, kLdP, sd + v0, LV, ty, tx);
+                for (int c = 0; c < 4; ++c) p[r][c] *= w[4 * ty + r];
+            mm64<kC, true, false, false>(p, sp, kLdP, sd + v0, LV, ty, tx);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 4 * ty + r;
-            if (i < len) {
-                Tin* dst = dv + ((size_t)(tok0 + i) * H + h) * DV + v0 + 4 * tx;
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * ty + r;
+                if (i < len) {
+                    Tin* dst = dv + ((size_t)(tok0 + i) * H + h) * DV + v0 + 4 * tx;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dst[c] = from_f32<Tin>(p[r][c]);
+                    for (int c = 0; c < 4; ++c) dst[c] = from_f32<Tin>(p[r][c]);
+                }
             }
         }
-    }
-    if (dla != nullptr && tid < 32) {
-        // suffix sums of ra, exclusive prefix sums of rb, two tokens a lane
-        __syncwarp();
-        const int t = 2 * tid;
-        float suf = ra[t] + ra[t + 1], pre = rb[t] + rb[t + 1];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float y = __shfl_down_sync(0xffffffffu, suf, off), z = __shfl_up_sync(0xffffffffu, pre, off);
-            if (tid + off < 32) suf += y;
-            if (tid >= off) pre += z;
-        }
-        // the lane's own terms are left out by taking its neighbour's sums, not by subtraction
-        float suf_next = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-        if (tid == 31) suf_next = 0.f;
-        pre = tid == 0 ? 0.f : before;
-        float whole = 0.f;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) whole += red[i];
-        whole *= exp_g(gh[kC - 1], gl[kC - 1]);
-        const float x0 = suf + pre + whole + rx[t];
-        const float x1 = suf_next + ra[t + 1] + pre + rb[t] + whole + rx[t + 1];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (t + u < len) {
-                const size_t tok = (size_t)tok0 + t + u;
-                const bool floored = lin_raw_decay<Tin>(dec, tok, H, h) < kLogAlphaFloor;
-                dla[tok * H + h] = from_f32<Tin>(floored ? 0.f : (u ? x1 : x0));
-            }
     }
 }
 
-template <typename Tin, bool REV>
-cudaError_t update_and_chain(const void* a, const void* b, LinDecay dec, const float* start, float* end,
+// dlog_alpha of one unit a warp: suffix sums of a, exclusive prefix sums of b, two tokens a lane
+template <typename Tin>
+__global__ void __launch_bounds__(128) lin_decay_grad(DecayParts parts, LinDecay dec, ChunkMap cmap, int n_units, int H,
+                                                      Tin* __restrict__ dla) {
+    const int unit = (int)blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (unit >= n_units) return;
+    int seq, tok0, len, idx;
+    cmap.locate(unit / H, seq, tok0, len, idx);
+    const int h = unit % H, t = 2 * lane;
+    const float2 a = reinterpret_cast<const float2*>(parts.a + (size_t)unit * kC)[lane];
+    const float2 b = reinterpret_cast<const float2*>(parts.b + (size_t)unit * kC)[lane];
+    const float2 r = reinterpret_cast<const float2*>(parts.r + (size_t)unit * kC)[lane];
+    const float whole = parts.e[unit];
+    float suf = a.x + a.y, pre = b.x + b.y;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, suf, off), z = __shfl_up_sync(0xffffffffu, pre, off);
+        if (lane + off < 32) suf += y;
+        if (lane >= off) pre += z;
+    }
+    // the lane's own terms are left out by taking its neighbour's sums, not by subtraction
+    float next = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+    if (lane == 31) next = 0.f;
+    if (lane == 0) before = 0.f;
+    const float x[2] = {suf + before + whole + r.x, next + a.y + before + b.x + whole + r.y};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (t + u < len) {
+            const size_t tok = (size_t)tok0 + t + u;
+            const bool floored = lin_raw_decay<Tin>(dec, tok, H, h) < kLogAlphaFloor;
+            dla[tok * H + h] = from_f32<Tin>(floored ? 0.f : x[u]);
+        }
+}
+
+// Tiles of 16 rows while 64-row ones would leave SMs without a block.
+bool small_grid(long long blocks) { return blocks < 148; }
+
+template <typename Tin>
+cudaError_t update_and_chain(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, int sides, LinDecay dec, ChainSide cf, ChainSide cr,
                              const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
-                             float* X, float* gam, cudaStream_t s) {
-    if (n_chunks > 0)
-        lin_update<Tin, REV><<<dim3(n_chunks, H, (dk / 64) * (dv / 64)), kThreads, 0, s>>>(
-            (const Tin*)a, (const Tin*)b, dec, cmap, H, dk, dv, X, gam);
+                             float* gam, cudaStream_t s) {
+    if (n_chunks > 0) {
+        const int tiles = (dk / 64) * (dv / 64) * sides;
+        if (small_grid((long long)n_chunks * H * tiles))
+            lin_update<Tin, 16><<<dim3(n_chunks, H, 4 * tiles), 64, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv, gam);
+        else
+            lin_update<Tin, 64><<<dim3(n_chunks, H, tiles), kThreads, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv, gam);
+    }
     const int e4 = dk * dv / 4;
-    lin_chain<REV><<<dim3((unsigned)n_seqs * H, e4 / kThreads), kThreads, 0, s>>>(X, gam, start, end, smap, H, e4);
+    lin_chain<<<dim3((unsigned)n_seqs * H, e4 / kThreads, sides), kThreads, 0, s>>>(cf, cr, gam, smap, H, e4);
+    return cudaGetLastError();
+}
+
+template <typename Tin, int DK, int ROWS>
+cudaError_t outputs(const void* q, const void* k, const void* v, LinDecay dec, void* o, const ChunkMap& cmap, int n_chunks,
+                    int H, int dv, const LinSimtWorkspace& ws, cudaStream_t s) {
+    auto kern = lin_out<Tin, DK, ROWS>;
+    constexpr size_t smem = out_smem<DK, ROWS>();
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    kern<<<dim3(n_chunks, H, dv / 64 * (kC / ROWS)), ROWS * 4, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec,
+                                                                        cmap, H, dv, ws.S, (Tin*)o);
     return cudaGetLastError();
 }
 
@@ -457,16 +534,15 @@ template <typename Tin>
 cudaError_t fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init, void* o, float* final,
                 const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
                 const LinSimtWorkspace& ws, cudaStream_t s) {
-    cudaError_t err = update_and_chain<Tin, false>(k, v, dec, init, final, cmap, smap, n_chunks, n_seqs, H, dk, dv,
-                                                   ws.S, ws.gam, s);
+    const UpdateSide<Tin> u{(const Tin*)k, (const Tin*)v, ws.S};
+    const ChainSide c{ws.S, init, final};
+    const cudaError_t err = update_and_chain<Tin>(u, u, 1, dec, c, c, cmap, smap, n_chunks, n_seqs, H, dk, dv, ws.gam, s);
     if (err != cudaSuccess || n_chunks == 0) return err;
-    const dim3 grid(n_chunks, H, dv / 64);
-    auto kern = dk == 128 ? lin_out<Tin, 128> : lin_out<Tin, 64>;
-    const size_t smem = dk == 128 ? out_smem<128>() : out_smem<64>();
-    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return err;
-    kern<<<grid, kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, cmap, H, dv, ws.S, (Tin*)o);
-    return cudaGetLastError();
+    if (small_grid((long long)n_chunks * H * (dv / 64)))
+        return dk == 128 ? outputs<Tin, 128, 16>(q, k, v, dec, o, cmap, n_chunks, H, dv, ws, s)
+                         : outputs<Tin, 64, 16>(q, k, v, dec, o, cmap, n_chunks, H, dv, ws, s);
+    return dk == 128 ? outputs<Tin, 128, 64>(q, k, v, dec, o, cmap, n_chunks, H, dv, ws, s)
+                     : outputs<Tin, 64, 64>(q, k, v, dec, o, cmap, n_chunks, H, dv, ws, s);
 }
 
 template <typename Tin, int DK, int DV>
@@ -477,9 +553,12 @@ cudaError_t grad(const void* q, const void* k, const void* v, LinDecay dec, cons
     constexpr size_t smem = grad_smem<DK, DV>();
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    kern<<<dim3(n_chunks, H), kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, (const Tin*)d_o,
-                                                   cmap, H, ws.S, ws.dS, (Tin*)dq, (Tin*)dk, (Tin*)dv,
-                                                   dec.per_head ? nullptr : (Tin*)dla);
+    const int units = n_chunks * H;
+    const size_t n = (size_t)units * kC;
+    const DecayParts parts{ws.parts, ws.parts + n, ws.parts + 2 * n, ws.parts + 3 * n};
+    kern<<<dim3(n_chunks, H, 3), kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, (const Tin*)d_o,
+                                                      cmap, H, ws.S, ws.dS, (Tin*)dq, (Tin*)dk, (Tin*)dv, parts);
+    if (!dec.per_head) lin_decay_grad<Tin><<<(units + 3) / 4, 128, 0, s>>>(parts, dec, cmap, units, H, (Tin*)dla);
     return cudaGetLastError();
 }
 
@@ -488,11 +567,10 @@ cudaError_t bwd(const void* q, const void* k, const void* v, LinDecay dec, const
                 const float* d_final, void* dq, void* dk_out, void* dv_out, void* dla, float* d_init,
                 const ChunkMap& cmap, const SeqMap& smap, int n_chunks, int n_seqs, int H, int dk, int dv,
                 const LinSimtWorkspace& ws, cudaStream_t s) {
-    cudaError_t err = update_and_chain<Tin, false>(k, v, dec, init, nullptr, cmap, smap, n_chunks, n_seqs, H, dk, dv,
-                                                   ws.S, ws.gam, s);
-    if (err != cudaSuccess) return err;
-    err = update_and_chain<Tin, true>(q, d_o, dec, d_final, d_init, cmap, smap, n_chunks, n_seqs, H, dk, dv, ws.dS,
-                                      ws.gam, s);
+    const UpdateSide<Tin> uf{(const Tin*)k, (const Tin*)v, ws.S}, ur{(const Tin*)q, (const Tin*)d_o, ws.dS};
+    const ChainSide cf{ws.S, init, nullptr}, cr{ws.dS, d_final, d_init};
+    const cudaError_t err = update_and_chain<Tin>(uf, ur, 2, dec, cf, cr, cmap, smap, n_chunks, n_seqs, H, dk, dv, ws.gam,
+                                                  s);
     if (err != cudaSuccess || n_chunks == 0) return err;
     if (dk == 128 && dv == 128)
         return grad<Tin, 128, 128>(q, k, v, dec, d_o, dq, dk_out, dv_out, dla, cmap, n_chunks, H, ws, s);
