@@ -35,9 +35,11 @@ struct Cut {
 
 constexpr int kSms = 148;
 
-// Microseconds a chunk of 128 tokens takes a block (one block an SM): all 128 value
-// columns, half of them, and the state alone; and the launches that a split adds.
-constexpr double kWalk128 = 1.75, kWalk64 = 1.35, kStateOnly = 1.1, kSplitCost = 8.0;
+// Microseconds a chunk of 128 tokens takes a block (one block an SM): all 128 value columns,
+// half of them, and the state alone; a block's start and end; and what a split adds (the
+// segments' chain, two more launches).  From 1 to 10 segments a sequence, 8 to 512 chunks
+// and 16 to 704 blocks, times estimated with these are within 15 % of the measured ones.
+constexpr double kWalk128 = 3.2, kWalk64 = 2.75, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
 
 long long longest_of(const Plan& chunks) {   // chunks of the longest sequence
     long long longest = 0;
@@ -55,6 +57,13 @@ long long segments_of(const Plan& chunks, long long longest, long long len) {   
     return segs;
 }
 
+// Time of `units` blocks, the longest of `len` chunks: whole waves where all are alike,
+// otherwise (packed sequences, the longest first) what the machine's work adds up to.
+double walk_time(const Plan& chunks, long long units, long long len, double work, bool alike, double t) {
+    const double waves = (double)((units + kSms - 1) / kSms);
+    return alike || !chunks.varlen ? waves * (len * t + kRamp) : std::max((double)len, work / kSms) * t + kRamp;
+}
+
 // The cut with the least estimated time.  A sequence's chunks follow one another, so with
 // few (sequence, head) pairs most SMs would idle: two blocks of 64 value columns a pair
 // repeat the scores and the weighted keys, and segments read k and v twice.
@@ -63,20 +72,19 @@ Cut choose_cut(const Plan& chunks, int H) {
     Cut best;
     if (longest == 0) return best;
     best.seg_chunks = (int)longest;
-    const double work = (double)total * H / kSms;
-    double t = std::max((double)longest, work) * kWalk128;
-    const double t64 = std::max((double)longest, 2 * work) * kWalk64;
+    const long long pairs = (long long)chunks.n_seqs * H;
+    double t = walk_time(chunks, pairs, longest, (double)total * H, false, kWalk128);
+    const double t64 = walk_time(chunks, 2 * pairs, longest, 2.0 * total * H, false, kWalk64);
     if (t64 < t) {
         t = t64;
         best.BV = 64;
     }
-    for (int m = 1; m <= 8; ++m) {
-        const long long len = std::max<long long>(4, (long long)(total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
+    for (int m = 1; m <= 6; ++m) {
+        const long long len = std::max<long long>(4, (total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
         if (len >= longest) continue;
         const long long segs = segments_of(chunks, longest, len);
-        const double waves = (double)((segs * H + kSms - 1) / kSms);
-        const double first = (double)(((segs - chunks.n_seqs) * H + kSms - 1) / kSms);
-        const double ts = len * (waves * kWalk128 + first * kStateOnly) + kSplitCost;
+        const double ts = walk_time(chunks, segs * H, len, 0, true, kWalk128) +
+                          walk_time(chunks, (segs - chunks.n_seqs) * H, len, 0, true, kStateOnly) + kSplitCost;
         if (ts < t) {
             t = ts;
             best = Cut{(int)len, 128, true};
@@ -88,19 +96,17 @@ Cut choose_cut(const Plan& chunks, int H) {
 // The same for the backward pass's state chains (both directions side by side, all value
 // columns): what a split saves in idle SMs against walking the chunks twice.
 Cut choose_state_cut(const Plan& chunks, int H) {
-    const long long total = chunks.n_chunks;
-    const long long longest = longest_of(chunks);
+    const long long longest = longest_of(chunks), total = chunks.n_chunks;
     Cut best;
     if (longest == 0) return best;
     best.seg_chunks = (int)longest;
-    double t = std::max((double)longest, 2.0 * total * H / kSms) * kStateOnly;
-    for (int m = 1; m <= 8; ++m) {
+    double t = walk_time(chunks, 2LL * chunks.n_seqs * H, longest, 2.0 * total * H, false, kStateOnly);
+    for (int m = 1; m <= 6; ++m) {
         const long long len = std::max<long long>(4, (2 * total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
         if (len >= longest) continue;
         const long long segs = segments_of(chunks, longest, len);
-        const double waves = (double)((2 * segs * H + kSms - 1) / kSms);
-        const double first = (double)((2 * (segs - chunks.n_seqs) * H + kSms - 1) / kSms);
-        const double ts = len * (waves + first) * kStateOnly + kSplitCost;
+        const double ts = walk_time(chunks, 2 * segs * H, len, 0, true, kStateOnly) +
+                          walk_time(chunks, 2 * (segs - chunks.n_seqs) * H, len, 0, true, kStateOnly) + kSplitCost;
         if (ts < t) {
             t = ts;
             best = Cut{(int)len, 128, true};
@@ -135,8 +141,11 @@ kda_status tc_layout(const Plan& chunks, const int32_t* cu, int n_seqs, int B, i
     return KDA_OK;
 }
 
-int empty_of(const Plan& p) {   // sequences without tokens: the last of the longest-first order
+// Sequences without tokens (the last of the longest-first order) that no walk visits: all of
+// them, unless the walk goes by that order.
+int empty_of(const Plan& p, bool split) {
     if (p.total_tokens == 0) return p.n_seqs;
+    if (!split) return 0;
     int n = 0;
     for (const SeqInfo& q : p.natural) n += q.len == 0;
     return n;
@@ -159,16 +168,17 @@ kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_s
     return KDA_OK;
 }
 
-kda_status make_maps(const Plan& p, int T, int C, char* ws, cudaStream_t s, ChunkMap& cmap, SeqMap& smap) {
+kda_status make_maps(const Plan& p, int T, int C, char* ws, cudaStream_t s, ChunkMap& cmap, SeqMap& smap,
+                     bool chunk_entries = true) {
     const int ncps = (int)(((long long)T + C - 1) / C);
     cmap = ChunkMap{nullptr, p.n_seqs, T, C, ncps};
     smap = SeqMap{nullptr, T, C, ncps};
     if (p.varlen) {
         cudaError_t err;
-        upload_tables((SeqInfo*)ws, p.natural, p.by_len, p.n_chunks, C, s, &err);
+        upload_tables((SeqInfo*)ws, p.natural, p.by_len, chunk_entries ? p.n_chunks : 0, C, s, &err);
         if (err != cudaSuccess) return KDA_ERR_CUDA;
         cmap.seqs = (const SeqInfo*)ws;
-        cmap.chunks = chunk_table((SeqInfo*)ws, p.n_seqs);
+        if (chunk_entries) cmap.chunks = chunk_table((SeqInfo*)ws, p.n_seqs);
         smap.order = (const SeqInfo*)ws + p.n_seqs;
     }
     return KDA_OK;
@@ -259,8 +269,9 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
             char* ws = (char*)workspace;
             ChunkMap segs;
             SeqMap smap;
-            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws, s, segs, smap)) != KDA_OK) return st;
-            const int empty = empty_of(p);
+            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws, s, segs, smap, L.cut.split)) != KDA_OK)
+                return st;
+            const int empty = empty_of(p, L.cut.split);
             cudaError_t e = launch_lin_empty_states(init_state, final_state, smap, p.n_seqs - empty, empty, H, s);
             if (e == cudaSuccess && p.total_tokens > 0)
                 e = launch_lin_tc_fwd(q, k, v, dec, init_state, o, final_state, segs, smap, L.segs.n_chunks, p.n_seqs,
@@ -341,10 +352,11 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
             char* ws = (char*)workspace;
             ChunkMap segs, chunks;
             SeqMap smap, cmap;
-            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws + L.seg_tables, s, segs, smap)) != KDA_OK ||
+            if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws + L.seg_tables, s, segs, smap,
+                                L.cut.split)) != KDA_OK ||
                 (st = make_maps(p, T, kLinTcChunk, ws, s, chunks, cmap)) != KDA_OK)
                 return st;
-            const int empty = empty_of(p);
+            const int empty = empty_of(p, L.cut.split);
             cudaError_t e = launch_lin_empty_states(d_final_state, d_init_state, smap, p.n_seqs - empty, empty, H, s);
             uint8_t *im = (uint8_t*)(ws + L.images), *dim = (uint8_t*)(ws + L.d_images);
             int* err = (int*)(ws + L.err);

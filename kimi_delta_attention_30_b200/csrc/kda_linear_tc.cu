@@ -13,16 +13,16 @@
 // errors would be carried from chunk to chunk and it is returned in fp32.
 //
 // Roles, each with its own barriers, so that they work on different chunks at once: 8 warps
-// form o and keep the state (warp w: rows 32 (w % 4) + lane, column half w / 4), 8 turn
-// scores into P and weight the keys, one issues the products, one the loads, one forms the
-// decays.  The state itself is off the critical path: U needs no state, so the chain from
-// chunk to chunk is one multiply-add and the copy for the next queries.  Products are issued
-// in the order P V, Q S, Q K^T of the next chunk, U: the first three run while the keys are
-// weighted (which waits for the last U to release the low parts' buffer), P of the next
-// chunk is formed while U runs.  Five 32 KB slots hold Q, K, V in turn (Q's slot is free
-// first and takes the next V).  A 128 x 128 x 16 product reads 8 KB in the 64 cycles it
-// takes, which is all that shared memory gives, so products, the loads' writes and the
-// weighting share 128 bytes a cycle.
+// form o and keep the state (warp w: rows 32 (w % 4) + lane, column half w / 4), 8 weight the
+// keys, 8 turn scores into P, one issues the products, one the loads, one forms the decays.
+// The state itself is off the critical path: U needs no state, so the chain from chunk to
+// chunk is one multiply-add and the copy for the next queries.  Products are issued in the
+// order P V, Q S, Q K^T of the next chunk, U: the first three run while the keys are weighted
+// (which waits for the last U to release the low parts' buffer), P of the next chunk is
+// formed meanwhile.  Five 32 KB slots hold Q, K, V in turn (Q's slot is free first and takes
+// the next V).  A 128 x 128 x 16 product reads 8 KB in the 64 cycles it takes, which is all
+// that shared memory gives, so products, the loads' writes and the weighting share 128 bytes
+// a cycle.
 // Rows past a sequence's end are loaded with the box (they belong to the next sequence); K's
 // are weighted with zero, V's are cleared, Q's only reach rows of o that are not stored.
 #include <algorithm>
@@ -56,7 +56,8 @@ bool make_map(CUtensorMap* map, const void* base, long long tokens, int H, int b
 
 namespace {
 
-constexpr int kWalkThreads = 640;   // warps 0-7 state (and o), 8-15 weights (and P), 16 products, 17 loads, 18 decays
+constexpr int kWalkThreads = 896;    // warps 0-7 o and the state, 8-15 weights, 16 products, 17 loads, 18 decays, 20-27 P
+constexpr int kStateThreads = 640;   // the same without P
 
 // whether segment `idx` of sequence `seq` is its last
 __device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int idx) {
@@ -73,14 +74,15 @@ constexpr uint32_t kOffBars = kOffGates + 2 * sizeof(Gates);
 constexpr uint32_t kWalkSmem = kOffBars + 256;
 static_assert(kWalkSmem <= 232448, "shared memory per block");
 
-enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady, kQsDone, kKReady, kODone, kORead, kUDone, kSReady,
+enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kKFree, kPReady = kKFree + 2, kQsDone, kKReady, kODone, kORead, kUDone, kSReady,
                kGFull, kGEmpty = kGFull + 2, kDrain = kGEmpty + 2, kWalkBars };
 
 template <int BV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, LinDecay dec, ChunkMap segs,
-         int H, const float* __restrict__ init_state, const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
+         const SeqInfo* __restrict__ order, int H, const float* __restrict__ init_state,
+         const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
          float* __restrict__ final_state, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
@@ -95,13 +97,27 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const int vt = (int)(blockIdx.x % NV), h = (int)(blockIdx.x / NV % H), seg = (int)(blockIdx.x / NV / H);
     const int j0 = vt * BV;
     int seq, tok0, len, idx;
-    segs.locate(seg, seq, tok0, len, idx);
+    if (order != nullptr) {   // whole sequences, the longest first, so that the last blocks are short
+        const SeqInfo s = order[seg];
+        seq = s.seq;
+        tok0 = s.tok0;
+        len = s.len;
+        idx = 0;
+        if (len == 0) {       // no tokens: the state stays
+            const size_t at = ((size_t)seq * H + h) * kD * kD;
+            for (int i = tid; final_state && vt == 0 && i < kD * kD; i += kWalkThreads)
+                final_state[at + i] = init_state ? init_state[at + i] : 0.f;
+            return;
+        }
+    } else {
+        segs.locate(seg, seq, tok0, len, idx);
+    }
     const int nch = (len + kT - 1) / kT;
 
     if (tid == 0) {
         for (int i = 0; i < kWalkBars; ++i)   // one arrival a warp
             mbar_init(&bars[i], i == kPReady || i == kKReady || i == kSReady || i == kORead ? 8
-                                : i == kGEmpty || i == kGEmpty + 1 ? 16 : 1);
+                                : i == kGEmpty || i == kGEmpty + 1 ? 24 : 1);
         mbar_init_fence();
         flags[1] = 0u;
     }
@@ -120,14 +136,16 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     auto full_par = [&](int i) { return (uint32_t)(i / kSlots) & 1u; };
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
     auto gates_full = [&](int n) { return wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
-    auto scores_done = [&](int n) { return wait_or_abort(&bars[kScores], (uint32_t)n & 1u, ab); };
+    // two barriers by turns: the next chunk's scores may be done before the weighting warps look
+    auto scores_read = [&](int n) { return wait_or_abort(&bars[kKFree + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
     const int sp = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * sp) << 16;
 
-    // 96 registers a thread at launch, 20 warps: 8 x 120 + 8 x 96 + 4 x 40 of 20 x 96
-    if (warp >= 16) fewer_registers<40>();
+    // 72 registers a thread at launch, 28 warps: 8 x 104 + 16 x 64 + 4 x 40 of 28 x 72
+    if (warp >= 16 && warp < 20) fewer_registers<40>();
+    else if (warp >= 8) fewer_registers<64>();
     if (warp < 8) {   // ---- o, and the state
-        more_registers<120>();
+        more_registers<104>();
         const int hb = warp >> 2, row = 32 * sp + lane;
         float s[HB];   // state row `row`, columns j0 + HB hb + [0, HB)
         {
@@ -221,69 +239,79 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             for (int j = 0; j < HB; j += 4)
                 *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         }
-    } else if (warp < 16) {   // ---- P, and the weighted keys
-        const int hb = (warp >> 2) & 1, row = 32 * sp + lane, r = tid & 127;
+    } else if (warp < 16) {   // ---- the weighted keys
+        const int blk = (warp >> 2) & 1, r = tid & 127;
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t par = (uint32_t)n & 1u;
+            if (!gates_full(n)) break;
+            const float wk = gates[n & 1].col[r] * gates[n & 1].end[r >> 5];
+            warp_arrive(&bars[kGEmpty + (n & 1)], lane);
+            // the scores have read the keys, the last U the low parts
+            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) || !scores_read(n) ||
+                (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)))
+                break;
+            scale_split_row(slot(3 * n + 1), sm + kOffLo, r, blk, wk, r < len - n * kT);
+            fence_async_smem();
+            warp_arrive(&bars[kKReady], lane);
+        }
+    } else if (warp >= 20) {   // ---- P
+        const int hb = (warp >> 2) & 1, row = 32 * sp + lane;
         for (int n = 0; n < nch; ++n) {
             const uint32_t par = (uint32_t)n & 1u;
             const int live = min(kT, len - n * kT);
             if (!gates_full(n)) break;
             if (live < kT) {
                 if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
-                zero_rows(slot(3 * n + 2), BV / 64, live, tid - 256, 256);
+                zero_rows(slot(3 * n + 2), BV / 64, live, tid - 640, 256);
                 fence_async_smem();
             }
             const Gates& G = gates[n & 1];
-            const float r2 = G.rel2[row], er = ex2_approx(r2), wk = G.col[r] * G.end[r >> 5];
-            if (!scores_done(n)) break;
+            const float r2 = G.rel2[row], er = ex2_approx(r2);
+            if (!wait_or_abort(&bars[kScores], par, ab)) break;
             tc_fence_after();
+            // this thread's row, 64 keys, 32 at a time; P's words go over scores already read
 #pragma unroll 1
-            for (int bb = 0; bb < 2; ++bb) {   // 32 keys at a time; P's words go over scores already read
+            for (int bb = 0; bb < 2; ++bb) {
                 const int B = 2 * hb + bb;
                 uint32_t w[16];
                 if (B > sp) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
                 } else {
-                    float a[2][16];
-                    tmem_ld16(tA + lanes + 32 * B, a[0]);
-                    tmem_ld16(tA + lanes + 32 * B + 16, a[1]);
+                    float x[2][16];
+                    tmem_ld16(tA + lanes + 32 * B, x[0]);
+                    tmem_ld16(tA + lanes + 32 * B + 16, x[1]);
                     tmem_ld_wait();
                     if (B < sp) {
                         const float f = er * G.fac[sp][B];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 c = *reinterpret_cast<const float4*>(&G.col[32 * B + e]);
-                            float* x = &a[e >> 4][e & 15];
-                            w[e / 2] = pack_bf16(x[0] * (f * c.x), x[1] * (f * c.y));
-                            w[e / 2 + 1] = pack_bf16(x[2] * (f * c.z), x[3] * (f * c.w));
+                            const float* y = &x[e >> 4][e & 15];
+                            w[e / 2] = pack_bf16(y[0] * (f * c.x), y[1] * (f * c.y));
+                            w[e / 2 + 1] = pack_bf16(y[2] * (f * c.z), y[3] * (f * c.w));
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 c = *reinterpret_cast<const float4*>(&G.rel2[32 * B + e]);
-                            float* x = &a[e >> 4][e & 15];
-                            const float y0 = e <= lane ? x[0] * ex2_approx(r2 - c.x) : 0.f;
-                            const float y1 = e + 1 <= lane ? x[1] * ex2_approx(r2 - c.y) : 0.f;
-                            const float y2 = e + 2 <= lane ? x[2] * ex2_approx(r2 - c.z) : 0.f;
-                            const float y3 = e + 3 <= lane ? x[3] * ex2_approx(r2 - c.w) : 0.f;
+                            const float* y = &x[e >> 4][e & 15];
+                            const float y0 = e <= lane ? y[0] * ex2_approx(r2 - c.x) : 0.f;
+                            const float y1 = e + 1 <= lane ? y[1] * ex2_approx(r2 - c.y) : 0.f;
+                            const float y2 = e + 2 <= lane ? y[2] * ex2_approx(r2 - c.z) : 0.f;
+                            const float y3 = e + 3 <= lane ? y[3] * ex2_approx(r2 - c.w) : 0.f;
                             w[e / 2] = pack_bf16(y0, y1);
                             w[e / 2 + 1] = pack_bf16(y2, y3);
                         }
                     }
                 }
-                tmem_st16u(tA + lanes + 64 * hb + 16 * bb, w);
+                tmem_st8u(tA + lanes + 64 * hb + 16 * bb, w);
+                tmem_st8u(tA + lanes + 64 * hb + 16 * bb + 8, w + 8);
             }
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&bars[kPReady], lane);
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
-            // the scores have read the keys, the last U the low parts
-            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) ||
-                (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)))
-                break;
-            scale_split_row(slot(3 * n + 1), sm + kOffLo, r, hb, wk, r < live);
-            fence_async_smem();
-            warp_arrive(&bars[kKReady], lane);
         }
     } else if (warp == 16) {   // ---- products
         constexpr uint32_t iS = idesc_bf16_f32(128, 128), iB = idesc_bf16_f32_bmn(128, BV), iU = idesc_amn_bmn(128, BV);
@@ -298,6 +326,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             product<false, false>(tA, sw128_desc(base + (3 * n) % kSlots * kTile),
                                   sw128_desc(base + (3 * n + 1) % kSlots * kTile), iS, false, lead);
             commit(kScores);
+            commit(kKFree + (n & 1));
             return true;
         };
         bool ok = scores(0);
@@ -319,8 +348,14 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             product<false, true>(tQS, sw128_desc(q), mn_desc_k(st, kD, 0), iB, false, lead);
             commit(kQsDone);
             commit(kEmpty + (3 * n) % kSlots);
-            // the next chunk's scores, once P has been read
-            if (n + 1 < nch && !(ok = wait_or_abort(&bars[kODone], par, ab) && scores(n + 1))) break;
+            // The next chunk's scores, once P has been read.  Half the value columns: early, the
+            // weighting would wait for them (93 against 104 us for 32 chunks on 128 blocks).  All
+            // of them: behind U, or the tiles that they need, still on their way, hold U up (117
+            // against 120 us for 32 chunks on 148 blocks).
+            auto next_scores = [&] {
+                return n + 1 >= nch || (wait_or_abort(&bars[kODone], par, ab) && scores(n + 1));
+            };
+            if (BV == 64 && !(ok = next_scores())) break;
             // weighted K^T V, high then low parts
             if (!(ok = wait_or_abort(&bars[kKReady], par, ab))) break;
             tc_fence_after();
@@ -329,6 +364,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             commit(kUDone);
             commit(kEmpty + (3 * n + 1) % kSlots);
             commit(kEmpty + (3 * n + 2) % kSlots);
+            if (BV == 128 && !(ok = next_scores())) break;
         }
         if (!ok) {   // given up: products in flight end before the tensor memory is freed
             commit(kDrain);
@@ -339,9 +375,9 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             int i = 0;
             bool ok = true;
             for (; i < 3 * nch; ++i) {
-                if (i >= kSlots && !(ok = wait_or_abort_lane(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
                 const int t = tok0 + (i / 3) * kT, kind = i % 3;
                 const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
+                if (i >= kSlots && !(ok = wait_or_abort_lane(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
                 uint8_t* dst = slot(i);
                 if (kind < 2 || BV == 128) {
                     mbar_arrive_expect_tx(full(i), kTile);
@@ -402,10 +438,10 @@ static_assert(kStSmem <= 232448, "shared memory per block");
 enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = kSWReady + 2, kSURead = kSUDone + 2,
              kSGFull = kSURead + 2, kSGEmpty = kSGFull + kStGateBufs, kSDrain = kSGEmpty + kStGateBufs, kStBarsN };
 
-__global__ void __launch_bounds__(kWalkThreads, 1)
+__global__ void __launch_bounds__(kStateThreads, 1)
 lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, LinDecay dec, ChunkMap segs,
-          int H, int n_fwd, StateSide fwd, StateSide bwd, int clear_err, int* __restrict__ err) {
+          const SeqInfo* __restrict__ order, int H, int n_fwd, StateSide fwd, StateSide bwd, int clear_err, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
@@ -421,7 +457,20 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     const CUtensorMap *ma = REV ? &mq : &mk, *mb = REV ? &mdo : &mv;
     const int h = unit % H, seg = unit / H;
     int seq, tok0, len, idx;
-    segs.locate(seg, seq, tok0, len, idx);
+    if (order != nullptr) {   // whole sequences, the longest first
+        const SeqInfo s = order[seg];
+        seq = s.seq;
+        tok0 = s.tok0;
+        len = s.len;
+        idx = 0;
+        if (len == 0) {       // no tokens: the state stays
+            const size_t at = ((size_t)seq * H + h) * kD * kD;
+            for (int i = tid; A.end && i < kD * kD; i += kStateThreads) A.end[at + i] = A.start ? A.start[at + i] : 0.f;
+            return;
+        }
+    } else {
+        segs.locate(seg, seq, tok0, len, idx);
+    }
     const bool last = REV ? idx == 0 : last_segment(segs, seq, idx);
     if (A.seg_end && last) return;   // nothing follows it
     const int nch = (len + kT - 1) / kT;
@@ -674,15 +723,17 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     if (split) {
         if ((e = allow_smem(lin_state, kStSmem)) != cudaSuccess) return e;
         const StateSide side{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
-        lin_state<<<(unsigned)n_segs * H, kWalkThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, H, n_segs * H, side,
+        lin_state<<<(unsigned)n_segs * H, kStateThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, nullptr, H, n_segs * H, side,
                                                                      side, 1, err);
         seg_chain<false><<<dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s>>>(seg_state, seg_gam, init_state,
                                                                                    smap, H);
     }
     auto kern = BV == 128 ? lin_walk<128> : lin_walk<64>;
     if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
-    kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
-        mq, mk, mv, mo, dec, segs, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
+    // whole packed sequences go by the longest-first table, empty ones among them
+    const SeqInfo* order = split ? nullptr : smap.order;
+    kern<<<(unsigned)(order ? n_seqs : n_segs) * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
+        mq, mk, mv, mo, dec, segs, order, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
     return cudaGetLastError();
 }
 
@@ -704,14 +755,16 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
     if (split) {
         const StateSide f{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
         const StateSide r{nullptr, nullptr, d_seg, d_gam, nullptr, nullptr};
-        lin_state<<<2u * units, kWalkThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, H, units, f, r, 1, err);
+        lin_state<<<2u * units, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, nullptr, H, units, f, r, 1, err);
         const dim3 grid((unsigned)n_seqs * H, kD * kD / 1024);
         seg_chain<false><<<grid, 256, 0, s>>>(seg_state, seg_gam, init_state, smap, H);
         seg_chain<true><<<grid, 256, 0, s>>>(d_seg, d_gam, d_final, smap, H);
     }
     const StateSide f{init_state, split ? seg_state : nullptr, nullptr, nullptr, images, nullptr};
     const StateSide r{d_final, split ? d_seg : nullptr, nullptr, nullptr, d_images, d_init};
-    lin_state<<<2u * units, kWalkThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, H, units, f, r, !split, err);
+    const SeqInfo* order = split ? nullptr : smap.order;
+    const int n = order ? n_seqs * H : units;
+    lin_state<<<2u * n, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, order, H, n, f, r, !split, err);
     return cudaGetLastError();
 }
 

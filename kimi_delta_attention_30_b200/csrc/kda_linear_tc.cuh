@@ -97,12 +97,11 @@ __device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint64_t b_mn
     for (int s = 0; s < 8; ++s) mma_lead_ta(d, a + 8 * s + 32 * (s >> 2), mn_step(b_mn, s), idesc, s > 0, lead);
 }
 
-// 16 words (bf16 pairs) a lane into tensor memory
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* w) {
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-    tmem_st16(taddr, v);
+// 8 words (bf16 pairs) a lane into tensor memory
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* w) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // ---- waits ----------------------------------------------------------------------------
