@@ -6,7 +6,9 @@
 //   A = Q K^T                      fp32 in tensor memory
 //   P = A . D                      rounded to bf16, back into tensor memory as an A operand
 //   O = P V + e^{g} (Q S)          S read as a bf16 copy
-//   U = (e^{g_C - g} K)^T V        the weighted keys as a bf16 pair (two products)
+//   U = (e^{g_C - g} K)^T V        the weighted keys as a bf16 pair (two products); with half
+//                                  the value columns the values are weighted instead, which
+//                                  is half the work and leaves the keys as they are
 //   S <- e^{g_C} S + U             fp32
 // The only roundings to 8 bits are P and the copy of S that the queries read, both of the
 // kind that o itself takes when it is stored; the state sees 16-bit operands, since its
@@ -66,15 +68,15 @@ __device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int 
 }
 
 // ---- outputs ------------------------------------------------------------------------
-constexpr int kSlots = 5;
-constexpr uint32_t kOffLo = kSlots * kTile;            // low parts of the weighted keys
-constexpr uint32_t kOffS = kOffLo + kTile;             // the state's copy
+constexpr int kSlots = 6;                              // barriers; five slots of 32 KB, or four and two halves
+constexpr uint32_t kOffLo = 5 * kTile;                 // low parts of the weighted keys; both parts of the values
+constexpr uint32_t kOffS = kOffLo + kTile;             // the state's copy (and o on its way out)
 constexpr uint32_t kOffGates = kOffS + kTile;
 constexpr uint32_t kOffBars = kOffGates + 2 * sizeof(Gates);
 constexpr uint32_t kWalkSmem = kOffBars + 256;
 static_assert(kWalkSmem <= 232448, "shared memory per block");
 
-enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kKFree, kPReady = kKFree + 2, kQsDone, kKReady, kODone, kORead, kUDone, kSReady,
+enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady = kScores + 2, kQsDone = kPReady + 2, kKReady, kODone, kORead, kUDone, kSReady,
                kGFull, kGEmpty = kGFull + 2, kDrain = kGEmpty + 2, kWalkBars };
 
 template <int BV>
@@ -116,7 +118,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 
     if (tid == 0) {
         for (int i = 0; i < kWalkBars; ++i)   // one arrival a warp
-            mbar_init(&bars[i], i == kPReady || i == kKReady || i == kSReady || i == kORead ? 8
+            mbar_init(&bars[i], i == kPReady || i == kPReady + 1 || i == kKReady || i == kSReady || i == kORead ? 8
                                 : i == kGEmpty || i == kGEmpty + 1 ? 24 : 1);
         mbar_init_fence();
         flags[1] = 0u;
@@ -129,15 +131,28 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = flags[0];
-    const uint32_t tA = tbase, tU = tbase + 128, tPV = tbase + 256, tQS = tbase + 384;
+    // scores (and P), and Q S: two by turns where the accumulators leave room for them
+    const uint32_t tU = tbase + 256, tPV = BV == 128 ? tbase + 384 : tbase + 320;
+    auto tA = [&](int n) { return BV == 128 ? tbase : tbase + 128 * (n & 1); };
+    auto tQS = [&](int n) { return BV == 128 ? tbase + 128 : tbase + 384 + 64 * (n & 1); };
     const Abort ab{&flags[1], err};
-    auto slot = [&](int i) { return sm + (uint32_t)(i % kSlots) * kTile; };   // tile i: Q 3 n, K 3 n + 1, V 3 n + 2
-    auto full = [&](int i) { return &bars[kFull + i % kSlots]; };
-    auto full_par = [&](int i) { return (uint32_t)(i / kSlots) & 1u; };
+    // Tile i: Q 3 n, K 3 n + 1, V 3 n + 2.  Five slots in turn (Q's is free first and takes the
+    // next V); with half the value columns there is room for two of each kind.
+    constexpr int kRing = BV == 128 ? 5 : 6;
+    auto offset = [&](int i) {
+        const uint32_t x = (uint32_t)i % kRing;
+        if (BV == 128) return x * kTile;
+        const uint32_t kind = x % 3, second = x / 3;
+        return kind == 2 ? 4 * kTile + second * kBlock : (2 * kind + second) * kTile;
+    };
+    auto slot = [&](int i) { return sm + offset(i); };
+    auto full = [&](int i) { return &bars[kFull + i % kRing]; };
+    auto empty = [&](int i) { return kEmpty + i % kRing; };
+    auto full_par = [&](int i) { return (uint32_t)(i / kRing) & 1u; };
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
     auto gates_full = [&](int n) { return wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
-    // two barriers by turns: the next chunk's scores may be done before the weighting warps look
-    auto scores_read = [&](int n) { return wait_or_abort(&bars[kKFree + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
+    // two barriers by turns: the next chunk's scores may be done before a warp looks
+    auto scores_done = [&](int n) { return wait_or_abort(&bars[kScores + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
     const int sp = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * sp) << 16;
 
@@ -160,8 +175,10 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             }
         }
         auto publish = [&]() {   // the state's bf16 copy, an MN-major B operand
-            if (lane == 0) bulk_wait_read_all();   // o has left its buffer
-            __syncwarp();
+            if (BV == 128) {     // o has left its buffer
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            }
 #pragma unroll
             for (int j = 0; j < HB; j += 8) {
                 const uint4 w = make_uint4(pack_bf16(s[j], s[j + 1]), pack_bf16(s[j + 2], s[j + 3]),
@@ -172,15 +189,11 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             tc_fence_before();
             warp_arrive(&bars[kSReady], lane);
         };
-        publish();
-        bool ok = true;
-        for (int n = 0; n < nch; ++n) {
-            const uint32_t par = (uint32_t)n & 1u;
-            if (!(ok = gates_full(n))) break;
-            const float gam = gates[n & 1].gam, eg = ex2_approx(gates[n & 1].rel2[row]) * gates[n & 1].start[sp];
-            warp_arrive(&bars[kGEmpty + (n & 1)], lane);
-            // o = P V + e^g (Q S)
-            if (!(ok = wait_or_abort(&bars[kODone], par, ab) && wait_or_abort(&bars[kQsDone], par, ab))) break;
+        // o = P V + e^g (Q S)
+        auto outputs = [&](int n, float eg) {
+            if (!wait_or_abort(&bars[kODone], (uint32_t)n & 1u, ab) ||   // BV = 64: Q S was issued before P V
+                (BV == 128 && !wait_or_abort(&bars[kQsDone], (uint32_t)n & 1u, ab)))
+                return false;
             tc_fence_after();
             // A lane's row in pieces of 32 bytes, straight to global memory, would cost the
             // load/store pipe 32 cycles a store; so the rows go by way of shared memory: into
@@ -189,11 +202,15 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             const bool whole = 32 * sp + 32 <= len - n * kT;
             __nv_bfloat16* dst = o + ((size_t)(tok0 + n * kT + row) * H + h) * kD + j0 + HB * hb;
             uint8_t* stage = sm + kOffS + (BV == 128 ? hb * kBlock + 32 * sp * 128 : kBlock + (4 * hb + sp) * 2048);
+            if (BV == 64) {      // the last o has left
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            }
 #pragma unroll 1
             for (int g = 0; g < HB / 16; ++g) {
                 float a[16], b[16];
                 tmem_ld16(tPV + lanes + HB * hb + 16 * g, a);
-                tmem_ld16(tQS + lanes + HB * hb + 16 * g, b);
+                tmem_ld16(tQS(n) + lanes + HB * hb + 16 * g, b);
                 tmem_ld_wait();
                 uint32_t w[8];
 #pragma unroll
@@ -217,7 +234,16 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             }
             tc_fence_before();
             warp_arrive(&bars[kORead], lane);
-            if (!(ok = wait_or_abort(&bars[kUDone], par, ab))) break;
+            return true;
+        };
+        publish();
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            if (!(ok = gates_full(n))) break;
+            const float gam = gates[n & 1].gam, eg = ex2_approx(gates[n & 1].rel2[row]) * gates[n & 1].start[sp];
+            warp_arrive(&bars[kGEmpty + (n & 1)], lane);
+            if (BV == 128 && !(ok = outputs(n, eg))) break;
+            if (!(ok = wait_or_abort(&bars[kUDone], (uint32_t)n & 1u, ab))) break;
             tc_fence_after();
 #pragma unroll
             for (int g = 0; g < HB / 16; ++g) {
@@ -227,10 +253,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[16 * g + e] = fmaf(gam, s[16 * g + e], a[e]);
             }
-            if (n + 1 < nch) {
-                // Q S of this chunk was issued before its U, which is done
-                publish();
-            }
+            if (n + 1 < nch) publish();   // Q S of this chunk was issued before its U, which is done
+            if (BV == 64 && !(ok = outputs(n, eg))) break;
         }
         if (lane == 0) bulk_wait_read_all();   // before the block's shared memory goes
         if (final_state && ok && last_segment(segs, seq, idx)) {
@@ -239,25 +263,33 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             for (int j = 0; j < HB; j += 4)
                 *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         }
-    } else if (warp < 16) {   // ---- the weighted keys
+    } else if (warp < 16) {   // ---- the weighted keys, or values
         const int blk = (warp >> 2) & 1, r = tid & 127;
         for (int n = 0; n < nch; ++n) {
             const uint32_t par = (uint32_t)n & 1u;
+            const int live = min(kT, len - n * kT);
             if (!gates_full(n)) break;
-            const float wk = gates[n & 1].col[r] * gates[n & 1].end[r >> 5];
+            const float w = gates[n & 1].col[r] * gates[n & 1].end[r >> 5];
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
-            // the scores have read the keys, the last U the low parts
-            if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) || !scores_read(n) ||
-                (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)))
-                break;
-            scale_split_row(slot(3 * n + 1), sm + kOffLo, r, blk, wk, r < len - n * kT);
+            if (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)) break;   // the last U has read the parts
+            if (BV == 128) {   // in place: the scores have read the keys
+                if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) || !scores_done(n)) break;
+                uint8_t* tile = slot(3 * n + 1) + blk * kBlock;
+                scale_split_row<8>(tile, tile, sm + kOffLo + blk * kBlock, r, 0, w, r < live);
+            } else {           // half the columns, into a buffer of their own (P V needs the values)
+                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
+                scale_split_row<4>(slot(3 * n + 2), sm + kOffLo, sm + kOffLo + kBlock, r, 4 * blk, w, r < live);
+                if (live < kT) {   // the keys' rows of the next sequence meet weights of zero
+                    if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab)) break;
+                    zero_rows(slot(3 * n + 1), 2, live, tid - 256, 256);
+                }
+            }
             fence_async_smem();
             warp_arrive(&bars[kKReady], lane);
         }
     } else if (warp >= 20) {   // ---- P
         const int hb = (warp >> 2) & 1, row = 32 * sp + lane;
         for (int n = 0; n < nch; ++n) {
-            const uint32_t par = (uint32_t)n & 1u;
             const int live = min(kT, len - n * kT);
             if (!gates_full(n)) break;
             if (live < kT) {
@@ -267,7 +299,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             }
             const Gates& G = gates[n & 1];
             const float r2 = G.rel2[row], er = ex2_approx(r2);
-            if (!wait_or_abort(&bars[kScores], par, ab)) break;
+            if (!scores_done(n)) break;
             tc_fence_after();
             // this thread's row, 64 keys, 32 at a time; P's words go over scores already read
 #pragma unroll 1
@@ -279,8 +311,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
                 } else {
                     float x[2][16];
-                    tmem_ld16(tA + lanes + 32 * B, x[0]);
-                    tmem_ld16(tA + lanes + 32 * B + 16, x[1]);
+                    tmem_ld16(tA(n) + lanes + 32 * B, x[0]);
+                    tmem_ld16(tA(n) + lanes + 32 * B + 16, x[1]);
                     tmem_ld_wait();
                     if (B < sp) {
                         const float f = er * G.fac[sp][B];
@@ -305,12 +337,12 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                         }
                     }
                 }
-                tmem_st8u(tA + lanes + 64 * hb + 16 * bb, w);
-                tmem_st8u(tA + lanes + 64 * hb + 16 * bb + 8, w + 8);
+                tmem_st8u(tA(n) + lanes + 64 * hb + 16 * bb, w);
+                tmem_st8u(tA(n) + lanes + 64 * hb + 16 * bb + 8, w + 8);
             }
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&bars[kPReady], lane);
+            warp_arrive(&bars[kPReady + (n & 1)], lane);
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
         }
     } else if (warp == 16) {   // ---- products
@@ -320,51 +352,51 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         auto commit = [&](int bar) {
             if (lead) mma_commit(&bars[bar]);
         };
-        auto scores = [&](int n) {
+        auto scores = [&](int n) {   // A = Q K^T
             if (!wait_or_abort(full(3 * n), full_par(3 * n), ab) || !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
                 return false;
-            product<false, false>(tA, sw128_desc(base + (3 * n) % kSlots * kTile),
-                                  sw128_desc(base + (3 * n + 1) % kSlots * kTile), iS, false, lead);
-            commit(kScores);
-            commit(kKFree + (n & 1));
+            product<false, false>(tA(n), sw128_desc(base + offset(3 * n)), sw128_desc(base + offset(3 * n + 1)), iS, false,
+                                  lead);
+            commit(kScores + (n & 1));
+            return true;
+        };
+        auto values = [&](int n) {   // P V
+            if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab) || !wait_or_abort(&bars[kPReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) ||
+                (n > 0 && !wait_or_abort(&bars[kORead], (uint32_t)(n + 1) & 1u, ab)))
+                return false;
+            tc_fence_after();
+            product_ta(tPV, tA(n), mn_desc_k(base + offset(3 * n + 2), kT, 0), iB, lead);
+            commit(kODone);
             return true;
         };
         bool ok = scores(0);
         for (int n = 0; ok && n < nch; ++n) {
-            const uint32_t par = (uint32_t)n & 1u;
-            const uint32_t q = base + (3 * n) % kSlots * kTile, k = base + (3 * n + 1) % kSlots * kTile,
-                           v = base + (3 * n + 2) % kSlots * kTile;
-            // P V
-            if (!(ok = wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab) && wait_or_abort(&bars[kPReady], par, ab) &&
-                       (n == 0 || wait_or_abort(&bars[kORead], par ^ 1u, ab))))
-                break;
-            tc_fence_after();
-            const uint64_t dv = mn_desc_k(v, kT, 0);
-            product_ta(tPV, tA, dv, iB, lead);
-            commit(kODone);
+            if (BV == 128 && !(ok = values(n))) break;
             // Q S
-            if (!(ok = wait_or_abort(&bars[kSReady], par, ab))) break;
+            if (!(ok = wait_or_abort(&bars[kSReady], (uint32_t)n & 1u, ab))) break;
             tc_fence_after();
-            product<false, true>(tQS, sw128_desc(q), mn_desc_k(st, kD, 0), iB, false, lead);
-            commit(kQsDone);
-            commit(kEmpty + (3 * n) % kSlots);
-            // The next chunk's scores, once P has been read.  Half the value columns: early, the
-            // weighting would wait for them (93 against 104 us for 32 chunks on 128 blocks).  All
-            // of them: behind U, or the tiles that they need, still on their way, hold U up (117
-            // against 120 us for 32 chunks on 148 blocks).
-            auto next_scores = [&] {
-                return n + 1 >= nch || (wait_or_abort(&bars[kODone], par, ab) && scores(n + 1));
-            };
-            if (BV == 64 && !(ok = next_scores())) break;
-            // weighted K^T V, high then low parts
-            if (!(ok = wait_or_abort(&bars[kKReady], par, ab))) break;
+            product<false, true>(tQS(n), sw128_desc(base + offset(3 * n)), mn_desc_k(st, kD, 0), iB, false, lead);
+            if (BV == 128) commit(kQsDone);
+            commit(empty(3 * n));
+            // K^T V with the weights, high then low parts
+            if (!(ok = wait_or_abort(&bars[kKReady], (uint32_t)n & 1u, ab))) break;
             tc_fence_after();
-            product<true, true>(tU, mn_desc_k(k, kT, 0), dv, iU, false, lead);
-            product<true, true>(tU, mn_desc_k(lo, kT, 0), dv, iU, true, lead);
+            const uint64_t dk = mn_desc_k(base + offset(3 * n + 1), kT, 0), dv = mn_desc_k(base + offset(3 * n + 2), kT, 0);
+            const uint64_t dl = mn_desc_k(lo, kT, 0);
+            product<true, true>(tU, dk, BV == 128 ? dv : dl, iU, false, lead);
+            product<true, true>(tU, BV == 128 ? dl : dk, BV == 128 ? dv : mn_desc_k(lo + kBlock, kT, 0), iU, true, lead);
             commit(kUDone);
-            commit(kEmpty + (3 * n + 1) % kSlots);
-            commit(kEmpty + (3 * n + 2) % kSlots);
-            if (BV == 128 && !(ok = next_scores())) break;
+            commit(empty(3 * n + 1));
+            if (BV == 128) {
+                commit(empty(3 * n + 2));
+                if (n + 1 < nch && !(ok = wait_or_abort(&bars[kODone], (uint32_t)n & 1u, ab) && scores(n + 1))) break;
+            } else {
+                // over the scores of the last chunk but one, whose P V is done
+                if (n > 0 && !(ok = wait_or_abort(&bars[kODone], (uint32_t)(n + 1) & 1u, ab))) break;
+                if (n + 1 < nch && !(ok = scores(n + 1))) break;
+                if (!(ok = values(n))) break;
+                commit(empty(3 * n + 2));
+            }
         }
         if (!ok) {   // given up: products in flight end before the tensor memory is freed
             commit(kDrain);
@@ -377,7 +409,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             for (; i < 3 * nch; ++i) {
                 const int t = tok0 + (i / 3) * kT, kind = i % 3;
                 const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
-                if (i >= kSlots && !(ok = wait_or_abort_lane(&bars[kEmpty + i % kSlots], full_par(i) ^ 1u, ab))) break;
+                if (i >= kRing && !(ok = wait_or_abort_lane(&bars[empty(i)], full_par(i) ^ 1u, ab))) break;
                 uint8_t* dst = slot(i);
                 if (kind < 2 || BV == 128) {
                     mbar_arrive_expect_tx(full(i), kTile);
@@ -389,7 +421,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                 }
             }
             if (!ok)   // given up: the copies in flight land before the block ends
-                for (int j = max(0, i - kSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
+                for (int j = max(0, i - kRing); j < i; ++j) mbar_wait(full(j), full_par(j));
         }
     } else if (warp == 18) {   // ---- decays
         float x[4], y[4];
@@ -577,7 +609,8 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
                 if (!wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab)) break;
                 zero_rows(slot(2 * n + 1), 2, live, tid - 256, 256);
             }
-            scale_split_row(slot(2 * n), sm + kStLo + (n & 1) * kTile, r, blk, w, r < live);
+            uint8_t *tile = slot(2 * n) + blk * kBlock, *low = sm + kStLo + (n & 1) * kTile + blk * kBlock;
+            scale_split_row<8>(tile, tile, low, r, 0, w, r < live);
             fence_async_smem();
             warp_arrive(&bars[kSWReady + (n & 1)], lane);
         }

@@ -269,15 +269,18 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
 }
 
 // ---- the weighted rows as a bf16 pair ------------------------------------------------------
-// One thread scales 64 channels (column block blk) of the tile's row by w: the high parts
-// replace the row, the low parts go to `lo` (same layout).  hi + lo carries 16 bits.
-__device__ __forceinline__ void scale_split_row(uint8_t* tile, uint8_t* lo, int row, int blk, float w, bool live) {
-    uint8_t* src = tile + blk * kBlock + row * 128;
-    uint8_t* dst = lo + blk * kBlock + row * 128;
+// One thread scales 8 N channels of a 64-column block's row, from 16-byte piece c0 on, by w:
+// high parts to `hi` (which may be the row itself), low parts to `lo`, all in the same
+// swizzled layout.  hi + lo carries 16 bits.
+template <int N>
+__device__ __forceinline__ void scale_split_row(const uint8_t* src_block, uint8_t* hi_block, uint8_t* lo_block, int row,
+                                                int c0, float w, bool live) {
+    const uint8_t* src = src_block + row * 128;
+    uint8_t *hi = hi_block + row * 128, *lo = lo_block + row * 128;
     const float2 w2 = make_float2(w, w);
 #pragma unroll 4
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t off = (uint32_t)((c ^ (row & 7)) << 4);
+    for (int c = 0; c < N; ++c) {
+        const uint32_t off = (uint32_t)(((c0 + c) ^ (row & 7)) << 4);
         uint4 x = *reinterpret_cast<const uint4*>(src + off), y = make_uint4(0u, 0u, 0u, 0u);
         if (live) {
             uint32_t* xp = &x.x;
@@ -290,8 +293,8 @@ __device__ __forceinline__ void scale_split_row(uint8_t* tile, uint8_t* lo, int 
         } else {
             x = y;   // rows past the chunk's end weigh nothing, whatever they hold
         }
-        *reinterpret_cast<uint4*>(src + off) = x;
-        *reinterpret_cast<uint4*>(dst + off) = y;
+        *reinterpret_cast<uint4*>(hi + off) = x;
+        *reinterpret_cast<uint4*>(lo + off) = y;
     }
 }
 
