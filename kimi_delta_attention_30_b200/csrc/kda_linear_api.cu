@@ -39,7 +39,7 @@ constexpr int kSms = 148;
 // half of them, and the state alone; a block's start and end; and what a split adds (the
 // segments' chain, two more launches).  From 1 to 10 segments a sequence, 8 to 512 chunks
 // and 16 to 704 blocks, times estimated with these are within 15 % of the measured ones.
-constexpr double kWalk128 = 3.2, kWalk64 = 2.75, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
+constexpr double kWalk128 = 3.2, kWalk64 = 2.25, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
 
 long long longest_of(const Plan& chunks) {   // chunks of the longest sequence
     long long longest = 0;
@@ -57,11 +57,26 @@ long long segments_of(const Plan& chunks, long long longest, long long len) {   
     return segs;
 }
 
+// Chunks a segment for `blocks` blocks of work (`per` of them a segment), so that as few as
+// possible run behind the others: one segment more than fit would start another wave.
+long long segment_len(const Plan& chunks, long long longest, long long per, long long blocks) {
+    const long long even = (chunks.n_chunks * per + blocks - 1) / blocks;
+    if (!chunks.varlen) {
+        const long long segs = blocks / (per * chunks.n_seqs);   // a sequence
+        return std::max<long long>(4, segs > 0 ? (longest + segs - 1) / segs : longest);
+    }
+    long long len = std::max<long long>(4, even);
+    for (int i = 0; i < 16 && len < longest && segments_of(chunks, longest, len) * per > blocks; ++i)
+        len += std::max<long long>(1, len / 16);
+    return len;
+}
+
 // Time of `units` blocks, the longest of `len` chunks: whole waves where all are alike,
 // otherwise (packed sequences, the longest first) what the machine's work adds up to.
 double walk_time(const Plan& chunks, long long units, long long len, double work, bool alike, double t) {
     const double waves = (double)((units + kSms - 1) / kSms);
-    return alike || !chunks.varlen ? waves * (len * t + kRamp) : std::max((double)len, work / kSms) * t + kRamp;
+    return alike || !chunks.varlen ? waves * (len * t + kRamp)
+                                   : std::max(len * t + kRamp, (work * t + units * kRamp) / kSms);
 }
 
 // The cut with the least estimated time.  A sequence's chunks follow one another, so with
@@ -80,7 +95,7 @@ Cut choose_cut(const Plan& chunks, int H) {
         best.BV = 64;
     }
     for (int m = 1; m <= 6; ++m) {
-        const long long len = std::max<long long>(4, (total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
+        const long long len = segment_len(chunks, longest, H, (long long)kSms * m);
         if (len >= longest) continue;
         const long long segs = segments_of(chunks, longest, len);
         const double ts = walk_time(chunks, segs * H, len, 0, true, kWalk128) +
@@ -102,7 +117,7 @@ Cut choose_state_cut(const Plan& chunks, int H) {
     best.seg_chunks = (int)longest;
     double t = walk_time(chunks, 2LL * chunks.n_seqs * H, longest, 2.0 * total * H, false, kStateOnly);
     for (int m = 1; m <= 6; ++m) {
-        const long long len = std::max<long long>(4, (2 * total * H + (long long)kSms * m - 1) / ((long long)kSms * m));
+        const long long len = segment_len(chunks, longest, 2LL * H, (long long)kSms * m);
         if (len >= longest) continue;
         const long long segs = segments_of(chunks, longest, len);
         const double ts = walk_time(chunks, 2 * segs * H, len, 0, true, kStateOnly) +

@@ -54,47 +54,63 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* map, const void
 
 // Products are issued by a whole warp whose elected lane (`lead`) carries the instruction:
 // control and descriptors then stay uniform for the warp.  A step of a rolled loop takes its
-// 64 cycles that way; the same loop under a branch of one lane took 100.
-__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate, uint32_t lead) {
+// 64 cycles that way; the same loop under a branch of one lane took 100.  Only the low words
+// of the descriptors change from step to step.
+__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                         uint32_t idesc, uint32_t accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(lead));
 }
 // A in tensor memory: bf16 pairs, one row a lane.
-__device__ __forceinline__ void mma_lead_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_lead_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc,
                                             uint32_t accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(lead));
 }
 
 __host__ __device__ constexpr uint32_t idesc_amn_bmn(int M, int N) {
     return idesc_bf16_f32(M, N) | (1u << 15) | (1u << 16);
 }
 
-// One product over K = 128 as eight steps of 16.  Kept as loops: the roles of a block run
-// different code at once, and what they run once a chunk has to stay small enough for the
-// instruction caches (unrolled code cost five times its issue time in fetches).
+// One product over K = 128 as two loops of four steps of 16.  Not unrolled further: the roles
+// of a block run different code at once, and what they run once a chunk has to stay small
+// enough for the instruction caches (unrolled code cost five times its issue time in fetches).
 // Descriptor steps, in 16-byte units: a K-major tile moves 32 bytes a step inside a
 // 64-column block and 16 KB to the next block, an MN-major tile 16 rows of 128 bytes.
-__device__ __forceinline__ uint64_t k_step(uint64_t desc, int s) { return desc + (uint64_t)((s >> 2) * 1024 + (s & 3) * 2); }
-__device__ __forceinline__ uint64_t mn_step(uint64_t desc, int s) { return desc + (uint64_t)(s * 128); }
+__device__ __forceinline__ uint32_t step_of(bool mn, int s) { return mn ? 128u : s == 3 ? 1024u - 6u : 2u; }
 
 template <bool AMN, bool BMN>
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+    uint32_t alo = (uint32_t)a, blo = (uint32_t)b, acc = add;
 #pragma unroll 1
-    for (int s = 0; s < 8; ++s)
-        mma_lead(d, AMN ? mn_step(a, s) : k_step(a, s), BMN ? mn_step(b, s) : k_step(b, s), idesc, add || s > 0, lead);
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            mma_lead(d, alo, (uint32_t)(a >> 32), blo, (uint32_t)(b >> 32), idesc, acc, lead);
+            acc = 1u;
+            alo += step_of(AMN, s);
+            blo += step_of(BMN, s);
+        }
 }
 // A in tensor memory, 128 bf16 a row: 32 words from a on and 32 from a + 64 on
 __device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint64_t b_mn, uint32_t idesc, uint32_t lead) {
+    uint32_t blo = (uint32_t)b_mn, acc = 0u;
 #pragma unroll 1
-    for (int s = 0; s < 8; ++s) mma_lead_ta(d, a + 8 * s + 32 * (s >> 2), mn_step(b_mn, s), idesc, s > 0, lead);
+    for (int half = 0; half < 2; ++half, a += 64)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            mma_lead_ta(d, a + 8 * s, blo, (uint32_t)(b_mn >> 32), idesc, acc, lead);
+            acc = 1u;
+            blo += 128u;
+        }
 }
 
 // 8 words (bf16 pairs) a lane into tensor memory
