@@ -21,6 +21,7 @@
 // 32 B + [0, 32).
 #include <algorithm>
 
+#include "kda_launch.cuh"
 #include "kda_linear_tc.cuh"
 
 namespace kda {
@@ -117,6 +118,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_kernels_before();   // the images
     const uint32_t tbase = flags[0];
     const uint32_t tA = tbase, tB = tbase + 128, tQ = tbase + 256, tK = tbase + 384;   // scores / dV parts, dQ, dK
     const Abort ab{&flags[1], err};
@@ -521,10 +523,9 @@ cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, cons
     const cudaError_t e = cudaFuncSetAttribute(lin_grad_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
     if (e != cudaSuccess) return e;
     const int units = n_chunks * H;
-    lin_grad_tc<<<std::min(units, 148), kGradThreads, kGradSmem, s>>>(
-        mq, mk, mv, mdo, dec, mdq, mdk, mdv, chunks, units, H, images, d_images, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk,
-        (__nv_bfloat16*)dv, dec.per_head ? nullptr : (__nv_bfloat16*)dla, err);
-    return cudaGetLastError();
+    return launch_behind(lin_grad_tc, std::min(units, 148), kGradThreads, kGradSmem, s, mq, mk, mv, mdo, dec, mdq, mdk, mdv,
+                         chunks, units, H, images, d_images, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv,
+                         dec.per_head ? nullptr : (__nv_bfloat16*)dla, err);
 }
 
 }  // namespace kda

@@ -31,6 +31,7 @@
 // dv of a chunk to three blocks, which costs the pair products twice (16 units of 64^3
 // instead of 13 at 64 x 128) and puts dlog_alpha's last sums into a kernel of its own.
 // Decays are formed from g as a (hi, lo) pair.
+#include "kda_launch.cuh"
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -121,10 +122,19 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const Tin* __restr
     }
 }
 
-// ROWS x COLS of a matrix with `pitch` columns, fp32
+// fp32 that a kernel before this one wrote
+struct Written {
+    float x;
+};
+__device__ __forceinline__ void load_vec(const Written* p, float (&x)[4]) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+
+// ROWS x COLS of such a matrix with `pitch` columns
 template <int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void load_tile(float* dst, int ld, const float* __restrict__ src, int pitch) {
-    load_rows<float, ROWS, COLS, THREADS>(dst, ld, src, 0, ROWS, 1, 0, pitch, 0);
+__device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, int pitch) {
+    load_rows<Written, ROWS, COLS, THREADS>(dst, ld, reinterpret_cast<const Written*>(src), 0, ROWS, 1, 0, pitch, 0);
 }
 
 // The chunk's inclusive cumulative log decay as (hi, lo), by the first warp; tokens past
@@ -167,6 +177,7 @@ __global__ void __launch_bounds__(ROWS * 4) lin_update(UpdateSide<Tin> fwd, Upda
     constexpr int LDA = ROWS + 4;
     __shared__ __align__(16) float sa[kC * LDA], sb[kC * kLdP];
     __shared__ float gh[kC], gl[kC], w[kC];
+    let_next_kernel_start();
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
     const int h = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -204,8 +215,10 @@ struct ChainSide {
     const float* start;
     float* end;
 };
-__global__ void __launch_bounds__(kThreads) lin_chain(ChainSide fwd, ChainSide rev, const float* __restrict__ gam,
+__global__ void __launch_bounds__(kThreads) lin_chain(ChainSide fwd, ChainSide rev, const float* gam,
                                                       SeqMap smap, int H, int E4) {
+    let_next_kernel_start();
+    wait_for_kernels_before();
     const bool REV = blockIdx.z != 0;
     float* X = REV ? rev.X : fwd.X;
     const float* start = REV ? rev.start : fwd.start;
@@ -226,8 +239,8 @@ __global__ void __launch_bounds__(kThreads) lin_chain(ChainSide fwd, ChainSide r
         for (int j = 0; j < kAhead; ++j) {
             if (i0 + j < n) {
                 const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i0 - j : i0 + j)) * H + h;
-                u[j] = x4[unit * E4 + e];
-                g[j] = gam[unit];
+                u[j] = __ldcg(x4 + unit * E4 + e);
+                g[j] = __ldcg(gam + unit);
             }
         }
 #pragma unroll
@@ -253,7 +266,7 @@ template <int DK, int ROWS> constexpr size_t out_smem() {
 template <typename Tin, int DK, int ROWS>
 __global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, const Tin* __restrict__ k,
                                                     const Tin* __restrict__ v, LinDecay dec, ChunkMap cmap, int H, int DV,
-                                                    const float* __restrict__ S, Tin* __restrict__ o) {
+                                                    const float* S, Tin* __restrict__ o) {
     extern __shared__ __align__(16) float sm[];
     __shared__ float gh[kC], gl[kC];
     constexpr int LD = DK + 4;
@@ -262,11 +275,13 @@ __global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, c
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
     const int h = blockIdx.y, nv = DV / 64, v0 = (int)blockIdx.z % nv * 64, i0 = (int)blockIdx.z / nv * ROWS;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (i0 >= len) return;
+    if (i0 >= len) {
+        wait_for_kernels_before();
+        return;
+    }
     load_rows<Tin, ROWS, DK, ROWS * 4>(sq, LD, q, (long long)tok0 + i0, len - i0, H, h, DK, 0);
     load_rows<Tin, kC, DK, ROWS * 4>(sk, LD, k, tok0, len, H, h, DK, 0);
     load_rows<Tin, kC, 64, ROWS * 4>(sv, kLdP, v, tok0, len, H, h, DV, v0);
-    load_tile<DK, 64, ROWS * 4>(ss, kLdP, S + ((size_t)blockIdx.x * H + h) * DK * DV + v0, DV);
     chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
     __syncthreads();
     float acc[4][4];
@@ -279,6 +294,9 @@ __global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, c
             const int i = i0 + 4 * ty + r, j = tx + 16 * c;
             sp[(4 * ty + r) * kLdP + j] = j <= i ? acc[r][c] * exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
         }
+    wait_for_kernels_before();
+    load_tile<DK, 64, ROWS * 4>(ss, kLdP, S + ((size_t)blockIdx.x * H + h) * DK * DV + v0, DV);
+    __syncthreads();
     clear(acc);
     mm64<DK, false, false, false>(acc, sq, LD, ss, kLdP, ty, tx);
 #pragma unroll
@@ -287,7 +305,6 @@ __global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, c
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] *= e;
     }
-    __syncthreads();
     mm64<kC, false, false, false>(acc, sp, kLdP, sv, kLdP, ty, tx);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -326,13 +343,14 @@ struct DecayParts {
 template <typename Tin, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, LinDecay dec,
-         const Tin* __restrict__ d_o, ChunkMap cmap, int H, const float* __restrict__ S, const float* __restrict__ dS,
+         const Tin* __restrict__ d_o, ChunkMap cmap, int H, const float* S, const float* dS,
          Tin* __restrict__ dq, Tin* __restrict__ dk, Tin* __restrict__ dv, DecayParts parts) {
     extern __shared__ __align__(16) float sm[];
     __shared__ float gh[kC], gl[kC], w[kC], ra[kC], red[kThreads / 32];
     constexpr int LK = DK + 4, LV = DV + 4;
     float *sq = sm, *sk = sq + kC * LK, *sv = sk + kC * LK, *sd = sv + kC * LV;
     float *sp = sd + kC * LV, *sa = sp + kC * kLdP, *tile = sa + kC * kLdP;
+    let_next_kernel_start();
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
     const int h = blockIdx.y, role = blockIdx.z, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;   // dq, dk, dv
@@ -343,27 +361,10 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
     if (role < 2) load_rows<Tin, kC, DV, kThreads>(sv, LV, v, tok0, len, H, h, DV, 0);
     load_rows<Tin, kC, DV, kThreads>(sd, LV, d_o, tok0, len, H, h, DV, 0);
     chunk_decay<Tin>(gh, gl, dec, tok0, len, H, h);
-    if (role == 2) {
-        float e = 0.f;   // <dS', S>
-#pragma unroll 8
-        for (int u = tid; u < DK * DV / 4; u += kThreads) {
-            const float4 x = reinterpret_cast<const float4*>(Sn)[u], y = reinterpret_cast<const float4*>(dSn)[u];
-            e += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
-        if ((tid & 31) == 0) red[tid >> 5] = e;
-    }
     __syncthreads();
     if (tid < kC) {
         w[tid] = role == 0 ? exp_g(gh[tid], gl[tid]) : exp_gdiff(gh[kC - 1], gl[kC - 1], gh[tid], gl[tid]);
         ra[tid] = 0.f;
-    }
-    if (role == 2 && tid == 0) {
-        float whole = 0.f;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) whole += red[i];
-        parts.e[unit] = whole * exp_g(gh[kC - 1], gl[kC - 1]);
     }
     float p[4][4], a[4][4];
     clear(p);
@@ -380,7 +381,25 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
             sa[i * kLdP + j] = j <= i ? a[r][c] * d : 0.f;
             tile[i * kLdM + j] = j < i ? p[r][c] * a[r][c] * d : 0.f;
         }
+    wait_for_kernels_before();
+    if (role == 2) {
+        float e = 0.f;   // <dS', S>
+#pragma unroll 8
+        for (int u = tid; u < DK * DV / 4; u += kThreads) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(Sn) + u), y = __ldcg(reinterpret_cast<const float4*>(dSn) + u);
+            e += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+        if ((tid & 31) == 0) red[tid >> 5] = e;
+    }
     __syncthreads();
+    if (role == 2 && tid == 0) {
+        float whole = 0.f;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) whole += red[i];
+        parts.e[unit] = whole * exp_g(gh[kC - 1], gl[kC - 1]);
+    }
     if (role == 0) {   // r[t] = sum of the pair products over i >= t > j, four threads a row, then four a column
         const int i = tid >> 2, part = tid & 3;
         float* row = tile + i * kLdM + 16 * part;
@@ -470,14 +489,15 @@ template <typename Tin>
 __global__ void __launch_bounds__(128) lin_decay_grad(DecayParts parts, LinDecay dec, ChunkMap cmap, int n_units, int H,
                                                       Tin* __restrict__ dla) {
     const int unit = (int)blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    wait_for_kernels_before();
     if (unit >= n_units) return;
     int seq, tok0, len, idx;
     cmap.locate(unit / H, seq, tok0, len, idx);
     const int h = unit % H, t = 2 * lane;
-    const float2 a = reinterpret_cast<const float2*>(parts.a + (size_t)unit * kC)[lane];
-    const float2 b = reinterpret_cast<const float2*>(parts.b + (size_t)unit * kC)[lane];
-    const float2 r = reinterpret_cast<const float2*>(parts.r + (size_t)unit * kC)[lane];
-    const float whole = parts.e[unit];
+    const float2 a = __ldcg(reinterpret_cast<const float2*>(parts.a + (size_t)unit * kC) + lane);
+    const float2 b = __ldcg(reinterpret_cast<const float2*>(parts.b + (size_t)unit * kC) + lane);
+    const float2 r = __ldcg(reinterpret_cast<const float2*>(parts.r + (size_t)unit * kC) + lane);
+    const float whole = __ldcg(parts.e + unit);
     float suf = a.x + a.y, pre = b.x + b.y;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -514,7 +534,9 @@ cudaError_t update_and_chain(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, int sides
             lin_update<Tin, 64><<<dim3(n_chunks, H, tiles), kThreads, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv, gam);
     }
     const int e4 = dk * dv / 4;
-    lin_chain<<<dim3((unsigned)n_seqs * H, e4 / kThreads, sides), kThreads, 0, s>>>(cf, cr, gam, smap, H, e4);
+    const dim3 grid((unsigned)n_seqs * H, e4 / kThreads, sides);
+    if (n_chunks > 0) return launch_behind(lin_chain, grid, kThreads, 0, s, cf, cr, gam, smap, H, e4);
+    lin_chain<<<grid, kThreads, 0, s>>>(cf, cr, gam, smap, H, e4);
     return cudaGetLastError();
 }
 
@@ -525,9 +547,8 @@ cudaError_t outputs(const void* q, const void* k, const void* v, LinDecay dec, v
     constexpr size_t smem = out_smem<DK, ROWS>();
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    kern<<<dim3(n_chunks, H, dv / 64 * (kC / ROWS)), ROWS * 4, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec,
-                                                                        cmap, H, dv, ws.S, (Tin*)o);
-    return cudaGetLastError();
+    return launch_behind(kern, dim3(n_chunks, H, dv / 64 * (kC / ROWS)), ROWS * 4, smem, s, (const Tin*)q, (const Tin*)k,
+                         (const Tin*)v, dec, cmap, H, dv, ws.S, (Tin*)o);
 }
 
 template <typename Tin>
@@ -556,10 +577,11 @@ cudaError_t grad(const void* q, const void* k, const void* v, LinDecay dec, cons
     const int units = n_chunks * H;
     const size_t n = (size_t)units * kC;
     const DecayParts parts{ws.parts, ws.parts + n, ws.parts + 2 * n, ws.parts + 3 * n};
-    kern<<<dim3(n_chunks, H, 3), kThreads, smem, s>>>((const Tin*)q, (const Tin*)k, (const Tin*)v, dec, (const Tin*)d_o,
-                                                      cmap, H, ws.S, ws.dS, (Tin*)dq, (Tin*)dk, (Tin*)dv, parts);
-    if (!dec.per_head) lin_decay_grad<Tin><<<(units + 3) / 4, 128, 0, s>>>(parts, dec, cmap, units, H, (Tin*)dla);
-    return cudaGetLastError();
+    const cudaError_t st = launch_behind(kern, dim3(n_chunks, H, 3), kThreads, smem, s, (const Tin*)q, (const Tin*)k,
+                                         (const Tin*)v, dec, (const Tin*)d_o, cmap, H, ws.S, ws.dS, (Tin*)dq, (Tin*)dk,
+                                         (Tin*)dv, parts);
+    if (st != cudaSuccess || dec.per_head) return st;
+    return launch_behind(lin_decay_grad<Tin>, (units + 3) / 4, 128, 0, s, parts, dec, cmap, units, H, (Tin*)dla);
 }
 
 template <typename Tin>

@@ -29,6 +29,7 @@
 // are weighted with zero, V's are cleared, Q's only reach rows of o that are not stored.
 #include <algorithm>
 
+#include "kda_launch.cuh"
 #include "kda_linear_tc.cuh"
 
 namespace kda {
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, LinDecay dec, ChunkMap segs,
          const SeqInfo* __restrict__ order, int H, const float* __restrict__ init_state,
-         const float* __restrict__ seg_start, __nv_bfloat16* __restrict__ o,
+         const float* seg_start, __nv_bfloat16* __restrict__ o,
          float* __restrict__ final_state, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
@@ -164,6 +165,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         const int hb = warp >> 2, row = 32 * sp + lane;
         float s[HB];   // state row `row`, columns j0 + HB hb + [0, HB)
         {
+            if (seg_start) wait_for_kernels_before();
             const float* src = seg_start ? seg_start + ((size_t)seg * H + h) * kD * kD
                                : init_state ? init_state + ((size_t)seq * H + h) * kD * kD
                                             : nullptr;
@@ -478,7 +480,9 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    if (tid == 0 && blockIdx.x == 0 && clear_err) *err = 0;   // first kernel of the call
+    let_next_kernel_start();
+    if (!clear_err) wait_for_kernels_before();
+    else if (tid == 0 && blockIdx.x == 0) *err = 0;   // first kernel of the call
     if (smem_u32(sm) & 1023u) {
         if (tid == 0) atomicCAS(err, 0, (int)KDA_ERR_DEVICE);
         return;
@@ -680,8 +684,10 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
 // start state of every segment from the segments' own sums, in place (as the chunk chain
 // of the CUDA-core path, with segments for chunks)
 template <bool REV>
-__global__ void __launch_bounds__(256) seg_chain(float* __restrict__ X, const float* __restrict__ gam,
+__global__ void __launch_bounds__(256) seg_chain(float* X, const float* gam,
                                                  const float* __restrict__ start, SeqMap smap, int H) {
+    let_next_kernel_start();
+    wait_for_kernels_before();
     const SeqInfo sq = smap.get((int)blockIdx.x / H);
     const int h = (int)blockIdx.x % H, e = (int)blockIdx.y * 256 + threadIdx.x;
     const int n = (sq.len + smap.C - 1) / smap.C;
@@ -700,8 +706,8 @@ __global__ void __launch_bounds__(256) seg_chain(float* __restrict__ X, const fl
             g[j] = 0.f;
             if (i + 1 < n) {   // nothing follows the last segment: its own sum was not formed
                 const size_t unit = (size_t)(sq.chunk0 + (REV ? n - 1 - i : i)) * H + h;
-                u[j] = x4[unit * E4 + e];
-                g[j] = gam[unit];
+                u[j] = __ldcg(x4 + unit * E4 + e);
+                g[j] = __ldcg(gam + unit);
             }
         }
 #pragma unroll
@@ -758,15 +764,18 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
         const StateSide side{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
         lin_state<<<(unsigned)n_segs * H, kStateThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, nullptr, H, n_segs * H, side,
                                                                      side, 1, err);
-        seg_chain<false><<<dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s>>>(seg_state, seg_gam, init_state,
-                                                                                   smap, H);
+        e = launch_behind(seg_chain<false>, dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s, seg_state, seg_gam,
+                          init_state, smap, H);
+        if (e != cudaSuccess) return e;
     }
     auto kern = BV == 128 ? lin_walk<128> : lin_walk<64>;
     if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
+    if (split)
+        return launch_behind(kern, (unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s, mq, mk, mv, mo, dec, segs,
+                             nullptr, H, init_state, seg_state, (__nv_bfloat16*)o, final_state, err);
     // whole packed sequences go by the longest-first table, empty ones among them
-    const SeqInfo* order = split ? nullptr : smap.order;
-    kern<<<(unsigned)(order ? n_seqs : n_segs) * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
-        mq, mk, mv, mo, dec, segs, order, H, init_state, split ? seg_state : nullptr, (__nv_bfloat16*)o, final_state, err);
+    kern<<<(unsigned)(smap.order ? n_seqs : n_segs) * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
+        mq, mk, mv, mo, dec, segs, smap.order, H, init_state, nullptr, (__nv_bfloat16*)o, final_state, err);
     return cudaGetLastError();
 }
 
@@ -790,14 +799,17 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
         const StateSide r{nullptr, nullptr, d_seg, d_gam, nullptr, nullptr};
         lin_state<<<2u * units, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, nullptr, H, units, f, r, 1, err);
         const dim3 grid((unsigned)n_seqs * H, kD * kD / 1024);
-        seg_chain<false><<<grid, 256, 0, s>>>(seg_state, seg_gam, init_state, smap, H);
-        seg_chain<true><<<grid, 256, 0, s>>>(d_seg, d_gam, d_final, smap, H);
+        if ((e = launch_behind(seg_chain<false>, grid, 256, 0, s, seg_state, seg_gam, init_state, smap, H)) != cudaSuccess ||
+            (e = launch_behind(seg_chain<true>, grid, 256, 0, s, d_seg, d_gam, d_final, smap, H)) != cudaSuccess)
+            return e;
     }
     const StateSide f{init_state, split ? seg_state : nullptr, nullptr, nullptr, images, nullptr};
     const StateSide r{d_final, split ? d_seg : nullptr, nullptr, nullptr, d_images, d_init};
-    const SeqInfo* order = split ? nullptr : smap.order;
-    const int n = order ? n_seqs * H : units;
-    lin_state<<<2u * n, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, order, H, n, f, r, !split, err);
+    if (split)
+        return launch_behind(lin_state, 2u * units, kStateThreads, kStSmem, s, mk, mv, mq, mdo, dec, segs, nullptr, H, units,
+                             f, r, 0, err);
+    const int n = smap.order ? n_seqs * H : units;
+    lin_state<<<2u * n, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, smap.order, H, n, f, r, 1, err);
     return cudaGetLastError();
 }
 

@@ -22,6 +22,7 @@
 // a turn, exact to position * 2^-53 of a turn (fp32 would keep two digits at position 10^6);
 // sincospif of its top 32 bits.  Norm weight and rotation are multiplied once a token and
 // side, so a row costs one rotation and one scaling.
+#include "kda_launch.cuh"
 #include "kda_rope.cuh"
 
 namespace kda {
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_
     constexpr int LANES = D / 16, ROWS = 32 / LANES;
     constexpr int DEPTH = kBwdDepth<Tin>(), BYTES = stage_bytes<Tin, 4>(), VEC = pieces8<Tin>() * kPiece;
     extern __shared__ __align__(16) uint8_t sm[];
+    let_next_kernel_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
     float* acc = reinterpret_cast<float*>(sm);   // [2][kWarps * ROWS][D]
     uint8_t* stages = sm + 2 * kWarps * ROWS * D * 4 + warp * (DEPTH * BYTES + D / 2 * 8);
@@ -465,15 +467,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_
 
 // dw of one side a block row: 32 columns x 32 runs of partial rows
 template <typename Tw, int D>
-__global__ void __launch_bounds__(1024) norm_rope_dw(const float* __restrict__ partial, int n, void* dwq, void* dwk) {
+__global__ void __launch_bounds__(1024) norm_rope_dw(const float* partial, int n, void* dwq, void* dwk) {
     __shared__ float red[32][33];
+    wait_for_kernels_before();
     const int side = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
     void* out = side ? dwk : dwq;
     if (out == nullptr) return;
     float s = 0.f;
     const int per = (n + 31) / 32;
 #pragma unroll 8
-    for (int i = run * per; i < min(n, (run + 1) * per); ++i) s += partial[((size_t)i * 2 + side) * D + c];
+    for (int i = run * per; i < min(n, (run + 1) * per); ++i) s += __ldcg(partial + ((size_t)i * 2 + side) * D + c);
     red[run][threadIdx.x & 31] = s;
     __syncthreads();
     if (run == 0) {
@@ -499,7 +502,7 @@ cudaError_t run(const NormRopeArgs& A, bool inter, bool bwd, float* partial, int
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         kern<<<blocks, kThreads, smem, s>>>(A, dw ? partial : nullptr);
-        if (dw) norm_rope_dw<Tw, D><<<dim3(D / 32, 2), 1024, 0, s>>>(partial, blocks, dwq, dwk);
+        if (dw) return launch_behind(norm_rope_dw<Tw, D>, dim3(D / 32, 2), 1024, 0, s, partial, blocks, dwq, dwk);
     }
     return cudaGetLastError();
 }
