@@ -183,15 +183,48 @@ kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_s
     return KDA_OK;
 }
 
+// The tables of a few sequences in one launch (2 KB of parameters): the sequence table and,
+// from the parameters too, the chunk table, which otherwise waits for the first.
+constexpr int kFewSeqs = 64;
+struct FewSeqs {
+    SeqInfo e[2 * kFewSeqs];   // natural order, then longest first
+};
+__global__ void __launch_bounds__(256) few_tables_write(SeqInfo* __restrict__ seqs, int n_seqs, int n_chunks, int C,
+                                                        int4* __restrict__ chunks, const __grid_constant__ FewSeqs b) {
+    const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+    if (c < 2 * n_seqs) seqs[c] = b.e[c];
+    if (c >= n_chunks) return;
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {   // last sequence whose first chunk is <= c
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.e[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+    }
+    const SeqInfo sq = b.e[lo];
+    const int idx = c - sq.chunk0;
+    chunks[c] = make_int4(sq.tok0 + idx * C, min(C, sq.len - idx * C), sq.seq, idx);
+}
+
+cudaError_t write_tables(const Plan& p, int n_chunks, int C, SeqInfo* ws, cudaStream_t s) {
+    cudaError_t err;
+    if (p.n_seqs > kFewSeqs) {
+        upload_tables(ws, p.natural, p.by_len, n_chunks, C, s, &err);
+        return err;
+    }
+    FewSeqs b;
+    std::copy(p.natural.begin(), p.natural.end(), b.e);
+    std::copy(p.by_len.begin(), p.by_len.end(), b.e + p.n_seqs);
+    few_tables_write<<<std::max(1, (n_chunks + 255) / 256), 256, 0, s>>>(ws, p.n_seqs, n_chunks, C,
+                                                                        chunk_table(ws, p.n_seqs), b);
+    return cudaGetLastError();
+}
+
 kda_status make_maps(const Plan& p, int T, int C, char* ws, cudaStream_t s, ChunkMap& cmap, SeqMap& smap,
                      bool chunk_entries = true) {
     const int ncps = (int)(((long long)T + C - 1) / C);
     cmap = ChunkMap{nullptr, p.n_seqs, T, C, ncps};
     smap = SeqMap{nullptr, T, C, ncps};
     if (p.varlen) {
-        cudaError_t err;
-        upload_tables((SeqInfo*)ws, p.natural, p.by_len, chunk_entries ? p.n_chunks : 0, C, s, &err);
-        if (err != cudaSuccess) return KDA_ERR_CUDA;
+        if (write_tables(p, chunk_entries ? p.n_chunks : 0, C, (SeqInfo*)ws, s) != cudaSuccess) return KDA_ERR_CUDA;
         cmap.seqs = (const SeqInfo*)ws;
         if (chunk_entries) cmap.chunks = chunk_table((SeqInfo*)ws, p.n_seqs);
         smap.order = (const SeqInfo*)ws + p.n_seqs;

@@ -528,10 +528,19 @@ cudaError_t update_and_chain(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, int sides
                              float* gam, cudaStream_t s) {
     if (n_chunks > 0) {
         const int tiles = (dk / 64) * (dv / 64) * sides;
-        if (small_grid((long long)n_chunks * H * tiles))
-            lin_update<Tin, 16><<<dim3(n_chunks, H, 4 * tiles), 64, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv, gam);
-        else
-            lin_update<Tin, 64><<<dim3(n_chunks, H, tiles), kThreads, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv, gam);
+        const bool small = small_grid((long long)n_chunks * H * tiles);
+        auto update = small ? lin_update<Tin, 16> : lin_update<Tin, 64>;
+        if (sides == 2) {
+            // The gradient kernel's 90 to 200 KB of shared memory can only come onto an SM beside
+            // these two if the SM is divided for that already (50 -> 46 us for 14 chunks x 3 heads).
+            cudaError_t e;
+            const auto all = cudaFuncAttributePreferredSharedMemoryCarveout;
+            if ((e = cudaFuncSetAttribute(update, all, cudaSharedmemCarveoutMaxShared)) != cudaSuccess ||
+                (e = cudaFuncSetAttribute(lin_chain, all, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+                return e;
+        }
+        update<<<dim3(n_chunks, H, small ? 4 * tiles : tiles), small ? 64 : kThreads, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv,
+                                                                                             gam);
     }
     const int e4 = dk * dv / 4;
     const dim3 grid((unsigned)n_seqs * H, e4 / kThreads, sides);
