@@ -120,7 +120,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     if (tid == 0) {
         for (int i = 0; i < kWalkBars; ++i)   // one arrival a warp
             mbar_init(&bars[i], i == kPReady || i == kPReady + 1 || i == kKReady || i == kSReady || i == kORead ? 8
-                                : i == kGEmpty || i == kGEmpty + 1 ? 24 : 1);
+                                : i == kGEmpty || i == kGEmpty + 1 ? 24
+                                : BV == 64 && (i == kFull + 1 || i == kFull + 4) ? 2 : 1);   // Q and K
         mbar_init_fence();
         flags[1] = 0u;
     }
@@ -147,7 +148,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         return kind == 2 ? 4 * kTile + second * kBlock : (2 * kind + second) * kTile;
     };
     auto slot = [&](int i) { return sm + offset(i); };
-    auto full = [&](int i) { return &bars[kFull + i % kRing]; };
+    // (half the value columns: a chunk's Q and K share K's barrier)
+    auto full = [&](int i) { return &bars[kFull + (BV == 64 && i % 3 == 0 ? i + 1 : i) % kRing]; };
     auto empty = [&](int i) { return kEmpty + i % kRing; };
     auto full_par = [&](int i) { return (uint32_t)(i / kRing) & 1u; };
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
@@ -354,17 +356,22 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         auto commit = [&](int bar) {
             if (lead) mma_commit(&bars[bar]);
         };
+        // The products' warp is the one that the chunks' time hangs on, and a wait costs it 100 to
+        // 200 cycles even when there is nothing to wait for; so it looks at as few barriers as
+        // will do (eight a chunk -> five with half the value columns).
         auto scores = [&](int n) {   // A = Q K^T
-            if (!wait_or_abort(full(3 * n), full_par(3 * n), ab) || !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
+            if ((BV == 128 && !wait_or_abort(full(3 * n), full_par(3 * n), ab)) ||
+                !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
                 return false;
             product<false, false>(tA(n), sw128_desc(base + offset(3 * n)), sw128_desc(base + offset(3 * n + 1)), iS, false,
                                   lead);
             commit(kScores + (n & 1));
             return true;
         };
-        auto values = [&](int n) {   // P V
-            if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab) || !wait_or_abort(&bars[kPReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) ||
-                (n > 0 && !wait_or_abort(&bars[kORead], (uint32_t)(n + 1) & 1u, ab)))
+        auto o_read = [&](int n) { return n < 0 || wait_or_abort(&bars[kORead], (uint32_t)n & 1u, ab); };
+        auto values = [&](int n) {   // P V (BV = 64: the weighted values, which U has waited for, come from V)
+            if ((BV == 128 && !wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) ||
+                !wait_or_abort(&bars[kPReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) || (BV == 128 && !o_read(n - 1)))
                 return false;
             tc_fence_after();
             product_ta(tPV, tA(n), mn_desc_k(base + offset(3 * n + 2), kT, 0), iB, lead);
@@ -393,8 +400,9 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                 commit(empty(3 * n + 2));
                 if (n + 1 < nch && !(ok = wait_or_abort(&bars[kODone], (uint32_t)n & 1u, ab) && scores(n + 1))) break;
             } else {
-                // over the scores of the last chunk but one, whose P V is done
-                if (n > 0 && !(ok = wait_or_abort(&bars[kODone], (uint32_t)(n + 1) & 1u, ab))) break;
+                // over the scores of the last chunk but one: o of that one has been read, so its
+                // P V is done, and this one's may go over it
+                if (!(ok = o_read(n - 1))) break;
                 if (n + 1 < nch && !(ok = scores(n + 1))) break;
                 if (!(ok = values(n))) break;
                 commit(empty(3 * n + 2));
