@@ -39,7 +39,7 @@ constexpr int kSms = 148;
 // half of them, and the state alone; a block's start and end; and what a split adds (the
 // segments' chain, two more launches).  From 1 to 10 segments a sequence, 8 to 512 chunks
 // and 16 to 704 blocks, times estimated with these are within 15 % of the measured ones.
-constexpr double kWalk128 = 3.2, kWalk64 = 2.25, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
+constexpr double kWalk128 = 3.2, kWalk64 = 2.1, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
 
 long long longest_of(const Plan& chunks) {   // chunks of the longest sequence
     long long longest = 0;

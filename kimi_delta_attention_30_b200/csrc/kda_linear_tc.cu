@@ -77,8 +77,11 @@ constexpr uint32_t kOffBars = kOffGates + 2 * sizeof(Gates);
 constexpr uint32_t kWalkSmem = kOffBars + 256;
 static_assert(kWalkSmem <= 232448, "shared memory per block");
 
-enum WalkBar { kFull = 0, kEmpty = kSlots, kScores = 2 * kSlots, kPReady = kScores + 2, kQsDone = kPReady + 2, kKReady, kODone, kORead, kUDone, kSReady,
-               kGFull, kGEmpty = kGFull + 2, kDrain = kGEmpty + 2, kWalkBars };
+// Barriers in pairs are used by turns, one chunk the one and the next the other: what waits for
+// one may come late by a chunk, but never by two.
+enum WalkBar { kFull = 0, kScores = kSlots, kPReady = kScores + 2, kQsDone = kPReady + 2, kUDone = kQsDone + 2,
+               kODone = kUDone + 2, kGFull = kODone + 2, kGEmpty = kGFull + 2, kKReady = kGEmpty + 2, kORead, kSReady,
+               kDrain, kWalkBars };
 
 template <int BV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
@@ -121,7 +124,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         for (int i = 0; i < kWalkBars; ++i)   // one arrival a warp
             mbar_init(&bars[i], i == kPReady || i == kPReady + 1 || i == kKReady || i == kSReady || i == kORead ? 8
                                 : i == kGEmpty || i == kGEmpty + 1 ? 24
-                                : BV == 64 && (i == kFull + 1 || i == kFull + 4) ? 2 : 1);   // Q and K
+                                : BV == 64 && i < kFull + 2 ? 2 : 1);   // Q and K
         mbar_init_fence();
         flags[1] = 0u;
     }
@@ -138,24 +141,21 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     auto tA = [&](int n) { return BV == 128 ? tbase : tbase + 128 * (n & 1); };
     auto tQS = [&](int n) { return BV == 128 ? tbase + 128 : tbase + 384 + 64 * (n & 1); };
     const Abort ab{&flags[1], err};
-    // Tile i: Q 3 n, K 3 n + 1, V 3 n + 2.  Five slots in turn (Q's is free first and takes the
-    // next V); with half the value columns there is room for two of each kind.
-    constexpr int kRing = BV == 128 ? 5 : 6;
-    auto offset = [&](int i) {
-        const uint32_t x = (uint32_t)i % kRing;
-        if (BV == 128) return x * kTile;
-        const uint32_t kind = x % 3, second = x / 3;
-        return kind == 2 ? 4 * kTile + second * kBlock : (2 * kind + second) * kTile;
+    // Where a chunk's tiles stand (kind 0 Q, 1 K, 2 V): five slots in turn (Q's is free first and
+    // takes the next V); with half the value columns there is room for two of each kind, and a
+    // chunk's Q and K share a barrier.
+    enum { Q, K, V };
+    auto offset = [&](int kind, int n) -> uint32_t {
+        if (BV == 128) return (uint32_t)(3 * n + kind) % 5u * kTile;
+        return kind == V ? 4 * kTile + (n & 1) * kBlock : (2 * kind + (n & 1)) * kTile;
     };
-    auto slot = [&](int i) { return sm + offset(i); };
-    // (half the value columns: a chunk's Q and K share K's barrier)
-    auto full = [&](int i) { return &bars[kFull + (BV == 64 && i % 3 == 0 ? i + 1 : i) % kRing]; };
-    auto empty = [&](int i) { return kEmpty + i % kRing; };
-    auto full_par = [&](int i) { return (uint32_t)(i / kRing) & 1u; };
+    auto full = [&](int kind, int n) {
+        return &bars[kFull + (BV == 128 ? (int)((uint32_t)(3 * n + kind) % 5u) : 2 * (kind == V) + (n & 1))];
+    };
+    auto full_par = [&](int kind, int n) { return BV == 128 ? (uint32_t)(3 * n + kind) / 5u & 1u : (uint32_t)(n >> 1) & 1u; };
+    auto wait_full = [&](int kind, int n) { return wait_or_abort(full(kind, n), full_par(kind, n), ab); };
+    auto wait_pair = [&](int bar, int n) { return wait_or_abort(&bars[bar + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
-    auto gates_full = [&](int n) { return wait_or_abort(&bars[kGFull + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
-    // two barriers by turns: the next chunk's scores may be done before a warp looks
-    auto scores_done = [&](int n) { return wait_or_abort(&bars[kScores + (n & 1)], (uint32_t)(n >> 1) & 1u, ab); };
     const int sp = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * sp) << 16;
 
@@ -195,8 +195,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         };
         // o = P V + e^g (Q S)
         auto outputs = [&](int n, float eg) {
-            if (!wait_or_abort(&bars[kODone], (uint32_t)n & 1u, ab) ||   // BV = 64: Q S was issued before P V
-                (BV == 128 && !wait_or_abort(&bars[kQsDone], (uint32_t)n & 1u, ab)))
+            if (!wait_pair(kODone, n) || (BV == 128 && !wait_pair(kQsDone, n)))   // BV = 64: P V comes last
                 return false;
             tc_fence_after();
             // A lane's row in pieces of 32 bytes, straight to global memory, would cost the
@@ -243,11 +242,11 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         publish();
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
-            if (!(ok = gates_full(n))) break;
+            if (!(ok = wait_pair(kGFull, n))) break;
             const float gam = gates[n & 1].gam, eg = ex2_approx(gates[n & 1].rel2[row]) * gates[n & 1].start[sp];
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
             if (BV == 128 && !(ok = outputs(n, eg))) break;
-            if (!(ok = wait_or_abort(&bars[kUDone], (uint32_t)n & 1u, ab))) break;
+            if (!(ok = wait_pair(kUDone, n))) break;
             tc_fence_after();
 #pragma unroll
             for (int g = 0; g < HB / 16; ++g) {
@@ -270,22 +269,21 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     } else if (warp < 16) {   // ---- the weighted keys, or values
         const int blk = (warp >> 2) & 1, r = tid & 127;
         for (int n = 0; n < nch; ++n) {
-            const uint32_t par = (uint32_t)n & 1u;
             const int live = min(kT, len - n * kT);
-            if (!gates_full(n)) break;
+            if (!wait_pair(kGFull, n)) break;
             const float w = gates[n & 1].col[r] * gates[n & 1].end[r >> 5];
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
-            if (n > 0 && !wait_or_abort(&bars[kUDone], par ^ 1u, ab)) break;   // the last U has read the parts
+            if (n > 0 && !wait_pair(kUDone, n - 1)) break;   // the last U has read the parts
             if (BV == 128) {   // in place: the scores have read the keys
-                if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab) || !scores_done(n)) break;
-                uint8_t* tile = slot(3 * n + 1) + blk * kBlock;
+                if (!wait_full(K, n) || !wait_pair(kScores, n)) break;
+                uint8_t* tile = sm + offset(K, n) + blk * kBlock;
                 scale_split_row<8>(tile, tile, sm + kOffLo + blk * kBlock, r, 0, w, r < live);
             } else {           // half the columns, into a buffer of their own (P V needs the values)
-                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
-                scale_split_row<4>(slot(3 * n + 2), sm + kOffLo, sm + kOffLo + kBlock, r, 4 * blk, w, r < live);
+                if (!wait_full(V, n)) break;
+                scale_split_row<4>(sm + offset(V, n), sm + kOffLo, sm + kOffLo + kBlock, r, 4 * blk, w, r < live);
                 if (live < kT) {   // the keys' rows of the next sequence meet weights of zero
-                    if (!wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab)) break;
-                    zero_rows(slot(3 * n + 1), 2, live, tid - 256, 256);
+                    if (!wait_full(K, n)) break;
+                    zero_rows(sm + offset(K, n), 2, live, tid - 256, 256);
                 }
             }
             fence_async_smem();
@@ -295,15 +293,15 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         const int hb = (warp >> 2) & 1, row = 32 * sp + lane;
         for (int n = 0; n < nch; ++n) {
             const int live = min(kT, len - n * kT);
-            if (!gates_full(n)) break;
+            if (!wait_pair(kGFull, n)) break;
             if (live < kT) {
-                if (!wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) break;
-                zero_rows(slot(3 * n + 2), BV / 64, live, tid - 640, 256);
+                if (!wait_full(V, n)) break;
+                zero_rows(sm + offset(V, n), BV / 64, live, tid - 640, 256);
                 fence_async_smem();
             }
             const Gates& G = gates[n & 1];
             const float r2 = G.rel2[row], er = ex2_approx(r2);
-            if (!scores_done(n)) break;
+            if (!wait_pair(kScores, n)) break;
             tc_fence_after();
             // this thread's row, 64 keys, 32 at a time; P's words go over scores already read
 #pragma unroll 1
@@ -353,29 +351,22 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         constexpr uint32_t iS = idesc_bf16_f32(128, 128), iB = idesc_bf16_f32_bmn(128, BV), iU = idesc_amn_bmn(128, BV);
         const uint32_t lead = elect_lane();
         const uint32_t base = smem_u32(sm), lo = base + kOffLo, st = base + kOffS;
-        auto commit = [&](int bar) {
-            if (lead) mma_commit(&bars[bar]);
-        };
+        auto commit = [&](int bar) { commit_lead(&bars[bar], lead); };
         // The products' warp is the one that the chunks' time hangs on, and a wait costs it 100 to
         // 200 cycles even when there is nothing to wait for; so it looks at as few barriers as
-        // will do (eight a chunk -> five with half the value columns).
+        // will do (with half the value columns, five a chunk instead of eight).
         auto scores = [&](int n) {   // A = Q K^T
-            if ((BV == 128 && !wait_or_abort(full(3 * n), full_par(3 * n), ab)) ||
-                !wait_or_abort(full(3 * n + 1), full_par(3 * n + 1), ab))
-                return false;
-            product<false, false>(tA(n), sw128_desc(base + offset(3 * n)), sw128_desc(base + offset(3 * n + 1)), iS, false,
-                                  lead);
+            if ((BV == 128 && !wait_full(Q, n)) || !wait_full(K, n)) return false;
+            product<false, false>(tA(n), sw128_desc(base + offset(Q, n)), sw128_desc(base + offset(K, n)), iS, false, lead);
             commit(kScores + (n & 1));
             return true;
         };
         auto o_read = [&](int n) { return n < 0 || wait_or_abort(&bars[kORead], (uint32_t)n & 1u, ab); };
         auto values = [&](int n) {   // P V (BV = 64: the weighted values, which U has waited for, come from V)
-            if ((BV == 128 && !wait_or_abort(full(3 * n + 2), full_par(3 * n + 2), ab)) ||
-                !wait_or_abort(&bars[kPReady + (n & 1)], (uint32_t)(n >> 1) & 1u, ab) || (BV == 128 && !o_read(n - 1)))
-                return false;
+            if ((BV == 128 && !wait_full(V, n)) || !wait_pair(kPReady, n) || (BV == 128 && !o_read(n - 1))) return false;
             tc_fence_after();
-            product_ta(tPV, tA(n), mn_desc_k(base + offset(3 * n + 2), kT, 0), iB, lead);
-            commit(kODone);
+            product_ta(tPV, tA(n), mn_desc_k(base + offset(V, n), kT, 0), iB, lead);
+            commit(kODone + (n & 1));
             return true;
         };
         bool ok = scores(0);
@@ -384,28 +375,24 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             // Q S
             if (!(ok = wait_or_abort(&bars[kSReady], (uint32_t)n & 1u, ab))) break;
             tc_fence_after();
-            product<false, true>(tQS(n), sw128_desc(base + offset(3 * n)), mn_desc_k(st, kD, 0), iB, false, lead);
-            if (BV == 128) commit(kQsDone);
-            commit(empty(3 * n));
+            product<false, true>(tQS(n), sw128_desc(base + offset(Q, n)), mn_desc_k(st, kD, 0), iB, false, lead);
+            if (BV == 128) commit(kQsDone + (n & 1));
             // K^T V with the weights, high then low parts
             if (!(ok = wait_or_abort(&bars[kKReady], (uint32_t)n & 1u, ab))) break;
             tc_fence_after();
-            const uint64_t dk = mn_desc_k(base + offset(3 * n + 1), kT, 0), dv = mn_desc_k(base + offset(3 * n + 2), kT, 0);
+            const uint64_t dk = mn_desc_k(base + offset(K, n), kT, 0), dv = mn_desc_k(base + offset(V, n), kT, 0);
             const uint64_t dl = mn_desc_k(lo, kT, 0);
             product<true, true>(tU, dk, BV == 128 ? dv : dl, iU, false, lead);
             product<true, true>(tU, BV == 128 ? dl : dk, BV == 128 ? dv : mn_desc_k(lo + kBlock, kT, 0), iU, true, lead);
-            commit(kUDone);
-            commit(empty(3 * n + 1));
+            commit(kUDone + (n & 1));
             if (BV == 128) {
-                commit(empty(3 * n + 2));
-                if (n + 1 < nch && !(ok = wait_or_abort(&bars[kODone], (uint32_t)n & 1u, ab) && scores(n + 1))) break;
+                if (n + 1 < nch && !(ok = wait_pair(kODone, n) && scores(n + 1))) break;
             } else {
                 // over the scores of the last chunk but one: o of that one has been read, so its
                 // P V is done, and this one's may go over it
                 if (!(ok = o_read(n - 1))) break;
                 if (n + 1 < nch && !(ok = scores(n + 1))) break;
                 if (!(ok = values(n))) break;
-                commit(empty(3 * n + 2));
             }
         }
         if (!ok) {   // given up: products in flight end before the tensor memory is freed
@@ -414,24 +401,32 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         }
     } else if (warp == 17) {
         if (lane == 0) {   // ---- loads
-            int i = 0;
+            // A slot is free when the last product that reads its tile is done.
+            constexpr int kRing = BV == 128 ? 5 : 6;
+            int i = 0;   // tile 3 n + kind
             bool ok = true;
             for (; i < 3 * nch; ++i) {
-                const int t = tok0 + (i / 3) * kT, kind = i % 3;
-                const CUtensorMap* m = kind == 0 ? &mq : kind == 1 ? &mk : &mv;
-                if (i >= kRing && !(ok = wait_or_abort_lane(&bars[empty(i)], full_par(i) ^ 1u, ab))) break;
-                uint8_t* dst = slot(i);
-                if (kind < 2 || BV == 128) {
-                    mbar_arrive_expect_tx(full(i), kTile);
-                    tma_box(dst, m, 0, h, t, full(i));
-                    tma_box(dst + kBlock, m, 64, h, t, full(i));
+                const int n = i / 3, kind = i % 3;
+                if (i >= kRing) {
+                    const int m = (i - kRing) / 3, was = (i - kRing) % 3;   // the tile before in this slot
+                    const int bar = BV == 128 ? (was == Q ? kQsDone : kUDone) : was == V ? kODone : kUDone;
+                    if (!(ok = wait_or_abort_lane(&bars[bar + (m & 1)], (uint32_t)(m >> 1) & 1u, ab))) break;
+                }
+                const CUtensorMap* map = kind == Q ? &mq : kind == K ? &mk : &mv;
+                uint8_t* dst = sm + offset(kind, n);
+                uint64_t* bar = full(kind, n);
+                const int t = tok0 + n * kT;
+                if (kind != V || BV == 128) {
+                    mbar_arrive_expect_tx(bar, kTile);
+                    tma_box(dst, map, 0, h, t, bar);
+                    tma_box(dst + kBlock, map, 64, h, t, bar);
                 } else {
-                    mbar_arrive_expect_tx(full(i), kBlock);
-                    tma_box(dst, m, j0, h, t, full(i));
+                    mbar_arrive_expect_tx(bar, kBlock);
+                    tma_box(dst, map, j0, h, t, bar);
                 }
             }
             if (!ok)   // given up: the copies in flight land before the block ends
-                for (int j = max(0, i - kRing); j < i; ++j) mbar_wait(full(j), full_par(j));
+                for (int j = max(0, i - kRing); j < i; ++j) mbar_wait(full(j % 3, j / 3), full_par(j % 3, j / 3));
         }
     } else if (warp == 18) {   // ---- decays
         float x[4], y[4];

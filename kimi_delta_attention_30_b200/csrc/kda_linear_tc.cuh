@@ -76,6 +76,15 @@ __device__ __forceinline__ void mma_lead_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate), "r"(lead));
 }
 
+// Arrival on `bar` once the products issued so far are done; the same lane as theirs.
+__device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
 __host__ __device__ constexpr uint32_t idesc_amn_bmn(int M, int N) {
     return idesc_bf16_f32(M, N) | (1u << 15) | (1u << 16);
 }
