@@ -500,10 +500,12 @@ typedef enum {
  * final_state may alias init_state; o must not overlap an input.  Packed batches
  * (cu_seqlens_host, B = 1) and empty sequences as in kda_chunk_fwd.  bf16 with
  * dk = dv = 128 runs on the tensor cores: products of bf16 operands with fp32
- * accumulation; the state's update takes the decayed keys as a bf16 pair (16
- * bits), so states keep fp32-like accuracy, while the scores and the state's
- * copy that the queries read are rounded to bf16 once, as o itself is.  Other
- * shapes and fp32 run in fp32 on the CUDA cores.  H <= 65535.
+ * accumulation; the state's update takes the decayed keys (or values) as a bf16
+ * pair, 16 bits, which leaves some 5e-6 relative in the fp32 states, while the
+ * scores and the state's copy that the queries read are rounded to bf16 once, as
+ * o itself is.  Other shapes and fp32 run in fp32 on the CUDA cores.  Inputs are
+ * finite: an infinity or NaN reaches its whole chunk (up to 128 tokens) and what
+ * follows it in the sequence, but no other sequence.  H <= 65535.
  * Errors as kda_chunk_fwd; an unknown decay is KDA_ERR_SHAPE.
  */
 KDA_API size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
@@ -567,8 +569,9 @@ KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const vo
  *                  16 bytes; written rows must not overlap one another; q_out may
  *                  be q itself and k_out k itself (same strides)
  *   q_weight, k_weight : device [d] of weight_dtype, or NULL (ones)
- *   positions    : device [T] int32, any value (angles are reduced in fp64)
- *   inv_freq     : device [rot / 2] fp32, angle per position
+ *   positions    : device [T] int32, any value (angles are reduced exactly, to
+ *                  position * 2^-53 of a turn)
+ *   inv_freq     : device [rot / 2] fp32, angle per position, finite
  *   d            : 64 or 128; rot : 0 (norm alone; positions and inv_freq may be
  *                  NULL) or a multiple of 16 up to d; Hq, Hk 1 .. 65535
  *   eps          : >= 0; with eps = 0 an all-zero row stays zero

@@ -447,7 +447,7 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, c
     kda_status st = check_decay(decay);
     if (st != KDA_OK) return st;
     if (N < 0 || H <= 0 || !((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return KDA_ERR_SHAPE;
-    if ((long long)N * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if ((long long)N * H * (dv / 32) > 0x7fffffffLL) return KDA_ERR_SHAPE;   // the grid
     if (N == 0) return KDA_OK;
     if (!q || !k || !v || !log_alpha || !state || !o) return KDA_ERR_NULL;
     if (!all_aligned({q, k, v, log_alpha, (const void*)state, (const void*)o})) return KDA_ERR_ALIGN;

@@ -13,8 +13,9 @@
 //
 // Eight products of 128^3 a chunk (4096 tensor cycles) against 288 KB of memory traffic
 // (6.6 us an SM at the measured copy rate): bound by memory as long as loads overlap the
-// work.  A block keeps one chunk in six 32 KB slots; a slot is loaded for the block's next
-// chunk as soon as nothing needs it.  P and B replace S and V.  The results leave through
+// work.  2048 (chunk, head) units take 138 us, 4.3 TB/s; of a unit's 17 K cycles the
+// elementwise warps spend 14 K, and 3 K waiting for the next Q and K.  A block keeps one chunk
+// in six 32 KB slots; a slot is loaded for the block's next chunk as soon as nothing needs it.  P and B replace S and V.  The results leave through
 // slots too (dV Z's, dQ K's, dK Q's: free by then, and needed last by the next chunk), one box
 // a warp: stored from registers, a row a lane, they held the load/store pipe for 3000 cycles.
 // 16 warps do the elementwise work: warp (R, B) owns rows 32 R + lane and columns

@@ -16,15 +16,22 @@
 //
 // Roles, each with its own barriers, so that they work on different chunks at once: 8 warps
 // form o and keep the state (warp w: rows 32 (w % 4) + lane, column half w / 4), 8 weight the
-// keys, 8 turn scores into P, one issues the products, one the loads, one forms the decays.
-// The state itself is off the critical path: U needs no state, so the chain from chunk to
-// chunk is one multiply-add and the copy for the next queries.  Products are issued in the
-// order P V, Q S, Q K^T of the next chunk, U: the first three run while the keys are weighted
-// (which waits for the last U to release the low parts' buffer), P of the next chunk is
-// formed meanwhile.  Five 32 KB slots hold Q, K, V in turn (Q's slot is free first and takes
-// the next V).  A 128 x 128 x 16 product reads 8 KB in the 64 cycles it takes, which is all
-// that shared memory gives, so products, the loads' writes and the weighting share 128 bytes
-// a cycle.
+// keys (or values), 8 turn scores into P, one issues the products, one the loads, one forms
+// the decays.  The state is off the products' path: U needs no state, so the chain from chunk
+// to chunk is one multiply-add and the copy for the next queries.
+//   All 128 value columns a block: five 32 KB slots hold Q, K, V in turn; products in the order
+//   P V, Q S, U, then Q K^T of the next chunk (the keys are weighted in place, behind the
+//   scores).  A chunk moves 576 KB through shared memory, 4500 cycles at 128 bytes a cycle, of
+//   5500 seen; 148 blocks of 32 chunks take 112 to 118 us, 5.3 to 5.5 TB/s, 0.82 to 0.85 of
+//   the copy rate.
+//   Half of them, where the pairs of sequence and head are fewer than the SMs: two chunks of
+//   each operand and two sets of scores; products in the order Q S, U, then Q K^T of the next
+//   chunk and P V, which give the state's warps time for S (86 us for 64 pairs of 32 chunks)
+//   and, with 32-bit descriptor steps (78 us) and five waits a chunk instead of eight (73 us),
+//   bring a chunk to 3700 cycles of 1920 that the products take alone: it is bound by
+//   latencies around the one warp that issues them.  98 us with all columns a block.  Two
+//   warps issuing (one Q S and U, the other Q K^T and P V) took 87 us instead of 78: the
+//   second's products delay the state's.
 // Rows past a sequence's end are loaded with the box (they belong to the next sequence); K's
 // are weighted with zero, V's are cleared, Q's only reach rows of o that are not stored.
 #include <algorithm>

@@ -159,6 +159,12 @@ struct Scratch {
     }
 };
 
+bool truth(PyObject* o) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) throw PythonError();
+    return t != 0;
+}
+
 std::vector<int32_t> offsets(PyObject* cu) {   // a list or tuple of ints
     std::vector<int32_t> v;
     if (cu == Py_None) return v;
@@ -249,7 +255,7 @@ PyObject* linear_chunk_fwd(PyObject* const* a) {
     Call c(L.dev, a[10]);
     const at::Tensor o = output(c, "o", a[7], L.dt, L.v.sizes());
     at::Tensor fs;
-    if (a[8] != Py_None || PyObject_IsTrue(a[6])) fs = output(c, "final_state", a[8], at::kFloat, st);
+    if (a[8] != Py_None || truth(a[6])) fs = output(c, "final_state", a[8], at::kFloat, st);
     const Scratch w(c, a[9], [&] {
         return kda_linear_chunk_fwd_workspace_size(L.B, L.T, L.H, L.dk, L.dv, L.type, L.cu_ptr(), L.n_seqs());
     });
@@ -268,14 +274,14 @@ PyObject* linear_chunk_bwd(PyObject* const* a) {
     void* init = dense("init_state", a[5], L.dev, at::kFloat, st);
     void* pdf = dense("d_final_state", a[6], L.dev, at::kFloat, st);
     Call c(L.dev, a[16]);
-    const bool given = PyObject_IsTrue(a[14]);
+    const bool given = truth(a[14]);
     at::Tensor dq, dk, dv, dla, ds;
     if (!given || a[9] != Py_None) dq = output(c, "dq", a[9], L.dt, L.q.sizes());
     if (!given || a[10] != Py_None) dk = output(c, "dk", a[10], L.dt, L.k.sizes());
     if (!given || a[11] != Py_None) dv = output(c, "dv", a[11], L.dt, L.v.sizes());
     if (given ? a[12] != Py_None : L.decay == KDA_DECAY_TOKEN)
         dla = output(c, "dlog_alpha", a[12], L.la.scalar_type(), L.la.sizes());
-    if (given ? a[13] != Py_None : PyObject_IsTrue(a[8])) ds = output(c, "d_init_state", a[13], at::kFloat, st);
+    if (given ? a[13] != Py_None : truth(a[8])) ds = output(c, "d_init_state", a[13], at::kFloat, st);
     const Scratch w(c, a[15], [&] {
         return kda_linear_chunk_bwd_workspace_size(L.B, L.T, L.H, L.dk, L.dv, L.type, L.cu_ptr(), L.n_seqs());
     });
@@ -377,7 +383,7 @@ struct NormRope {
         const double e = PyFloat_AsDouble(a[6]);
         if (e == -1.0 && PyErr_Occurred()) throw PythonError();
         eps = (float)e;
-        interleaved = PyObject_IsTrue(a[7]);
+        interleaved = truth(a[7]);
     }
     kda_dtype wtype() const { return wdt == at::kFloat ? KDA_F32 : KDA_BF16; }
     kda_rows out_rows(const char* name, const at::Tensor& t, const at::Tensor& like) const {
@@ -407,7 +413,7 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
     const kda_rows gq = A.out_rows("d_q_out", tensor("d_q_out", a[8]), A.q),
                    gk = A.out_rows("d_k_out", tensor("d_k_out", a[9]), A.k);
     Call c(A.dev, a[17]);
-    const bool given = PyObject_IsTrue(a[15]), weights = PyObject_IsTrue(a[10]);
+    const bool given = truth(a[15]), weights = truth(a[10]);
     if (given && (a[11] == Py_None || a[12] == Py_None)) throw BadValue("grads must hold dq and dk");
     const at::Tensor dq = A.out(c, "dq", a[11], A.q), dk = A.out(c, "dk", a[12], A.k);
     at::Tensor dwq, dwk;
