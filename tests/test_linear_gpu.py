@@ -122,6 +122,11 @@ def check_bwd(x, dt, dk, dv, grads, label):
         if got.dtype == torch.bfloat16:
             b = b + 2.0 ** -8 * np.abs(ref[name])
         close(f"{label} {name}", got, ref[name], b)
+        if np.abs(ref[name]).max() < 2.0 ** -126:
+            # a reset at the first token: e^-100 = 2^-144.3 is below fp32's smallest normal number,
+            # so no digit of the result can be asked for, only that it is as small
+            assert np.abs(to_f64(got)).max() <= 2.0 ** -126, f"{label} {name}"
+            continue
         tol = TOL["f32"] if name == "d_init_state" else parity_bound(dt, dk, dv, ref[name], name)
         assert parity(f"{label} {name}", to_f64(got).reshape(ref[name].shape), ref[name], tol,
                       stored_as="bf16" if got.dtype == torch.bfloat16 else None) <= tol
@@ -143,8 +148,16 @@ SHAPES = [  # dtype, lengths, heads, dk, dv, packed, decay, initial state, gates
     ("bf16", (300, 0, 1, 64, 511, 0), 3, 128, 128, True, "token", True, "hard"),
     ("bf16", (257, 900, 2), 2, 128, 128, True, "head", False, "mixed"),
     ("bf16", (1400, 5, 640), 1, 128, 128, True, "token", True, "mixed"),
+    # long sequences with few heads: cut into segments, forward and backward
+    ("bf16", (3333,), 1, 128, 128, False, "token", True, "hard"),
+    ("bf16", (3200, 3200), 1, 128, 128, False, "head", False, "mixed"),
+    ("bf16", (2900, 0, 3500, 5), 1, 128, 128, True, "token", True, "mixed"),
+    # more sequences than one launch of the tables takes
+    ("f32", (3,) * 40 + (0, 70) * 20, 1, 64, 64, True, "token", True, "mixed"),
+    ("bf16", (3,) * 40 + (0, 130) * 20, 1, 128, 128, True, "token", True, "mixed"),
 ]
-IDS = ["-".join(str(y) for y in s).replace(" ", "") for s in SHAPES]
+IDS = ["-".join(str(y if i != 1 or len(y) < 9 else f"{len(y)}seqs") for i, y in enumerate(s)).replace(" ", "")
+       for s in SHAPES]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
@@ -428,3 +441,47 @@ def test_far_offsets(cuda_ok):
     o_abs, f_abs = ol.forward(np.abs(pick(q)), np.abs(pick(k)), np.abs(pick(v)), pick(la), ss)
     close("o", o[0, a:][:, heads], o_ref, (F32U + 2.0 ** -8) * o_abs + 2.0 ** -8 * np.abs(o_ref))
     close("state", fs[1:, heads], f_ref, F32U * f_abs)
+
+
+@pytest.mark.parametrize("dt,d,lens,H", [("f32", 64, (300, 41), 2), ("bf16", 128, (300, 41), 2),
+                                         ("bf16", 128, (3333,), 1)], ids=["f32", "bf16", "bf16-segments"])
+def test_calls_back_to_back_share_a_workspace(cuda_ok, dt, d, lens, H):
+    """Calls queued without a pause on one stream, one workspace for all of them: the kernels
+    of a call overlap one another, and must not overlap the next call's.  The same from a graph."""
+    import kimi_delta_attention_30_b200 as kda
+    xs = [make(dt, lens, H, d, d, True, seed=s) for s in (40, 41, 42)]
+    size = lambda backward: kda.linear_workspace_size(1, sum(lens), H, d, d, DT[dt], cu_seqlens=xs[0]["cu"],
+                                                      backward=backward)
+    ws = torch.empty(max(size(False), size(True)), dtype=torch.uint8, device="cuda")
+
+    def both(x, workspace):
+        o, fs = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"],
+                                     workspace=workspace)
+        g = kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                 d_final_state=x["d_final"], cu_seqlens=x["cu"], workspace=workspace)
+        return (o, fs) + g
+
+    want = []
+    for x in xs:
+        want.append(both(x, None))
+        torch.cuda.synchronize()
+    got = [both(xs[i % 3], ws) for i in range(12)]
+    assert kda.linear_device_status(ws, DT[dt], 1, sum(lens), H, d, d, cu_seqlens=xs[0]["cu"], backward=True) == 0
+    for i, r in enumerate(got):
+        assert all(torch.equal(t, u) for t, u in zip(r, want[i % 3]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [both(xs[i % 3], ws) for i in range(3)]
+    for _ in range(3):
+        for r in got:
+            for t in r:
+                t.fill_(9.0)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for r, w in zip(got, want):
+            assert all(torch.equal(t, u) for t, u in zip(r, w))
+    o, _ = kda.linear_chunk_fwd(xs[0]["q"], xs[0]["k"], xs[0]["v"], xs[0]["log_alpha"], init_state=xs[0]["init"],
+                                cu_seqlens=xs[0]["cu"], workspace=ws)
+    assert kda.linear_device_status(ws, DT[dt], 1, sum(lens), H, d, d, cu_seqlens=xs[0]["cu"]) == 0
+    assert torch.equal(o, want[0][0])
