@@ -2,13 +2,14 @@
 //   S = a S + k v^T,   o = S^T q = a S_old^T q + (k . q) v.
 //
 // Bound by HBM: every state element is read once and written once (8 dk dv bytes against
-// 5 dk dv operations): 256 sequences of 32 heads of 128 x 128 take 159 us, 6.8 TB/s, the copy
-// rate.  A block owns 32 value columns of one (sequence, head) state; the columns are
-// independent of one another, so a single sequence's heads put four times as many blocks to
-// work (the cost is the k . q product once per tile).  Blocks with all 128 columns take 162 us
-// there, 16.4 instead of 14.4 us for 16 sequences, 9.7 instead of 10.2 for 8.  A thread keeps
-// its slice of the state in registers between the read and the write; the column sums S^T q
-// meet in shared memory.
+// 5 dk dv operations): 256 sequences of 32 heads of 128 x 128 take 158 to 165 us, 6.5 to 6.8
+// TB/s, the copy rate.  A block owns 32 value columns of one (sequence, head) state; the
+// columns are independent of one another, so a single sequence's heads put four times as many
+// blocks to work (the cost is the k . q product once per tile).  Blocks with all 128 columns
+// took 161 us where this takes 158 (calls back to back) and 162 where this takes 165 (with
+// other work between), 16.4 instead of 14.4 us for 16 sequences, 9.7 instead of 10.2 for 8.
+// A thread keeps its slice of the state in registers between the read and the write; the
+// column sums S^T q meet in shared memory.
 #include "kda_linear.cuh"
 
 namespace kda {
