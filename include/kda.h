@@ -567,7 +567,8 @@ KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const vo
  *                  t * token_stride + h * head_stride, so views of a fused
  *                  projection need no copy.  Starts and strides are multiples of
  *                  16 bytes; written rows must not overlap one another; q_out may
- *                  be q itself and k_out k itself (same strides)
+ *                  be q itself and k_out k itself (same strides; otherwise
+ *                  results must not overlap inputs)
  *   q_weight, k_weight : device [d] of weight_dtype, or NULL (ones)
  *   positions    : device [T] int32, any value (angles are reduced exactly, to
  *                  position * 2^-53 of a turn)

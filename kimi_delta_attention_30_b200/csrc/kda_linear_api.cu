@@ -180,6 +180,7 @@ kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_s
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
     kda_status st = check_decay(decay);
     if (st != KDA_OK) return st;
+    if (T > 0x7fffffff - C) return KDA_ERR_SHAPE;   // chunk ends are ints
     st = make_plan(B, T, H, dk, dv, C, cu, n_seqs, p);
     if (st != KDA_OK) return st;
     if (H > 65535 || (long long)p.n_seqs * H > 0x7fffffffLL) return KDA_ERR_SHAPE;

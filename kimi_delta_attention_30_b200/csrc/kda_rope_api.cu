@@ -21,9 +21,21 @@ kda_status check_out(const kda_rows* x, size_t elem, long long T, int H, int d) 
     const kda_status st = check_in(x, elem);
     if (st != KDA_OK) return st;
     const long long t = x->token_stride, h = x->head_stride;
-    const bool token_major = (H == 1 || h >= d) && (T == 1 || t >= (H - 1) * h + d);
-    const bool head_major = (T == 1 || t >= d) && (H == 1 || h / d >= T - 1 && h >= (T - 1) * t + d);
+    // `steps` strides of `inner` and a row fit into `outer` (without forming the product, which could overflow)
+    auto fits = [&](long long outer, long long inner, long long steps) {
+        return outer >= d && (steps == 0 || (inner >= d && (outer - d) / steps >= inner));
+    };
+    const bool token_major = T == 1 ? H == 1 || h >= d : fits(t, h, H - 1);
+    const bool head_major = H == 1 ? T == 1 || t >= d : fits(h, t, T - 1);
     return token_major || head_major ? KDA_OK : KDA_ERR_SHAPE;
+}
+
+// A result in its input's own memory: the rows have to be the same ones.
+kda_status check_in_place(const kda_rows* in, const kda_rows* out, long long T, int H) {
+    if (in->data != out->data) return KDA_OK;
+    return (T == 1 || in->token_stride == out->token_stride) && (H == 1 || in->head_stride == out->head_stride)
+               ? KDA_OK
+               : KDA_ERR_SHAPE;
 }
 
 kda_status check_sizes(kda_dtype dtype, kda_dtype wdtype, long long T, int Hq, int Hk, int d, int rot, float eps) {
@@ -62,6 +74,8 @@ kda_status kda_qk_norm_rope(const kda_rows* q, const kda_rows* k, const void* q_
     const kda_status each[4] = {check_in(q, e), check_in(k, e), check_out(q_out, e, T, Hq, d),
                                 check_out(k_out, e, T, Hk, d)};
     if ((st = first_error(each, 4)) != KDA_OK) return st;
+    const kda_status place[2] = {check_in_place(q, q_out, T, Hq), check_in_place(k, k_out, T, Hk)};
+    if ((st = first_error(place, 2)) != KDA_OK) return st;
     if (rot > 0 && (!positions || !inv_freq)) return KDA_ERR_NULL;
     if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions) ||
         !aligned4(inv_freq))
@@ -109,6 +123,9 @@ kda_status kda_qk_norm_rope_bwd(const kda_rows* q, const kda_rows* k, const void
     const kda_status each[6] = {check_in(q, e),       check_in(k, e),           check_in(d_q_out, e),
                                 check_in(d_k_out, e), check_out(dq, e, T, Hq, d), check_out(dk, e, T, Hk, d)};
     if ((st = first_error(each, 6)) != KDA_OK) return st;
+    const kda_status place[4] = {check_in_place(q, dq, T, Hq), check_in_place(d_q_out, dq, T, Hq),
+                                 check_in_place(k, dk, T, Hk), check_in_place(d_k_out, dk, T, Hk)};
+    if ((st = first_error(place, 4)) != KDA_OK) return st;
     if (rot > 0 && (!positions || !inv_freq)) return KDA_ERR_NULL;
     if (!workspace) return KDA_ERR_WORKSPACE;
     if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) || !aligned4(positions) ||

@@ -50,6 +50,7 @@ COMMON = [
     (dict(k=0x20004), E_ALIGN), (dict(la=0x40002), E_ALIGN), (dict(ws=0x100010), E_ALIGN),
     (dict(cu=[0, 100, 50, 256], n=3), E_SEQ), (dict(cu=[1, 256], n=1), E_SEQ), (dict(cu=[0, 200], n=1), E_SEQ),
     (dict(cu=[0, 256], n=1, B=2), E_SEQ), (dict(cu=[0], n=0), E_SEQ),
+    (dict(T=0x7fffffff, H=1), E_SHAPE), (dict(T=1 << 30, B=4), E_SHAPE),
 ]
 
 
@@ -122,14 +123,16 @@ ROPE = [
 
 @pytest.mark.parametrize("kw,code", ROPE + [
     (dict(qo=_rows(t=64)), E_SHAPE),            # written rows overlap
-    (dict(ko=_rows(h=0)), E_SHAPE), (dict(qo=_rows(t=64, h=128)), E_SHAPE)])
+    (dict(ko=_rows(h=0)), E_SHAPE), (dict(qo=_rows(t=64, h=128)), E_SHAPE),
+    (dict(qo=_rows(t=192)), E_SHAPE),           # in place, but not the same rows
+    (dict(qo=_rows(t=1 << 62, h=1 << 62)), E_SHAPE), (dict(ko=_rows(t=0, h=1 << 62)), E_SHAPE)])
 def test_norm_rope_rejects_before_launch(kw, code):
     assert _rope(**kw) == code
 
 
 @pytest.mark.parametrize("kw,code", ROPE + [
     (dict(dq=_rows(t=64)), E_SHAPE), (dict(ws=None), E_WS), (dict(wsb=8), E_WS), (dict(ws=0x100040), E_ALIGN),
-    (dict(dwq=0x50004), E_ALIGN), (dict(qo=_rows(0)), E_NULL)])
+    (dict(dwq=0x50004), E_ALIGN), (dict(qo=_rows(0)), E_NULL), (dict(dk=_rows(t=192)), E_SHAPE)])
 def test_norm_rope_bwd_rejects_before_launch(kw, code):
     assert _rope(bwd=True, **kw) == code
 
