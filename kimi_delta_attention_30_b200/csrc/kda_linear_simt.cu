@@ -34,7 +34,7 @@
 // each kernel behind the first starts early and loads and multiplies what needs only the
 // call's inputs (outputs: the scores; gradients: the pair products) before it waits.  fp32,
 // 256 tokens of 2 heads of 64: 12.4 us (20.5 without); backward of 5 sequences, 705 tokens of
-// 3 heads of 64 x 128: 44 us.
+// 3 heads of 64 x 128: 43 us.
 #include "kda_launch.cuh"
 #include "kda_linear.cuh"
 
@@ -322,9 +322,11 @@ __global__ void __launch_bounds__(ROWS * 4) lin_out(const Tin* __restrict__ q, c
 }
 
 // ---- backward: one (chunk, head) and one of dq, dk, dv a block ---------------------------
+// k, d_o, the decayed pairs, q, v; the tiles of S and dS' go where a role is done with an
+// operand, so that two blocks fit on an SM where the widths are 64 (backward of 1024 tokens of
+// 16 heads 80 -> 69 us).
 template <int DK, int DV> constexpr size_t grad_smem() {
-    constexpr int tile = (64 * (DV + 4) > DK * kLdP) ? 64 * (DV + 4) : DK * kLdP;
-    return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * (DV + 4) + tile + 2 * kC * kLdP);
+    return sizeof(float) * (2 * kC * (DK + 4) + 2 * kC * (DV + 4) + kC * kLdP);
 }
 
 // sum over the 16 threads that share rows 4 ty + r, added to dst by the first of them
@@ -345,19 +347,20 @@ struct DecayParts {
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, LinDecay dec,
          const Tin* __restrict__ d_o, ChunkMap cmap, int H, const float* S, const float* dS,
          Tin* __restrict__ dq, Tin* __restrict__ dk, Tin* __restrict__ dv, DecayParts parts) {
     extern __shared__ __align__(16) float sm[];
     __shared__ float gh[kC], gl[kC], w[kC], ra[kC], red[kThreads / 32];
     constexpr int LK = DK + 4, LV = DV + 4;
-    float *sq = sm, *sk = sq + kC * LK, *sv = sk + kC * LK, *sd = sv + kC * LV;
-    float *sp = sd + kC * LV, *sa = sp + kC * kLdP, *tile = sa + kC * kLdP;
+    static_assert(DK * kLdP <= kC * LK + kC * LV, "dv's tile goes over q and v");
+    float *sk = sm, *sd = sk + kC * LK, *sp = sd + kC * LV, *sq = sp + kC * kLdP, *sv = sq + kC * LK;
     let_next_kernel_start();
     int seq, tok0, len, idx;
     cmap.locate((int)blockIdx.x, seq, tok0, len, idx);
     const int h = blockIdx.y, role = blockIdx.z, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;   // dq, dk, dv
+    float* tile = role == 0 ? sv : role == 1 ? sd : sq;   // once the pairs are formed
     const size_t unit = (size_t)blockIdx.x * H + h;
     const float *Sn = S + unit * DK * DV, *dSn = dS + unit * DK * DV;
     load_rows<Tin, kC, DK, kThreads>(sq, LK, q, tok0, len, H, h, DK, 0);
@@ -375,15 +378,15 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
     clear(a);
     if (role != 1) mm64<DK, false, true, true>(p, sq, LK, sk, LK, ty, tx);
     if (role != 2) mm64<DV, false, true, true>(a, sd, LV, sv, LV, ty, tx);
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int i = 4 * ty + r, j = tx + 16 * c;
             const float d = j <= i ? exp_gdiff(gh[i], gl[i], gh[j], gl[j]) : 0.f;
-            sp[i * kLdP + j] = j <= i ? p[r][c] * d : 0.f;
-            sa[i * kLdP + j] = j <= i ? a[r][c] * d : 0.f;
-            tile[i * kLdM + j] = j < i ? p[r][c] * a[r][c] * d : 0.f;
+            sp[i * kLdP + j] = j <= i ? (role == 2 ? p[r][c] : a[r][c]) * d : 0.f;   // P, or dA
+            if (role == 0) tile[i * kLdM + j] = j < i ? p[r][c] * a[r][c] * d : 0.f;
         }
     wait_for_kernels_before();
     if (role == 2) {
@@ -440,10 +443,10 @@ lin_grad(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
             clear(a);
             if (role == 0) {
                 mm64<DV, false, true, true>(p, sd, LV, tile, LV, ty, tx);
-                mm64<kC, false, false, true>(a, sa, kLdP, sk + k0, LK, ty, tx);
+                mm64<kC, false, false, true>(a, sp, kLdP, sk + k0, LK, ty, tx);
             } else {
                 mm64<DV, false, true, true>(p, sv, LV, tile, LV, ty, tx);
-                mm64<kC, true, false, true>(a, sa, kLdP, sq + k0, LK, ty, tx);
+                mm64<kC, true, false, true>(a, sp, kLdP, sq + k0, LK, ty, tx);
             }
             float s1[4];
 #pragma unroll
