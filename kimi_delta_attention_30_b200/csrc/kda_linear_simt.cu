@@ -540,7 +540,7 @@ cudaError_t update_and_chain(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, int sides
         const bool small = small_grid((long long)n_chunks * H * tiles);
         auto update = small ? lin_update<Tin, 16> : lin_update<Tin, 64>;
         if (sides == 2) {
-            // The gradient kernel's 90 to 200 KB of shared memory can only come onto an SM beside
+            // The gradient kernel's 87 to 153 KB of shared memory can only come onto an SM beside
             // these two if the SM is divided for that already (50 -> 46 us for 14 chunks x 3 heads).
             cudaError_t e;
             const auto all = cudaFuncAttributePreferredSharedMemoryCarveout;
