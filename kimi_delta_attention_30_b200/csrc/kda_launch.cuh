@@ -3,11 +3,12 @@
 // waits for the earlier one's results.  The gap between two dependent launches, 1 to 2 us, and
 // the later kernel's start go from the path that way.
 //
-// The first kernel of a call (and any table it reads) is launched the ordinary way, so the
-// call's inputs are complete before any kernel launched here begins.  Every block of such a
-// kernel waits before it ends or writes.  What the earlier kernel wrote is read behind the
-// wait through pointers that are not __restrict__, or with __ldcg or bulk copies: a load that
-// takes the data for constant could move ahead of it.
+// The first kernel of a call is launched the ordinary way, so the call's inputs are complete
+// before any kernel launched here begins.  Every block of such a kernel waits before it ends or
+// writes.  What the earlier kernels wrote is read behind the wait through pointers that are not
+// __restrict__, or with __ldcg or bulk copies: a load that takes the data for constant could
+// move ahead of it.  So too the tables of sequences, where their kernel is the one before; a
+// kernel that reads them as constants, and the first behind them then, has an ordinary launch.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "kda_host.cuh"
+#include "kda_launch.cuh"
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -195,6 +196,7 @@ struct FewSeqs {
 };
 __global__ void __launch_bounds__(256) few_tables_write(SeqInfo* __restrict__ seqs, int n_seqs, int n_chunks, int C,
                                                         int4* __restrict__ chunks, const __grid_constant__ FewSeqs b) {
+    let_next_kernel_start();
     const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x);
     if (c < 2 * n_seqs) seqs[c] = b.e[c];
     if (c >= n_chunks) return;

@@ -69,6 +69,15 @@ namespace {
 constexpr int kWalkThreads = 896;    // warps 0-7 o and the state, 8-15 weights, 16 products, 17 loads, 18 decays, 20-27 P
 constexpr int kStateThreads = 640;   // the same without P
 
+// an entry of a table that the kernel before wrote
+__device__ __forceinline__ SeqInfo load_written(const SeqInfo* p) {
+    static_assert(sizeof(SeqInfo) == sizeof(int4), "one load");
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(p));
+    SeqInfo s;
+    memcpy(&s, &x, sizeof s);
+    return s;
+}
+
 // whether segment `idx` of sequence `seq` is its last
 __device__ __forceinline__ bool last_segment(const ChunkMap& segs, int seq, int idx) {
     const int len = segs.seqs ? segs.seqs[seq].len : segs.T;
@@ -94,7 +103,7 @@ template <int BV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
 lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, LinDecay dec, ChunkMap segs,
-         const SeqInfo* __restrict__ order, int H, const float* __restrict__ init_state,
+         const SeqInfo* order, int H, const float* __restrict__ init_state,
          const float* seg_start, __nv_bfloat16* __restrict__ o,
          float* __restrict__ final_state, int* __restrict__ err) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -111,7 +120,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const int j0 = vt * BV;
     int seq, tok0, len, idx;
     if (order != nullptr) {   // whole sequences, the longest first, so that the last blocks are short
-        const SeqInfo s = order[seg];
+        wait_for_kernels_before();   // the table
+        const SeqInfo s = load_written(order + seg);
         seq = s.seq;
         tok0 = s.tok0;
         len = s.len;
@@ -783,9 +793,11 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     if (split)
         return launch_behind(kern, (unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s, mq, mk, mv, mo, dec, segs,
                              nullptr, H, init_state, seg_state, (__nv_bfloat16*)o, final_state, err);
-    // whole packed sequences go by the longest-first table, empty ones among them
-    kern<<<(unsigned)(smap.order ? n_seqs : n_segs) * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(
-        mq, mk, mv, mo, dec, segs, smap.order, H, init_state, nullptr, (__nv_bfloat16*)o, final_state, err);
+    if (smap.order)   // whole packed sequences go by the longest-first table, empty ones among them
+        return launch_behind(kern, (unsigned)n_seqs * H * (kD / BV), kWalkThreads, kWalkSmem, s, mq, mk, mv, mo, dec, segs,
+                             smap.order, H, init_state, nullptr, (__nv_bfloat16*)o, final_state, err);
+    kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(mq, mk, mv, mo, dec, segs, nullptr, H, init_state,
+                                                                          nullptr, (__nv_bfloat16*)o, final_state, err);
     return cudaGetLastError();
 }
 
