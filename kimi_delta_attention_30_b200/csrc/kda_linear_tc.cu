@@ -399,8 +399,10 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             tc_fence_after();
             const uint64_t dk = mn_desc_k(base + offset(K, n), kT, 0), dv = mn_desc_k(base + offset(V, n), kT, 0);
             const uint64_t dl = mn_desc_k(lo, kT, 0);
-            product<true, true>(tU, dk, BV == 128 ? dv : dl, iU, false, lead);
-            product<true, true>(tU, BV == 128 ? dl : dk, BV == 128 ? dv : mn_desc_k(lo + kBlock, kT, 0), iU, true, lead);
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part)
+                product<true, true>(tU, BV == 128 && part ? dl : dk,
+                                    BV == 128 ? dv : dl + (uint64_t)(part ? kBlock >> 4 : 0), iU, part > 0, lead);
             commit(kUDone + (n & 1));
             if (BV == 128) {
                 if (n + 1 < nch && !(ok = wait_pair(kODone, n) && scores(n + 1))) break;
