@@ -531,6 +531,9 @@ KDA_API kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda
  *   d_init_state : device [N, H, dk, dv] fp32, or NULL (not written)
  * d_final_state may be NULL (zero) and may alias d_init_state.  The other
  * outputs must not overlap an input.  Results are reproducible bit for bit.
+ * On the tensor cores dq, dk and dv carry one operand rounded to bf16 (the
+ * scores, or a copy of a state), dlog_alpha two: each of its terms, the product
+ * of the state and its gradient among them, is off by at most 2^-7 of itself.
  */
 KDA_API size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
                                                    const int32_t* cu_seqlens_host, int n_seqs);
