@@ -485,3 +485,39 @@ def test_calls_back_to_back_share_a_workspace(cuda_ok, dt, d, lens, H):
                                 cu_seqlens=xs[0]["cu"], workspace=ws)
     assert kda.linear_device_status(ws, DT[dt], 1, sum(lens), H, d, d, cu_seqlens=xs[0]["cu"]) == 0
     assert torch.equal(o, want[0][0])
+
+
+@pytest.mark.parametrize("lens,H,packed", [((45,), 2, False), ((300, 300), 2, False), ((70, 0, 1, 131), 3, True),
+                                           ((3333,), 1, False)], ids=["45", "2x300", "packed", "segments"])
+@pytest.mark.parametrize("dt,dk,dv", [("bf16", 128, 128), ("bf16", 64, 128), ("f32", 128, 64)])
+def test_results_aligned_to_16_bytes(cuda_ok, dt, dk, dv, lens, H, packed):
+    """Every tensor of a call may start on any 16-byte boundary, results whose last rows are cut
+    by a sequence's end among them."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, lens, H, dk, dv, packed, seed=70)
+
+    def off(t):   # the same values 16 bytes behind a 256-byte boundary
+        if t is None:
+            return None
+        n = 16 // t.element_size()
+        buf = torch.full((t.numel() + 2 * n,), 5.0, dtype=t.dtype, device="cuda")
+        view = buf[n:n + t.numel()].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 32 == 16
+        return view
+
+    names = ("q", "k", "v", "log_alpha")
+    args = [x[n] for n in names]
+    o, fs = kda.linear_chunk_fwd(*args, init_state=x["init"], cu_seqlens=x["cu"])
+    g = kda.linear_chunk_bwd(*args, x["d_o"], init_state=x["init"], d_final_state=x["d_final"], cu_seqlens=x["cu"])
+    moved = [off(t) for t in args]
+    init, d_o, d_final = off(x["init"]), off(x["d_o"]), off(x["d_final"])
+    o2, fs2 = kda.linear_chunk_fwd(*moved, init_state=init, cu_seqlens=x["cu"], o=off(torch.zeros_like(o)),
+                                   final_state=off(torch.zeros_like(fs)))
+    g2 = kda.linear_chunk_bwd(*moved, d_o, init_state=init, d_final_state=d_final, cu_seqlens=x["cu"],
+                              grads=tuple(off(torch.zeros_like(t)) for t in g))
+    torch.cuda.synchronize()
+    for a, b in zip((o, fs) + g, (o2, fs2) + g2):
+        assert torch.equal(a, b)
+        n = 16 // b.element_size()
+        assert (b._base[:n] == 5.0).all() and (b._base[-n:] == 5.0).all()
