@@ -199,10 +199,12 @@ def _launch_on(device, stream, tensors=()):
     """Run one library call on ``device``: it is made the current device for the
     duration (the library launches on the current device), and the call's stream
     is ``stream`` or that device's current stream.  Every tensor must live on
-    ``device``.  Yields ``(stream, allocated)``: tensors the wrapper allocates
-    are appended to ``allocated`` and, when the stream is not the device's
-    current stream, recorded on it afterwards so that the caching allocator does
-    not reuse their memory while the call's kernels may still run."""
+    ``device``.  Yields ``(stream, results)``.  What the wrapper allocates comes
+    from the memory pool of the call's own stream: a block of the current
+    stream's pool may still be in use by what is queued there, which another
+    stream does not wait for.  Tensors appended to ``results`` become the
+    caller's, so they are recorded on the current stream where that is another
+    one: their memory is not handed out again while work queued there uses it."""
     for name, t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
@@ -211,12 +213,15 @@ def _launch_on(device, stream, tensors=()):
         s = cur if stream is None else stream
         if s.device != device:
             raise ValueError(f"stream belongs to {s.device}, the call runs on {device}")
-        allocated = []
-        yield s, allocated
-        if s != cur:
-            for t in allocated:
-                if t is not None:
-                    t.record_stream(s)
+        results = []
+        if s == cur:
+            yield s, results
+            return
+        with torch.cuda.stream(s):
+            yield s, results
+        for t in results:
+            if t is not None:
+                t.record_stream(cur)
 
 
 def _check_cuda(name, t, dtype=None):
@@ -307,19 +312,18 @@ def chunk_fwd(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None, C: int
     dev = q.device
     with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta),
                                   ("init_state", init_state), ("o", o), ("final_state", final_state),
-                                  ("workspace", workspace))) as (s, allocated):
+                                  ("workspace", workspace))) as (s, results):
         if o is None:
             o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
-            allocated.append(o)
+            results.append(o)
         if final_state is None and output_final_state:
             final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-            allocated.append(final_state)
+            results.append(final_state)
         _check_cuda("o", o, dt)
         _check_cuda("final_state", final_state, torch.float32)
         need = lib().kda_chunk_fwd_workspace_size_ex(B, T, H, dk, dv, C, _DTYPES[dt], cu, n_seqs, ALGOS[algo])
         if workspace is None:
             workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-            allocated.append(workspace)
         _check_cuda("workspace", workspace)
         wsb = workspace.numel() * workspace.element_size()
         if prep:
@@ -387,11 +391,10 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, cu_seqlens, init_state=None, C: int
     _check_host("o", o, dt)
     _check_host("final_state", final_state, torch.float32)
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _launch_on(dev, stream, (("device_buffer", device_buffer),)) as (s, allocated):
+    with _launch_on(dev, stream, (("device_buffer", device_buffer),)) as (s, results):
         need = lib().kda_chunk_fwd_host_buffer_size(_DTYPES[dt], cu, n_seqs, H, dk, dv, C, n_groups)
         if device_buffer is None:
             device_buffer = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-            allocated.append(device_buffer)
         _check_cuda("device_buffer", device_buffer)
         st = lib().kda_chunk_fwd_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
                                       beta.data_ptr(), _DTYPES[dt],
@@ -409,7 +412,7 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, cu_seqlens, init_state=None, C: int
 def host_device_status(device_buffer, stream=None) -> int:
     """kda_chunk_fwd_host_device_status: 0, or the error a bounded device wait
     recorded during the last chunk_fwd_host call that used ``device_buffer``."""
-    with _launch_on(device_buffer.device, stream, ()) as (s, _allocated):
+    with _launch_on(device_buffer.device, stream, ()) as (s, _):
         return int(lib().kda_chunk_fwd_host_device_status(_ptr(device_buffer), _stream_handle(s)))
 
 
@@ -467,12 +470,12 @@ def chunk_bwd(q, k, v, log_alpha, beta, d_o, init_state=None, d_final_state=None
     given = () if grads is None else tuple((f"grads[{i}]", t) for i, t in enumerate(grads))
     with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta), ("d_o", d_o),
                                   ("init_state", init_state), ("d_final_state", d_final_state),
-                                  ("workspace", workspace)) + given) as (s, allocated):
+                                  ("workspace", workspace)) + given) as (s, results):
         if grads is None:
             grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(log_alpha),
                      torch.empty_like(beta),
                      torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if need_d_init_state else None)
-            allocated.extend(grads)
+            results.extend(grads)
         dq, dk_, dv_, dla, dbeta, dinit = grads
         for name, t in (("dq", dq), ("dk", dk_), ("dv", dv_), ("dlog_alpha", dla), ("dbeta", dbeta)):
             _check_cuda(name, t, dt)
@@ -480,7 +483,6 @@ def chunk_bwd(q, k, v, log_alpha, beta, d_o, init_state=None, d_final_state=None
         need = lib().kda_chunk_bwd_workspace_size(B, T, H, dk, dv, C, cu, n_seqs)
         if workspace is None:
             workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-            allocated.append(workspace)
         _check_cuda("workspace", workspace)
         st = lib().kda_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _DTYPES[dt],
                                  _ptr(init_state), cu, n_seqs, B, T, H, dk, dv, C, _ptr(d_o), _ptr(d_final_state),
@@ -535,19 +537,18 @@ def segment_map(q, k, v, log_alpha, beta, cu_seqlens=None, C: int = 64, M=None, 
     N = n_seqs if cu_seqlens is not None else B
     dev = q.device
     with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta), ("M", M),
-                                  ("F", F), ("workspace", workspace))) as (s, allocated):
+                                  ("F", F), ("workspace", workspace))) as (s, results):
         if M is None:
             M = torch.empty((N, H, dk, dk), dtype=torch.float32, device=dev)
-            allocated.append(M)
+            results.append(M)
         if F is None:
             F = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-            allocated.append(F)
+            results.append(F)
         _check_cuda("M", M, torch.float32)
         _check_cuda("F", F, torch.float32)
         need = lib().kda_chunk_fwd_workspace_size(B, T, H, dk, dv, C, _DTYPES[dt], cu, n_seqs)
         if workspace is None:
             workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-            allocated.append(workspace)
         _check_cuda("workspace", workspace)
         st = lib().kda_chunk_segment_map(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _DTYPES[dt], cu,
                                          n_seqs, B, T, H, dk, dv, C, _ptr(M), _ptr(F), _ptr(workspace),
@@ -568,10 +569,10 @@ def compose_states(M, F, init_state=None, out=None, stream=None):
     for name, t in (("M", M), ("F", F), ("init_state", init_state)):
         _check_cuda(name, t, torch.float32)
     dev = M.device
-    with _launch_on(dev, stream, (("F", F), ("init_state", init_state), ("out", out))) as (s, allocated):
+    with _launch_on(dev, stream, (("F", F), ("init_state", init_state), ("out", out))) as (s, results):
         if out is None:
             out = torch.empty((R + 1, N, H, dk, dv), dtype=torch.float32, device=dev)
-            allocated.append(out)
+            results.append(out)
         _check_cuda("out", out, torch.float32)
         st = lib().kda_compose_states(_ptr(M), _ptr(F), _ptr(init_state), R, N, H, dk, dv, _ptr(out),
                                       _stream_handle(s))
@@ -603,13 +604,13 @@ def chunk_fwd_noalloc(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None
     dev = q.device
     with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta),
                                   ("init_state", init_state), ("o", o), ("final_state", final_state))) \
-            as (s, allocated):
+            as (s, results):
         if o is None:
             o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
-            allocated.append(o)
+            results.append(o)
         if final_state is None:
             final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-            allocated.append(final_state)
+            results.append(final_state)
         _check_cuda("o", o, dt)
         _check_cuda("final_state", final_state, torch.float32)
         st = lib().kda_chunk_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _DTYPES[dt],
@@ -635,10 +636,10 @@ def decode_step(q, k, v, log_alpha, beta, state, o=None, stream=None, prep: int 
     dv = v.shape[-1]
     dev = q.device
     with _launch_on(dev, stream, (("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta),
-                                  ("state", state), ("o", o))) as (s, allocated):
+                                  ("state", state), ("o", o))) as (s, results):
         if o is None:
             o = torch.empty((N, H, dv), dtype=dt, device=dev)
-            allocated.append(o)
+            results.append(o)
         _check_cuda("o", o, dt)
         if prep:
             st = lib().kda_decode_step_prep(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _DTYPES[dt],

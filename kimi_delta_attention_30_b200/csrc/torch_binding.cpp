@@ -99,12 +99,15 @@ int device_of(const char* name, const at::Tensor& t) {
     return t.get_device();
 }
 
-// The device and stream of one call, and the tensors it allocates.
+// The device and stream of one call, and the tensors it allocates.  Memory comes from the pool
+// of the call's own stream: a block of the current stream's pool may still be in use by what is
+// queued there, which another stream does not wait for.
 struct Call {
     c10::cuda::OptionalCUDAGuard guard;
+    c10::cuda::OptionalCUDAStreamGuard on;
     int dev;
     void* raw;
-    std::optional<c10::Stream> side;
+    std::optional<c10::Stream> home;   // the current stream, where the call runs on another
     std::vector<at::Tensor> made;
 
     Call(int device, PyObject* stream) : dev(device) {
@@ -120,19 +123,23 @@ struct Call {
                                std::to_string(device));
             if ((void*)handle != raw) {
                 raw = (void*)handle;
-                side = c10::Stream::unpack3(id, (c10::DeviceIndex)index, (c10::DeviceType)type);
+                home = cur.unwrap();
+                on.reset_stream(c10::Stream::unpack3(id, (c10::DeviceIndex)index, (c10::DeviceType)type));
             }
         }
     }
-    at::Tensor make(at::IntArrayRef shape, at::ScalarType dt) {
-        at::Tensor t = at::detail::empty_cuda(shape, dt, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
-        if (side) made.push_back(t);
+    at::Tensor scratch(at::IntArrayRef shape, at::ScalarType dt) {
+        return at::detail::empty_cuda(shape, dt, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+    }
+    at::Tensor make(at::IntArrayRef shape, at::ScalarType dt) {   // a result
+        at::Tensor t = scratch(shape, dt);
+        if (home) made.push_back(t);
         return t;
     }
-    // the memory is in use on a stream that is not the one it was allocated for
+    // results are the caller's from here on, whose stream is not the one they were allocated for
     void done(int status, const char* what) {
-        if (side)
-            for (const at::Tensor& t : made) t.record_stream(*side);
+        if (home)
+            for (const at::Tensor& t : made) t.record_stream(*home);
         if (status != KDA_OK) throw Status{status, what};
     }
 };
@@ -146,7 +153,7 @@ struct Scratch {
     Scratch(Call& c, PyObject* given, Need need) {
         if (given == Py_None) {
             const size_t n = need();
-            own = c.make({(int64_t)(n > 256 ? n : 256)}, at::kByte);
+            own = c.scratch({(int64_t)(n > 256 ? n : 256)}, at::kByte);
             ptr = own.data_ptr();
             bytes = (size_t)own.numel();
         } else {
