@@ -579,7 +579,8 @@ KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const vo
  *   d            : 64 or 128; rot : 0 (norm alone; positions and inv_freq may be
  *                  NULL) or a multiple of 16 up to d; Hq, Hk 1 .. 65535
  *   eps          : >= 0; with eps = 0 an all-zero row stays zero
- * All arithmetic in fp32; y is rounded once.  Asynchronous on `stream`.
+ * A NaN in a row makes the whole row NaN (and, in the gradients, the row's dx and
+ * the weight gradients); other rows do not see it.  All arithmetic in fp32; y is rounded once.  Asynchronous on `stream`.
  */
 typedef struct {
     void* data;

@@ -155,8 +155,11 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// 1 / sqrt(mean of squares + eps); 0 for a zero row with eps = 0, which stays zero, and NaN for a
+// row that holds one, so that the whole row shows it
 __device__ __forceinline__ float rms_scale(float sum_sq, int d, float eps) {
-    return inv_norm_from_sq(fmaf(sum_sq, 1.f / (float)d, eps));   // a zero row with eps = 0 stays zero
+    const float m = fmaf(sum_sq, 1.f / (float)d, eps);
+    return m == 0.f ? 0.f : rsqrtf(m);
 }
 
 template <typename Tw>

@@ -191,3 +191,38 @@ def test_streams_graph_and_autograd(cuda_ok):
     q, k = norm_rope(*leaves, x["pos"], x["fr"])
     torch.autograd.backward([q, k], [x["dq"], x["dk"]])
     assert all(torch.equal(t.grad, u) for t, u in zip(leaves, want[2:]))
+
+
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("dt,d,rot", [("bf16", 128, 64), ("f32", 64, 64), ("f32", 128, 0)])
+def test_nan_reaches_its_row_and_no_other(cuda_ok, dt, d, rot, inter):
+    """The norm divides a whole row by one number, so a NaN channel is a NaN row."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, (9,), 6, 2, d, rot, dt, False, seed=11)
+    args = (x["wq"], x["wk"], x["pos"], x["fr"])
+    kw = dict(eps=EPS, interleaved=inter)
+    want = kda.qk_norm_rope(x["q"], x["k"], *args, **kw)
+    grads = kda.qk_norm_rope_bwd(x["q"], x["k"], *args, x["dq"], x["dk"], **kw)
+    q = x["q"].clone()
+    q[3, 4, d - 1] = q[7, 0, 0] = float("nan")
+    bad = torch.zeros(9, 6, dtype=torch.bool, device="cuda")
+    bad[3, 4] = bad[7, 0] = True
+    for eps in (EPS, 0.0):
+        got, k = kda.qk_norm_rope(q, x["k"], *args, eps=eps, interleaved=inter)
+        assert got[bad].isnan().all() and got[~bad].isfinite().all()
+        if eps == EPS:
+            assert torch.equal(got[~bad], want[0][~bad]) and torch.equal(k, want[1])
+    g = kda.qk_norm_rope_bwd(q, x["k"], *args, x["dq"], x["dk"], **kw)
+    assert g[0][bad].isnan().all() and torch.equal(g[0][~bad], grads[0][~bad]) and torch.equal(g[1], grads[1])
+    assert g[2].isnan().all() and torch.equal(g[3], grads[3])
+    # an upstream gradient's NaN: its row of dx through the mean, and the weight channels of its pair
+    dq = x["dq"].clone()
+    dq[2, 1, 5] = float("nan")
+    g = kda.qk_norm_rope_bwd(x["q"], x["k"], *args, dq, x["dk"], **kw)
+    bad[:] = False
+    bad[2, 1] = True
+    assert g[0][bad].isnan().all() and torch.equal(g[0][~bad], grads[0][~bad])
+    pair = [5] if rot == 0 else [4, 5] if inter else [5, 5 + rot // 2]
+    one = torch.zeros(d, dtype=torch.bool, device="cuda")
+    one[pair] = True
+    assert g[2][one].isnan().all() and torch.equal(g[2][~one], grads[2][~one])
