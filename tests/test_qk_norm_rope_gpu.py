@@ -226,3 +226,26 @@ def test_nan_reaches_its_row_and_no_other(cuda_ok, dt, d, rot, inter):
     one = torch.zeros(d, dtype=torch.bool, device="cuda")
     one[pair] = True
     assert g[2][one].isnan().all() and torch.equal(g[2][~one], grads[2][~one])
+
+
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("dt,d,rot", [("bf16", 128, 32), ("f32", 64, 16), ("f32", 128, 0)])
+def test_channels_that_do_not_turn_stay_apart(cuda_ok, dt, d, rot, inter):
+    """An infinite channel behind the rotated ones: its row's scale is 0, so it is NaN and every other
+    channel 0; an infinite upstream gradient there reaches one weight channel."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, (5,), 3, 1, d, rot, dt, False, seed=12)
+    args = (x["wq"], x["wk"], x["pos"], x["fr"])
+    for c in (rot, rot + 9, d - 1):
+        q = x["q"].clone()
+        q[1, 2, c] = float("inf")
+        got, _ = kda.qk_norm_rope(q, x["k"], *args, eps=EPS, interleaved=inter)
+        row = got[1, 2]
+        assert row[c].isnan() and not row[:c].any() and not row[c + 1:].any()
+        dq = x["dq"].clone()
+        want = kda.qk_norm_rope_bwd(x["q"], x["k"], *args, dq, x["dk"], eps=EPS, interleaved=inter)
+        dq[1, 2, c] = float("inf")
+        g = kda.qk_norm_rope_bwd(x["q"], x["k"], *args, dq, x["dk"], eps=EPS, interleaved=inter)
+        one = torch.zeros(d, dtype=torch.bool, device="cuda")
+        one[c] = True
+        assert not g[2][one].isfinite().any() and torch.equal(g[2][~one], want[2][~one])
