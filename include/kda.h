@@ -504,8 +504,9 @@ typedef enum {
  * pair, 16 bits, which leaves some 5e-6 relative in the fp32 states, while the
  * scores and the state's copy that the queries read are rounded to bf16 once, as
  * o itself is.  Other shapes and fp32 run in fp32 on the CUDA cores.  Inputs are
- * finite: an infinity or NaN reaches its whole chunk (up to 128 tokens) and what
- * follows it in the sequence, but no other sequence.  H <= 65535.
+ * finite (log_alpha may be -inf, a reset): an infinity or NaN, a NaN log_alpha
+ * among them, reaches its whole chunk (up to 128 tokens) and what follows it in
+ * the sequence, but no other sequence.  H <= 65535.
  * Errors as kda_chunk_fwd; an unknown decay is KDA_ERR_SHAPE.
  */
 KDA_API size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,

@@ -19,9 +19,12 @@ __device__ __forceinline__ float lin_raw_decay(const LinDecay& d, size_t tok, in
     return d.per_head ? reinterpret_cast<const float*>(d.la)[h]
                       : to_f32(reinterpret_cast<const Tin*>(d.la)[tok * (size_t)H + h]);
 }
+// A NaN passes the floor (fmaxf would take it for a reset); the sums in fixed point, which have
+// none, pass it on by themselves.
 template <typename Tin>
 __device__ __forceinline__ float lin_log_decay(const LinDecay& d, size_t tok, int H, int h) {
-    return fmaxf(lin_raw_decay<Tin>(d, tok, H, h), kLogAlphaFloor);
+    const float x = lin_raw_decay<Tin>(d, tok, H, h);
+    return x < kLogAlphaFloor ? kLogAlphaFloor : x;
 }
 
 // ---- CUDA-core path (fp32 inputs, or a width of 64): 64-token chunks -------------

@@ -143,7 +143,7 @@ __device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, 
 
 // The chunk's inclusive cumulative log decay as (hi, lo), by the first warp; tokens past
 // `len` add nothing, so g stays at the last token's value there.  Summed in 64-bit fixed
-// point (32 fractional bits of log_alpha; exact sums).
+// point (32 fractional bits of log_alpha; exact sums).  A NaN among them is the whole chunk's.
 template <typename Tin>
 __device__ __forceinline__ void chunk_decay(float* gh, float* gl, const LinDecay& dec, size_t tok0, int len, int H,
                                             int h) {
@@ -151,6 +151,7 @@ __device__ __forceinline__ void chunk_decay(float* gh, float* gl, const LinDecay
         const int t = 2 * threadIdx.x;
         const float x = t < len ? lin_log_decay<Tin>(dec, tok0 + t, H, h) : 0.f;
         const float y = t + 1 < len ? lin_log_decay<Tin>(dec, tok0 + t + 1, H, h) : 0.f;
+        const bool nan = __any_sync(0xffffffffu, x != x || y != y);
         const long long a = __float2ll_rn(x * 4294967296.f), b = __float2ll_rn(y * 4294967296.f);
         long long s = a + b;
 #pragma unroll
@@ -162,7 +163,7 @@ __device__ __forceinline__ void chunk_decay(float* gh, float* gl, const LinDecay
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const float hi = __ll2float_rn(g[u]);
-            gh[t + u] = hi * (1.f / 4294967296.f);
+            gh[t + u] = nan ? __int_as_float(0x7fffffff) : hi * (1.f / 4294967296.f);
             gl[t + u] = __ll2float_rn(g[u] - __float2ll_rn(hi)) * (1.f / 4294967296.f);
         }
     }

@@ -201,11 +201,16 @@ __device__ __forceinline__ long long fixed_log2(float log_alpha) {
 __device__ __forceinline__ float from_fixed(long long x) { return __ll2float_rn(x) * (1.f / 4294967296.f); }
 
 // Inclusive sums over the warp's 128 tokens: p[u] inside the lane, the lane's total scanned.
+// Fixed point has no NaN: where one is among the decays, the chunk's weights and its whole decay
+// are set to it, so that results and states show it as they would any other NaN.
 struct Sums {
     long long p[4], incl, before;   // incl: sum up to the lane's last token; before: ahead of its first
+    bool nan;
 };
+__device__ __forceinline__ float or_nan(bool nan, float x) { return nan ? __int_as_float(0x7fffffff) : x; }
 __device__ __forceinline__ Sums scan_gates(const float (&x)[4], int lane) {
     Sums S;
+    S.nan = __any_sync(0xffffffffu, x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3]);
     S.p[0] = fixed_log2(x[0]);
 #pragma unroll
     for (int u = 1; u < 4; ++u) S.p[u] = S.p[u - 1] + fixed_log2(x[u]);
@@ -233,8 +238,8 @@ __device__ __forceinline__ void make_gates(Gates* G, const float (&x)[4], int la
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const long long g = S.before + S.p[u];
-        r2p[u] = from_fixed(g - s);
-        cop[u] = ex2_approx(from_fixed(e - g));
+        r2p[u] = or_nan(S.nan, from_fixed(g - s));
+        cop[u] = or_nan(S.nan, ex2_approx(from_fixed(e - g)));
     }
     reinterpret_cast<float4*>(G->rel2)[lane] = r2;
     reinterpret_cast<float4*>(G->col)[lane] = co;
@@ -245,7 +250,7 @@ __device__ __forceinline__ void make_gates(Gates* G, const float (&x)[4], int la
     if (lane < 16) G->fac[R][B] = B < R ? ex2_approx(from_fixed(rs - be)) : 0.f;
     if (lane < 16 && B == 0) G->start[R] = ex2_approx(from_fixed(rs));
     if (lane < 4) G->end[B] = ex2_approx(from_fixed(all - be));
-    if (lane == 0) G->gam = ex2_approx(from_fixed(all));
+    if (lane == 0) G->gam = or_nan(S.nan, ex2_approx(from_fixed(all)));
 }
 
 // The state chains need only the weights of a chunk's rows (e^{g_C - g}, reversed e^g) and
@@ -263,10 +268,10 @@ __device__ __forceinline__ long long make_weights(Weights* W, const float (&x)[4
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const long long g = S.before + S.p[u];
-        wp[u] = ex2_approx(from_fixed(rev ? g : all - g));
+        wp[u] = or_nan(S.nan, ex2_approx(from_fixed(rev ? g : all - g)));
     }
     reinterpret_cast<float4*>(W->w)[lane] = w;
-    if (lane == 0) W->gam = ex2_approx(from_fixed(all));
+    if (lane == 0) W->gam = or_nan(S.nan, ex2_approx(from_fixed(all)));
     return all;
 }
 

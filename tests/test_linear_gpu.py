@@ -521,3 +521,42 @@ def test_results_aligned_to_16_bytes(cuda_ok, dt, dk, dv, lens, H, packed):
         assert torch.equal(a, b)
         n = 16 // b.element_size()
         assert (b._base[:n] == 5.0).all() and (b._base[-n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dt,d,lens", [("f32", 64, (70, 90, 40)), ("bf16", 128, (300, 500, 40)),
+                                       ("bf16", 128, (300, 4000, 40)), ("bf16", 64, (70, 200, 40))],
+                         ids=["f32", "bf16", "bf16-segments", "bf16-64"])
+def test_nan_decay_is_no_reset(cuda_ok, dt, d, lens):
+    """A NaN log decay shows in its sequence's results from its chunk on, in its state and, backward,
+    in every gradient that it enters; other sequences keep their bits.  -inf stays a reset."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make(dt, lens, 1, d, d, True, seed=80)
+
+    def run(la):
+        f = kda.linear_chunk_fwd(x["q"], x["k"], x["v"], la, init_state=x["init"], cu_seqlens=x["cu"])
+        return f + kda.linear_chunk_bwd(x["q"], x["k"], x["v"], la, x["d_o"], init_state=x["init"],
+                                        d_final_state=x["d_final"], cu_seqlens=x["cu"])
+
+    want = run(x["log_alpha"])
+    at = x["cu"][1] + lens[1] - 30
+    la = x["log_alpha"].clone()
+    la[0, at, 0] = float("nan")
+    got = run(la)
+    torch.cuda.synchronize()
+    a, b = x["cu"][1], x["cu"][2]
+    for i, (t, u) in enumerate(zip(want, got)):
+        if i in (1, 6):      # states: o, final, dq, dk, dv, dlog_alpha, d_init
+            assert torch.equal(t[[0, 2]], u[[0, 2]]) and u[1].isnan().all(), i
+        else:
+            assert torch.equal(t[:, :a], u[:, :a]) and torch.equal(t[:, b:], u[:, b:]), i
+            assert u[:, at].isnan().all(), i
+    assert got[0][0, at:b].isnan().all()               # o: the token and what follows it
+    chunk = 128 if _tc(dt, d, d) else 64
+    before = a + (at - a) // chunk * chunk
+    assert torch.equal(got[0][:, a:before], want[0][:, a:before])
+    assert got[3][0, a:at].isnan().all()               # dk of what is read behind it
+    state = x["init"].clone()
+    la1 = torch.tensor([[0.0], [float("nan")], [-float("inf")]], dtype=DT[dt], device="cuda")
+    o = kda.linear_decode_step(x["q"][0, :3], x["k"][0, :3], x["v"][0, :3], la1, state)
+    assert o[1].isnan().all() and state[1].isnan().all()
+    assert o[[0, 2]].isfinite().all() and state[[0, 2]].isfinite().all()
