@@ -227,19 +227,25 @@ KDA_API kda_status kda_set_timing_events(void* const* events, int n_events);
 /*
  * Test hook for the failure path of the bounded device-side waits (no
  * counterpart on the pages; it exists so that tests can make a wait expire
- * without breaking anything on the GPU).  Arms, for the next tensor-core
- * prefill (kda_chunk_fwd / _ex / _prep / _noalloc) called from this host
- * thread, one extra wait in the first CTA of the chosen kernels on a barrier
- * that nothing ever completes, bounded by limit_ns.  That wait expires: the
- * kernel records KDA_ERR_TIMEOUT (read back with kda_chunk_fwd_device_status),
- * waits for the copies and products it has already issued, frees its tensor
- * memory and returns; the call's outputs are then undefined.  The next call is
- * unaffected.
- *   kernels  : bit 0 the chunk-local kernel (tc_intra), bit 1 the state carry
- *              (tc_recur); 0 disarms
+ * without breaking anything on the GPU).  Arms, for the next call from this host
+ * thread that runs the chosen kernels, one extra wait in their first CTA on a
+ * barrier that nothing ever completes, bounded by limit_ns.  That wait expires:
+ * the kernel records KDA_ERR_TIMEOUT (read back with
+ * kda_chunk_fwd_device_status, kda_linear_chunk_fwd_device_status,
+ * kda_linear_chunk_bwd_device_status), waits for the copies and products it has
+ * already issued, frees its tensor memory and returns; the call's outputs are
+ * then undefined.  The next call is unaffected.
+ *   kernels  : tensor-core prefill (kda_chunk_fwd / _ex / _prep / _noalloc): bit 0
+ *              the chunk-local kernel (tc_intra), bit 1 the state carry (tc_recur);
+ *              kda_linear_chunk_fwd, kda_linear_chunk_bwd: the three bits named
+ *              below (any call of the two on the tensor cores disarms them);
+ *              0 disarms all
  *   limit_ns : 1 .. 1e9 (ignored when kernels == 0)
  * Errors: KDA_ERR_SHAPE for unknown bits or a limit out of range.
  */
+#define KDA_TEST_WAIT_LINEAR_WALK 8u    /* the outputs' walk (lin_walk) */
+#define KDA_TEST_WAIT_LINEAR_STATE 16u  /* the state chains (lin_state) */
+#define KDA_TEST_WAIT_LINEAR_GRAD 32u   /* the gradients (lin_grad_tc) */
 KDA_API kda_status kda_set_test_wait_limit(unsigned int kernels, unsigned long long limit_ns);
 
 /*

@@ -262,10 +262,11 @@ def chunk_kernels(B, T, H, dk, dv, C, dtype, cu_seqlens=None, algo="auto"):
 
 
 def set_test_wait_limit(kernels: int, limit_ns: int):
-    """Failure-path test hook (``kda_set_test_wait_limit``): the next
-    tensor-core prefill from this thread makes a bounded wait expire in the
-    first CTA of the chosen kernels (bit 0 tc_intra, bit 1 tc_recur) and records
-    KDA_ERR_TIMEOUT; 0 disarms."""
+    """Failure-path test hook (``kda_set_test_wait_limit``): the next call from
+    this thread that runs the chosen kernels makes a bounded wait expire in their
+    first CTA and records KDA_ERR_TIMEOUT.  Bits: 1 tc_intra and 2 tc_recur
+    (tensor-core prefill); 8 lin_walk, 16 lin_state and 32 lin_grad_tc (linear
+    attention on the tensor cores); 0 disarms."""
     st = lib().kda_set_test_wait_limit(int(kernels), int(limit_ns))
     if st != 0:
         raise KdaError(st, "kda_set_test_wait_limit")
@@ -698,7 +699,8 @@ def linear_workspace_size(B, T, H, dk, dv, dtype, cu_seqlens=None, backward: boo
 def linear_device_status(workspace, dtype, B, T, H, dk, dv, cu_seqlens=None, backward: bool = False,
                          stream=None) -> int:
     """As :func:`device_status`, for the last :func:`linear_chunk_fwd` (or
-    :func:`linear_chunk_bwd`) call that used ``workspace`` with these sizes."""
+    :func:`linear_chunk_bwd`) call that used ``workspace`` with these sizes.  The
+    status is kept in the workspace: a caller who wants it passes one to the call."""
     cu, n, _keep = _cu_arg(cu_seqlens)
     d = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     f = lib().kda_linear_chunk_bwd_device_status if backward else lib().kda_linear_chunk_fwd_device_status

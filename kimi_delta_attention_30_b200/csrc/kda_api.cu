@@ -25,8 +25,8 @@ TimingHook& timing_hook() {
     return hook;
 }
 
-// kda_set_test_wait_limit: armed per host thread, consumed by the next
-// tensor-core prefill from that thread.
+// kda_set_test_wait_limit: armed per host thread, consumed by the next call
+// from that thread that runs the kernel.
 struct TestWait {
     unsigned kernels;
     unsigned long long ns;
@@ -34,6 +34,13 @@ struct TestWait {
 TestWait& test_wait() {
     static thread_local TestWait w{0u, 0ull};
     return w;
+}
+
+unsigned long long take_test_wait(unsigned bit) {
+    TestWait& w = test_wait();
+    const unsigned long long ns = (w.kernels & bit) ? w.ns : 0ull;
+    w.kernels &= ~bit;
+    return ns;
 }
 
 extern const char* const kTcKernelNames[];
@@ -384,11 +391,9 @@ kda_status chunk_fwd_impl(const void* q, const void* k, const void* v, const voi
         err = launch_simt_prefill(dtype, q, k, v, log_alpha, beta, init_state, o, final_state, cmap, smap,
                                   p.n_chunks, p.n_seqs, H, dk, dv, C, w, s);
     } else {
-        const TestWait tw = test_wait();
-        test_wait() = TestWait{0u, 0ull};
+        const unsigned long long stall1 = take_test_wait(1u), stall2 = take_test_wait(2u);
         err = launch_tc_prefill(q, k, v, log_alpha, beta, init_state, o, final_state, cmap, smap, p.n_chunks,
-                                p.n_seqs, H, C, ws + table_bytes(p), prep, s, (tw.kernels & 1u) ? tw.ns : 0ull,
-                                (tw.kernels & 2u) ? tw.ns : 0ull);
+                                p.n_seqs, H, C, ws + table_bytes(p), prep, s, stall1, stall2);
     }
     timing_hook().n = 0;
     timing_hook().base = 0;
@@ -500,7 +505,8 @@ kda_status kda_chunk_fwd(const void* q, const void* k, const void* v, const void
 }
 
 kda_status kda_set_test_wait_limit(unsigned int kernels, unsigned long long limit_ns) {
-    if (kernels & ~3u) return KDA_ERR_SHAPE;
+    if (kernels & ~(3u | KDA_TEST_WAIT_LINEAR_WALK | KDA_TEST_WAIT_LINEAR_STATE | KDA_TEST_WAIT_LINEAR_GRAD))
+        return KDA_ERR_SHAPE;
     if (kernels != 0u && (limit_ns == 0ull || limit_ns > 1000000000ull)) return KDA_ERR_SHAPE;
     test_wait() = TestWait{kernels, kernels ? limit_ns : 0ull};
     return KDA_OK;

@@ -42,6 +42,10 @@ int upload_tables(SeqInfo* dst, const std::vector<SeqInfo>& natural, const std::
 // Device capability check, cached per device ordinal.
 kda_status check_device();
 
+// The limit that kda_set_test_wait_limit armed on this thread for the kernel of `bit` (0: none),
+// disarmed by the asking.
+unsigned long long take_test_wait(unsigned bit);
+
 // Copy the error word at `offset` of the workspace to the host after `stream` finishes.
 kda_status read_error_word(const void* workspace, size_t offset, void* stream);
 

@@ -54,13 +54,19 @@ cudaError_t launch_lin_decode(kda_dtype dtype, const void* q, const void* k, con
 // ---- tensor-core path (bf16, 128 x 128): 128-token chunks, walked in segments ------
 constexpr int kLinTcChunk = 128;
 
+// Nanoseconds after which an extra wait in the first block of each kernel runs out; 0: none
+// (kda_set_test_wait_limit).
+struct TestStall {
+    unsigned long long walk = 0, state = 0, grad = 0;
+};
+
 // `segs` / `smap` number segments of segs.C tokens as the CUDA-core path numbers chunks.
 // With `split` the segments' own sums come first (seg_state [segments, H, dk, dv], seg_gam
 // [segments, H]) and are chained into start states.  BV: value columns a block, 128 or 64.
 cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init_state,
                               void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
                               int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
-                              float* seg_gam, int* err, cudaStream_t stream);
+                              float* seg_gam, int* err, TestStall stall, cudaStream_t stream);
 // Backward, two parts.  States: the bf16 images of every chunk's start state and of its end
 // state's gradient, [chunk image, H] x 32 KB, and d_init (seg_state and seg_gam hold both
 // directions, one behind the other).  Gradients: everything else, from the images.
@@ -68,10 +74,11 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
                                  const float* init_state, const float* d_final, float* d_init, const ChunkMap& segs,
                                  const SeqMap& smap, int n_segs, int n_seqs, bool split, long long tokens, int H,
                                  float* seg_state, float* seg_gam, uint8_t* images, uint8_t* d_images, int* err,
-                                 cudaStream_t stream);
+                                 TestStall stall, cudaStream_t stream);
 cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, const void* d_o, LinDecay dec, void* dq,
                                void* dk, void* dv, void* dla, const ChunkMap& chunks, int n_chunks, long long tokens,
-                               int H, const uint8_t* images, const uint8_t* d_images, int* err, cudaStream_t stream);
+                               int H, const uint8_t* images, const uint8_t* d_images, int* err, TestStall stall,
+                               cudaStream_t stream);
 
 // end = start (or 0) for n sequences without tokens from rank `first` of smap on
 cudaError_t launch_lin_empty_states(const float* start, float* end, const SeqMap& smap, int first, int n, int H,

@@ -245,6 +245,14 @@ bool all_aligned(const void* const (&ptrs)[N]) {
     return true;
 }
 
+TestStall take_stall() {
+    TestStall t;
+    t.walk = take_test_wait(KDA_TEST_WAIT_LINEAR_WALK);
+    t.state = take_test_wait(KDA_TEST_WAIT_LINEAR_STATE);
+    t.grad = take_test_wait(KDA_TEST_WAIT_LINEAR_GRAD);
+    return t;
+}
+
 // A C entry point lets no C++ exception out (the sequence tables are std::vectors).
 template <typename F>
 kda_status guarded(F&& f) {
@@ -326,11 +334,12 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
             if ((st = make_maps(L.segs, T, L.cut.seg_chunks * kLinTcChunk, ws, s, segs, smap, L.cut.split)) != KDA_OK)
                 return st;
             const int empty = empty_of(p, L.cut.split);
+            const TestStall stall = take_stall();
             cudaError_t e = launch_lin_empty_states(init_state, final_state, smap, p.n_seqs - empty, empty, H, s);
             if (e == cudaSuccess && p.total_tokens > 0)
                 e = launch_lin_tc_fwd(q, k, v, dec, init_state, o, final_state, segs, smap, L.segs.n_chunks, p.n_seqs,
                                       L.cut.split, L.cut.BV, p.total_tokens, H, (float*)(ws + L.state),
-                                      (float*)(ws + L.gam), (int*)(ws + L.err), s);
+                                      (float*)(ws + L.gam), (int*)(ws + L.err), stall, s);
             return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
         }
         const LinLayout L = simt_layout(p, H, dk, dv, false);
@@ -411,16 +420,17 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                 (st = make_maps(p, T, kLinTcChunk, ws, s, chunks, cmap)) != KDA_OK)
                 return st;
             const int empty = empty_of(p, L.cut.split);
+            const TestStall stall = take_stall();
             cudaError_t e = launch_lin_empty_states(d_final_state, d_init_state, smap, p.n_seqs - empty, empty, H, s);
             uint8_t *im = (uint8_t*)(ws + L.images), *dim = (uint8_t*)(ws + L.d_images);
             int* err = (int*)(ws + L.err);
             if (e == cudaSuccess && p.total_tokens > 0)
                 e = launch_lin_tc_states(q, k, v, d_o, dec, init_state, d_final_state, d_init_state, segs, smap,
                                          L.segs.n_chunks, p.n_seqs, L.cut.split, p.total_tokens, H,
-                                         (float*)(ws + L.state), (float*)(ws + L.gam), im, dim, err, s);
+                                         (float*)(ws + L.state), (float*)(ws + L.gam), im, dim, err, stall, s);
             if (e == cudaSuccess && p.total_tokens > 0)
                 e = launch_lin_tc_grad(q, k, v, d_o, dec, dq, dk_out, dv_out, dlog_alpha, chunks, p.n_chunks,
-                                       p.total_tokens, H, im, dim, err, s);
+                                       p.total_tokens, H, im, dim, err, stall, s);
             return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
         }
         const LinLayout L = simt_layout(p, H, dk, dv, true);

@@ -93,7 +93,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             const __grid_constant__ CUtensorMap mdv, ChunkMap chunks, int n_units, int H,
             const uint8_t* __restrict__ s_images,
             const uint8_t* __restrict__ z_images, __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
-            __nv_bfloat16* __restrict__ dv, __nv_bfloat16* __restrict__ dla, int* __restrict__ err) {
+            __nv_bfloat16* __restrict__ dv, __nv_bfloat16* __restrict__ dla, int* __restrict__ err, unsigned long long stall_ns) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kGradBars);
@@ -128,12 +128,15 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     auto slot = [&](int i) { return sm + (uint32_t)i * kTile; };
     // unit -> chunk, head; `it` counts this block's units: the parity of every barrier but the gates'
     const int first = (int)blockIdx.x, step = (int)gridDim.x;
+    constexpr int kOrder[kSlotsN] = {kS, kDO, kV, kZ, kK, kQ};   // loads, in the order the slots are free and needed
+    int loads = 0;   // tiles asked for (the loads' lane): tile n stands in slot kOrder[n % 6]
 
     if (warp < 16) {   // ---- elementwise
         const int R = warp & 3, B = warp >> 2, row = 32 * R + lane;
         const uint32_t at = ((uint32_t)(32 * R) << 16) + 32 * B;   // this warp's lanes and columns
         int it = 0, tails = 0;   // units so far, and those with rows to clear
-        for (int u = first; u < n_units; u += step, ++it) {
+        const bool stalled = warp == 0 && stall(&bars[kDrain], stall_ns, ab);
+        for (int u = first; !stalled && u < n_units; u += step, ++it) {
             const uint32_t par = (uint32_t)it & 1u;
             int seq, tok0, len, idx;
             chunks.locate(u / H, seq, tok0, len, idx);
@@ -327,6 +330,8 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             }
         }
         if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        tmem_st_wait();   // (given up in between)
     } else if (warp == 16) {   // ---- products
         constexpr uint32_t iKK = idesc_bf16_f32(128, 128), iKM = idesc_bf16_f32_bmn(128, 128), iMM = idesc_amn_bmn(128, 128);
         const uint32_t lead = elect_lane(), base = smem_u32(sm);
@@ -335,32 +340,31 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         };
         auto ktile = [&](int i) { return sw128_desc(base + (uint32_t)i * kTile); };
         auto mtile = [&](int i) { return mn_desc_k(base + (uint32_t)i * kTile, kT, 0); };
-        bool ok = true;
         int it = 0, tails = 0;
         for (int u = first; u < n_units; u += step, ++it) {
             const uint32_t par = (uint32_t)it & 1u;
             int seq, tok0, len, idx;
             chunks.locate(u / H, seq, tok0, len, idx);
             // (each accumulator once the last unit's result has been read from it)
-            if (it > 0 && !(ok = wait_or_abort(&bars[kRead + 1], par ^ 1u, ab))) break;
-            if (!(ok = wait_or_abort(&bars[kFull + kDO], par, ab) && wait_or_abort(&bars[kFull + kS], par, ab) &&
-                       (len == kT || wait_or_abort(&bars[kClean], (uint32_t)tails++ & 1u, ab))))
+            if (it > 0 && !wait_or_abort(&bars[kRead + 1], par ^ 1u, ab)) break;
+            if (!wait_or_abort(&bars[kFull + kDO], par, ab) || !wait_or_abort(&bars[kFull + kS], par, ab) ||
+                (len < kT && !wait_or_abort(&bars[kClean], (uint32_t)tails++ & 1u, ab)))
                 break;
             tc_fence_after();
             product<false, false>(tQ, ktile(kDO), ktile(kS), iKK, false, lead);
             commit(kInter);
-            if (it > 0 && !(ok = wait_or_abort(&bars[kRead + 2], par ^ 1u, ab) && wait_or_abort(&bars[kRead], par ^ 1u, ab)))
+            if (it > 0 && (!wait_or_abort(&bars[kRead + 2], par ^ 1u, ab) || !wait_or_abort(&bars[kRead], par ^ 1u, ab)))
                 break;
-            if (!(ok = wait_or_abort(&bars[kFull + kV], par, ab) && wait_or_abort(&bars[kFull + kZ], par, ab))) break;
+            if (!wait_or_abort(&bars[kFull + kV], par, ab) || !wait_or_abort(&bars[kFull + kZ], par, ab)) break;
             tc_fence_after();
             product<false, false>(tK, ktile(kV), ktile(kZ), iKK, false, lead);
             commit(kKInter);
-            if (!(ok = wait_or_abort(&bars[kFull + kQ], par, ab) && wait_or_abort(&bars[kFull + kK], par, ab))) break;
+            if (!wait_or_abort(&bars[kFull + kQ], par, ab) || !wait_or_abort(&bars[kFull + kK], par, ab)) break;
             product<false, false>(tA, ktile(kQ), ktile(kK), iKK, false, lead);
             product<false, false>(tB, ktile(kDO), ktile(kV), iKK, false, lead);
             commit(kScores);
             // P is in S's slot, B in V's
-            if (!(ok = wait_or_abort(&bars[kPReady], par, ab))) break;
+            if (!wait_or_abort(&bars[kPReady], par, ab)) break;
             tc_fence_after();
             product<false, true>(tA, ktile(kK), mtile(kZ), iKM, false, lead);
             commit(kFree + kZ);
@@ -376,14 +380,9 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             commit(kFree + kV);
             commit(kFree + kQ);
         }
-        if (!ok) {   // given up: products in flight end before the tensor memory is freed
-            commit(kDrain);
-            mbar_wait(&bars[kDrain], 0u);
-        }
     } else if (warp == 17) {
-        if (lane == 0) {   // ---- loads, in the order the slots are free and needed
-            constexpr int kOrder[kSlotsN] = {kS, kDO, kV, kZ, kK, kQ};
-            int it = 0, i = 0;
+        if (lane == 0) {   // ---- loads
+            int it = 0;
             bool ok = true;
             for (int u = first; ok && u < n_units; u += step, ++it) {
                 const uint32_t par = (uint32_t)it & 1u;
@@ -391,7 +390,7 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 chunks.locate(u / H, seq, tok0, len, idx);
                 const int h = u % H;
                 const size_t image = (size_t)(image_of(tok0 - idx * kT, seq) + idx) * H + h;
-                for (i = 0; i < kSlotsN; ++i) {
+                for (int i = 0; i < kSlotsN; ++i, ++loads) {
                     const int k = kOrder[i];
                     if (it > 0 && !(ok = wait_or_abort_lane(&bars[kFree + k], par ^ 1u, ab))) break;
                     uint64_t* bar = &bars[kFull + k];
@@ -403,11 +402,6 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                         tma_box(slot(k), m, 0, h, tok0, bar);
                         tma_box(slot(k) + kBlock, m, 64, h, tok0, bar);
                     }
-                }
-                if (!ok) {   // given up: the copies in flight land before the block ends
-                    for (int j = 0; j < kSlotsN; ++j)
-                        if (j < i || it > 0)
-                            mbar_wait(&bars[kFull + kOrder[j]], j < i ? par : par ^ 1u);
                 }
             }
         }
@@ -502,6 +496,13 @@ lin_grad_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (gave_up(ab)) {
+        if (warp == 16) drain_products(&bars[kDrain]);
+#pragma unroll
+        for (int j = 0; j < kSlotsN; ++j)   // the last tile of each slot
+            if (loads > j) mbar_wait(&bars[kFull + kOrder[j]], (uint32_t)((loads - 1 - j) / kSlotsN) & 1u);
+        __syncwarp();
+    }
     if (warp == 16) tmem_dealloc(tbase, 512);
 }
 
@@ -512,7 +513,8 @@ using namespace lintc;
 
 cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, const void* d_o, LinDecay dec, void* dq,
                                void* dk, void* dv, void* dla, const ChunkMap& chunks, int n_chunks, long long tokens,
-                               int H, const uint8_t* images, const uint8_t* d_images, int* err, cudaStream_t s) {
+                               int H, const uint8_t* images, const uint8_t* d_images, int* err, TestStall stall,
+                               cudaStream_t s) {
     CUtensorMap mq, mk, mv, mdo;
     if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
         !make_map(&mdo, d_o, tokens, H))
@@ -526,7 +528,7 @@ cudaError_t launch_lin_tc_grad(const void* q, const void* k, const void* v, cons
     const int units = n_chunks * H;
     return launch_behind(lin_grad_tc, std::min(units, 148), kGradThreads, kGradSmem, s, mq, mk, mv, mdo, dec, mdq, mdk, mdv,
                          chunks, units, H, images, d_images, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv,
-                         dec.per_head ? nullptr : (__nv_bfloat16*)dla, err);
+                         dec.per_head ? nullptr : (__nv_bfloat16*)dla, err, stall.grad);
 }
 
 }  // namespace kda

@@ -105,7 +105,7 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, LinDecay dec, ChunkMap segs,
          const SeqInfo* order, int H, const float* __restrict__ init_state,
          const float* seg_start, __nv_bfloat16* __restrict__ o,
-         float* __restrict__ final_state, int* __restrict__ err) {
+         float* __restrict__ final_state, int* __restrict__ err, unsigned long long stall_ns) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int NV = kD / BV, HB = BV / 2;   // value tiles a head; state columns a thread
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBars);
@@ -175,6 +175,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     Gates* gates = reinterpret_cast<Gates*>(sm + kOffGates);
     const int sp = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * sp) << 16;
+    constexpr int kRing = BV == 128 ? 5 : 6;   // tiles in flight
+    int loads = 0;                             // tiles asked for (the loads' lane)
 
     // 72 registers a thread at launch, 28 warps: 8 x 104 + 16 x 64 + 4 x 40 of 28 x 72
     if (warp >= 16 && warp < 20) fewer_registers<40>();
@@ -257,8 +259,8 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             return true;
         };
         publish();
-        bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        bool ok = warp != 0 || !stall(&bars[kDrain], stall_ns, ab);
+        for (int n = 0; ok && n < nch; ++n) {
             if (!(ok = wait_pair(kGFull, n))) break;
             const float gam = gates[n & 1].gam, eg = ex2_approx(gates[n & 1].rel2[row]) * gates[n & 1].start[sp];
             warp_arrive(&bars[kGEmpty + (n & 1)], lane);
@@ -414,22 +416,15 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                 if (!(ok = values(n))) break;
             }
         }
-        if (!ok) {   // given up: products in flight end before the tensor memory is freed
-            commit(kDrain);
-            mbar_wait(&bars[kDrain], 0u);
-        }
     } else if (warp == 17) {
         if (lane == 0) {   // ---- loads
             // A slot is free when the last product that reads its tile is done.
-            constexpr int kRing = BV == 128 ? 5 : 6;
-            int i = 0;   // tile 3 n + kind
-            bool ok = true;
-            for (; i < 3 * nch; ++i) {
-                const int n = i / 3, kind = i % 3;
+            for (; loads < 3 * nch; ++loads) {
+                const int i = loads, n = i / 3, kind = i % 3;   // tile 3 n + kind
                 if (i >= kRing) {
                     const int m = (i - kRing) / 3, was = (i - kRing) % 3;   // the tile before in this slot
                     const int bar = BV == 128 ? (was == Q ? kQsDone : kUDone) : was == V ? kODone : kUDone;
-                    if (!(ok = wait_or_abort_lane(&bars[bar + (m & 1)], (uint32_t)(m >> 1) & 1u, ab))) break;
+                    if (!wait_or_abort_lane(&bars[bar + (m & 1)], (uint32_t)(m >> 1) & 1u, ab)) break;
                 }
                 const CUtensorMap* map = kind == Q ? &mq : kind == K ? &mk : &mv;
                 uint8_t* dst = sm + offset(kind, n);
@@ -444,8 +439,6 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
                     tma_box(dst, map, j0, h, t, bar);
                 }
             }
-            if (!ok)   // given up: the copies in flight land before the block ends
-                for (int j = max(0, i - kRing); j < i; ++j) mbar_wait(full(j % 3, j / 3), full_par(j % 3, j / 3));
         }
     } else if (warp == 18) {   // ---- decays
         float x[4], y[4];
@@ -463,6 +456,11 @@ lin_walk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (gave_up(ab)) {
+        if (warp == 16) drain_products(&bars[kDrain]);
+        for (int j = max(0, loads - kRing); j < loads; ++j) mbar_wait(full(j % 3, j / 3), full_par(j % 3, j / 3));
+        __syncwarp();
+    }
     if (warp == 16) tmem_dealloc(tbase, 512);
 }
 
@@ -497,7 +495,8 @@ enum StBar { kSFull = 0, kSEmpty = kStSlots, kSWReady = 2 * kStSlots, kSUDone = 
 __global__ void __launch_bounds__(kStateThreads, 1)
 lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, LinDecay dec, ChunkMap segs,
-          const SeqInfo* __restrict__ order, int H, int n_fwd, StateSide fwd, StateSide bwd, int clear_err, int* __restrict__ err) {
+          const SeqInfo* __restrict__ order, int H, int n_fwd, StateSide fwd, StateSide bwd, int clear_err, int* __restrict__ err,
+          unsigned long long stall_ns) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kStBars);
     uint32_t* flags = reinterpret_cast<uint32_t*>(bars + kStBarsN);
@@ -558,6 +557,7 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         return wait_or_abort(&bars[kSGFull + n % kStGateBufs], (uint32_t)(n / kStGateBufs) & 1u, ab);
     };
 
+    int loads = 0;   // tiles asked for (the loads' lane)
     if (warp >= 16) fewer_registers<40>();
     if (warp < 8) {   // ---- the state
         more_registers<120>();
@@ -577,8 +577,8 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
             }
         }
         const long long image0 = image_of(tok0 - idx * segs.C, seq) + (long long)idx * (segs.C / kT);
-        bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        bool ok = warp != 0 || !stall(&bars[kSDrain], stall_ns, ab);
+        for (int n = 0; ok && n < nch; ++n) {
             if (!(ok = gates_full(n))) break;
             const float gam = gates[n % kStGateBufs].gam;
             warp_arrive(&bars[kSGEmpty + n % kStGateBufs], lane);
@@ -646,11 +646,10 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         auto commit = [&](int bar) {
             if (lead) mma_commit(&bars[bar]);
         };
-        bool ok = true;
         for (int n = 0; n < nch; ++n) {
-            if (!(ok = wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab) &&
-                       wait_or_abort(&bars[kSWReady + (n & 1)], half_par(n), ab) &&
-                       (n < 2 || wait_or_abort(&bars[kSURead + (n & 1)], half_par(n) ^ 1u, ab))))
+            if (!wait_or_abort(full(2 * n + 1), full_par(2 * n + 1), ab) ||
+                !wait_or_abort(&bars[kSWReady + (n & 1)], half_par(n), ab) ||
+                (n >= 2 && !wait_or_abort(&bars[kSURead + (n & 1)], half_par(n) ^ 1u, ab)))
                 break;
             tc_fence_after();
             const uint64_t b = mn_desc_k(base + (2 * n + 1) % kStSlots * kTile, kT, 0);
@@ -661,23 +660,16 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
             commit(kSEmpty + (2 * n) % kStSlots);
             commit(kSEmpty + (2 * n + 1) % kStSlots);
         }
-        if (!ok) {
-            commit(kSDrain);
-            mbar_wait(&bars[kSDrain], 0u);
-        }
     } else if (warp == 17) {
         if (lane == 0) {   // ---- loads
-            int i = 0;
-            bool ok = true;
-            for (; i < 2 * nch; ++i) {
-                if (i >= kStSlots && !(ok = wait_or_abort_lane(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab))) break;
+            for (; loads < 2 * nch; ++loads) {
+                const int i = loads;
+                if (i >= kStSlots && !wait_or_abort_lane(&bars[kSEmpty + i % kStSlots], full_par(i) ^ 1u, ab)) break;
                 const int t = tok0 + chunk(i / 2) * kT;
                 mbar_arrive_expect_tx(full(i), kTile);
                 tma_box(slot(i), i & 1 ? mb : ma, 0, h, t, full(i));
                 tma_box(slot(i) + kBlock, i & 1 ? mb : ma, 64, h, t, full(i));
             }
-            if (!ok)
-                for (int j = max(0, i - kStSlots); j < i; ++j) mbar_wait(full(j), full_par(j));
         }
     } else if (warp == 18) {   // ---- decays
         float x[4], y[4];
@@ -700,6 +692,11 @@ lin_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (gave_up(ab)) {
+        if (warp == 16) drain_products(&bars[kSDrain]);
+        for (int j = max(0, loads - kStSlots); j < loads; ++j) mbar_wait(full(j), full_par(j));
+        __syncwarp();
+    }
     if (warp == 16) tmem_dealloc(tbase, 256);
 }
 
@@ -775,7 +772,7 @@ cudaError_t launch_lin_empty_states(const float* start, float* end, const SeqMap
 cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDecay dec, const float* init_state,
                               void* o, float* final_state, const ChunkMap& segs, const SeqMap& smap, int n_segs,
                               int n_seqs, bool split, int BV, long long tokens, int H, float* seg_state,
-                              float* seg_gam, int* err, cudaStream_t s) {
+                              float* seg_gam, int* err, TestStall stall, cudaStream_t s) {
     CUtensorMap mq, mk, mv, mo;
     if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
         !make_map(&mo, o, tokens, H, BV / 2, 32))
@@ -785,7 +782,7 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
         if ((e = allow_smem(lin_state, kStSmem)) != cudaSuccess) return e;
         const StateSide side{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
         lin_state<<<(unsigned)n_segs * H, kStateThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, nullptr, H, n_segs * H, side,
-                                                                     side, 1, err);
+                                                                     side, 1, err, stall.state);
         e = launch_behind(seg_chain<false>, dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s, seg_state, seg_gam,
                           init_state, smap, H);
         if (e != cudaSuccess) return e;
@@ -794,12 +791,13 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
     if ((e = allow_smem(kern, kWalkSmem)) != cudaSuccess) return e;
     if (split)
         return launch_behind(kern, (unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s, mq, mk, mv, mo, dec, segs,
-                             nullptr, H, init_state, seg_state, (__nv_bfloat16*)o, final_state, err);
+                             nullptr, H, init_state, seg_state, (__nv_bfloat16*)o, final_state, err, stall.walk);
     if (smap.order)   // whole packed sequences go by the longest-first table, empty ones among them
         return launch_behind(kern, (unsigned)n_seqs * H * (kD / BV), kWalkThreads, kWalkSmem, s, mq, mk, mv, mo, dec, segs,
-                             smap.order, H, init_state, nullptr, (__nv_bfloat16*)o, final_state, err);
+                             smap.order, H, init_state, nullptr, (__nv_bfloat16*)o, final_state, err, stall.walk);
     kern<<<(unsigned)n_segs * H * (kD / BV), kWalkThreads, kWalkSmem, s>>>(mq, mk, mv, mo, dec, segs, nullptr, H, init_state,
-                                                                          nullptr, (__nv_bfloat16*)o, final_state, err);
+                                                                          nullptr, (__nv_bfloat16*)o, final_state, err,
+                                                                          stall.walk);
     return cudaGetLastError();
 }
 
@@ -809,7 +807,7 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
                                  const float* init_state, const float* d_final, float* d_init, const ChunkMap& segs,
                                  const SeqMap& smap, int n_segs, int n_seqs, bool split, long long tokens, int H,
                                  float* seg_state, float* seg_gam, uint8_t* images, uint8_t* d_images, int* err,
-                                 cudaStream_t s) {
+                                 TestStall stall, cudaStream_t s) {
     CUtensorMap mq, mk, mv, mdo;
     if (!make_map(&mq, q, tokens, H) || !make_map(&mk, k, tokens, H) || !make_map(&mv, v, tokens, H) ||
         !make_map(&mdo, d_o, tokens, H))
@@ -821,7 +819,8 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
     if (split) {
         const StateSide f{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
         const StateSide r{nullptr, nullptr, d_seg, d_gam, nullptr, nullptr};
-        lin_state<<<2u * units, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, nullptr, H, units, f, r, 1, err);
+        lin_state<<<2u * units, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, nullptr, H, units, f, r, 1, err,
+                                                           stall.state);
         const dim3 grid((unsigned)n_seqs * H, kD * kD / 1024);
         if ((e = launch_behind(seg_chain<false>, grid, 256, 0, s, seg_state, seg_gam, init_state, smap, H)) != cudaSuccess ||
             (e = launch_behind(seg_chain<true>, grid, 256, 0, s, d_seg, d_gam, d_final, smap, H)) != cudaSuccess)
@@ -831,9 +830,10 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
     const StateSide r{d_final, split ? d_seg : nullptr, nullptr, nullptr, d_images, d_init};
     if (split)
         return launch_behind(lin_state, 2u * units, kStateThreads, kStSmem, s, mk, mv, mq, mdo, dec, segs, nullptr, H, units,
-                             f, r, 0, err);
+                             f, r, 0, err, stall.state);
     const int n = smap.order ? n_seqs * H : units;
-    lin_state<<<2u * n, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, smap.order, H, n, f, r, 1, err);
+    lin_state<<<2u * n, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, smap.order, H, n, f, r, 1, err,
+                                                   stall.state);
     return cudaGetLastError();
 }
 

@@ -162,6 +162,27 @@ __device__ __forceinline__ bool wait_or_abort_lane(uint64_t* bar, uint32_t parit
     }
 }
 
+// Test of the failure path (ns != 0: kda_set_test_wait_limit): one warp of the first block waits on
+// a barrier that nothing completes before a role gives up, and then gives up as any wait that
+// has run out.  True if it has.
+__device__ __forceinline__ bool stall(uint64_t* never, unsigned long long ns, const Abort& A) {
+    if (ns == 0ull || blockIdx.x != 0) return false;
+    const bool out = !mbar_wait(never, 0u, ns);
+    if (out) {
+        atomicCAS(A.err, 0, (int)KDA_ERR_TIMEOUT);
+        *reinterpret_cast<volatile uint32_t*>(A.flag) = 1u;
+    }
+    return __any_sync(0xffffffffu, out);
+}
+// The block's end (all roles are out of their loops): whether one of them gave up.  What the others
+// had issued by then may still be on its way, so copies have to land and products to end first.
+__device__ __forceinline__ bool gave_up(const Abort& A) { return *reinterpret_cast<volatile uint32_t*>(A.flag) != 0u; }
+// (by the warp that issued the products)
+__device__ __forceinline__ void drain_products(uint64_t* bar) {
+    commit_lead(bar, elect_lane());
+    mbar_wait(bar, 0u);
+}
+
 // ---- a chunk's decays -------------------------------------------------------------------
 // The 128 tokens are four blocks of 32.  With g the inclusive sum of log decays from the
 // chunk's start, every decay the kernels need is a product of numbers that are at most 1:

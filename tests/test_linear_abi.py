@@ -81,6 +81,14 @@ def test_decode_rejects_before_launch():
     assert f(*args, 0, 0, vp(0x70000), 0, 2, 64, 64, vp(0x80000), None) == OK   # N = 0: no work
 
 
+def test_wait_limit_knows_the_linear_kernels():
+    f = kda.lib().kda_set_test_wait_limit
+    for bits in (8, 16, 32, 8 | 16 | 32 | 3):
+        assert f(bits, 1000) == OK
+    assert f(64, 1000) == E_SHAPE and f(8 | 64, 1000) == E_SHAPE and f(8, 0) == E_SHAPE
+    assert f(0, 0) == OK   # disarm
+
+
 def test_workspace_sizes():
     for dt, d in ((1, 64), (1, 128), (0, 64), (0, 128)):
         one = kda.linear_workspace_size(1, 1, 1, d, d, dt)

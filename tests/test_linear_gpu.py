@@ -560,3 +560,51 @@ def test_nan_decay_is_no_reset(cuda_ok, dt, d, lens):
     o = kda.linear_decode_step(x["q"][0, :3], x["k"][0, :3], x["v"][0, :3], la1, state)
     assert o[1].isnan().all() and state[1].isnan().all()
     assert o[[0, 2]].isfinite().all() and state[[0, 2]].isfinite().all()
+
+
+WALK, STATE, GRAD = 8, 16, 32
+
+
+@pytest.mark.parametrize("kernels,lens,H,packed", [
+    (WALK, (45,), 2, False), (WALK, (700,), 2, False),          # one chunk; several (half the value columns a block)
+    (WALK, (130,) * 40, 4, False),                              # all value columns a block
+    (WALK, (300, 0, 1, 64, 511), 3, True),
+    (WALK, (3333,), 1, False), (STATE, (3333,), 1, False), (WALK | STATE, (3333,), 1, False),   # segments
+    (STATE, (100,), 2, False), (STATE, (700,), 2, False), (STATE, (300, 0, 1, 64, 511), 3, True),
+    (GRAD, (45,), 2, False), (GRAD, (1400, 1400), 12, False), (GRAD, (300, 0, 1, 64, 511), 3, True),
+    (STATE | GRAD, (3333,), 1, False)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(cuda_ok, kernels, lens, H, packed):
+    """The failure path of the bounded waits: one wait in the first block of a kernel runs out
+    after 1 ms, with loads and products in flight.  The call returns, the device status says so, and
+    the next call with the same workspace gives the bits of a call that never saw it."""
+    import kimi_delta_attention_30_b200 as kda
+    d = 128
+    x = make("bf16", lens, H, d, d, packed, seed=90)
+    B, T = x["q"].shape[:2]
+
+    def fwd(ws):
+        return kda.linear_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], init_state=x["init"], cu_seqlens=x["cu"],
+                                    workspace=ws)
+
+    def bwd(ws):
+        return kda.linear_chunk_bwd(x["q"], x["k"], x["v"], x["log_alpha"], x["d_o"], init_state=x["init"],
+                                    d_final_state=x["d_final"], cu_seqlens=x["cu"], workspace=ws)
+
+    for call, backward in ((fwd, False), (bwd, True)):
+        runs = (GRAD | STATE) if backward else WALK | (STATE if lens == (3333,) else 0)
+        if not kernels & runs:
+            continue
+        ws = torch.empty(kda.linear_workspace_size(B, T, H, d, d, torch.bfloat16, cu_seqlens=x["cu"],
+                                                   backward=backward), dtype=torch.uint8, device="cuda")
+        status = lambda: kda.linear_device_status(ws, torch.bfloat16, B, T, H, d, d, cu_seqlens=x["cu"],
+                                                  backward=backward)
+        want = call(None)
+        torch.cuda.synchronize()
+        kda.set_test_wait_limit(kernels, 1_000_000)
+        call(ws)
+        assert status() == kda.KDA_ERR_TIMEOUT
+        for _ in range(2):
+            got = call(ws)
+            assert status() == 0
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+    kda.set_test_wait_limit(0, 0)
