@@ -224,6 +224,12 @@ def _launch_on(device, stream, tensors=()):
                 t.record_stream(cur)
 
 
+def _written(*tensors):
+    """Tensors that a library call has written: their version counters go up, so
+    that autograd notices if one of them had been saved for a backward pass."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _check_cuda(name, t, dtype=None):
     if t is None:
         return
@@ -339,6 +345,7 @@ def chunk_fwd(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None, C: int
             what = "kda_chunk_fwd"
     if st != 0:
         raise KdaError(st, what)
+    _written(o, final_state)
     return o, final_state
 
 
@@ -407,6 +414,7 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, cu_seqlens, init_state=None, C: int
             s.synchronize()
     if st != 0:
         raise KdaError(st, "kda_chunk_fwd_host")
+    _written(o, final_state)
     return o, final_state
 
 
@@ -491,6 +499,7 @@ def chunk_bwd(q, k, v, log_alpha, beta, d_o, init_state=None, d_final_state=None
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(s))
     if st != 0:
         raise KdaError(st, "kda_chunk_bwd")
+    _written(*grads)
     return dq, dk_, dv_, dla, dbeta, dinit
 
 
@@ -556,6 +565,7 @@ def segment_map(q, k, v, log_alpha, beta, cu_seqlens=None, C: int = 64, M=None, 
                                          workspace.numel() * workspace.element_size(), _stream_handle(s))
     if st != 0:
         raise KdaError(st, "kda_chunk_segment_map")
+    _written(M, F)
     return M, F
 
 
@@ -579,6 +589,7 @@ def compose_states(M, F, init_state=None, out=None, stream=None):
                                       _stream_handle(s))
     if st != 0:
         raise KdaError(st, "kda_compose_states")
+    _written(out)
     return out
 
 
@@ -619,6 +630,7 @@ def chunk_fwd_noalloc(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None
                                          _ptr(final_state), _stream_handle(s))
     if st != 0:
         raise KdaError(st, "kda_chunk_fwd_noalloc")
+    _written(o, final_state)
     return o, final_state
 
 
@@ -652,6 +664,7 @@ def decode_step(q, k, v, log_alpha, beta, state, o=None, stream=None, prep: int 
             what = "kda_decode_step"
     if st != 0:
         raise KdaError(st, what)
+    _written(state, o)
     return o
 
 

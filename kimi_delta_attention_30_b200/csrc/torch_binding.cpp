@@ -236,11 +236,18 @@ struct Linear {
 
 PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 
+// A tensor of the caller's that the call writes: its version counter goes up, so that autograd
+// notices if it had been saved for a backward pass.
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The caller's output tensor, or a new one.
 at::Tensor output(Call& c, const char* name, PyObject* given, at::ScalarType dt, at::IntArrayRef shape) {
     if (given == Py_None) return c.make(shape, dt);
     const at::Tensor& t = tensor(name, given);
     dense(name, t, c.dev, dt, shape);
+    written(t);
     return t;
 }
 
@@ -310,8 +317,10 @@ PyObject* linear_decode_step(PyObject* const* a) {
          *pv = dense("v", v, dev, dt, {N, H, dv});
     const bool per_head = la.dim() == 1;
     void* pla = per_head ? dense("log_alpha", la, dev, at::kFloat, {H}) : dense("log_alpha", la, dev, dt, {N, H});
-    void* ps = dense("state", tensor("state", a[4]), dev, at::kFloat, {N, H, dk, dv});
+    const at::Tensor& state = tensor("state", a[4]);
+    void* ps = dense("state", state, dev, at::kFloat, {N, H, dk, dv});
     Call c(dev, a[6]);
+    written(state);
     const at::Tensor o = output(c, "o", a[5], dt, v.sizes());
     c.done(kda_linear_decode_step(pq, pk, pv, pla, per_head ? KDA_DECAY_HEAD : KDA_DECAY_TOKEN, type_of(q), (float*)ps,
                                   small("N", N), small("H", H), small("dk", dk), small("dv", dv), o.data_ptr(), c.raw),
@@ -398,7 +407,10 @@ struct NormRope {
         return rows(name, t, dev, dt);
     }
     at::Tensor out(Call& c, const char* name, PyObject* given, const at::Tensor& like) const {
-        return given == Py_None ? c.make(like.sizes(), dt) : tensor(name, given);
+        if (given == Py_None) return c.make(like.sizes(), dt);
+        const at::Tensor& t = tensor(name, given);
+        written(t);
+        return t;
     }
 };
 
