@@ -217,8 +217,11 @@ def _launch_on(device, stream, tensors=()):
         if s == cur:
             yield s, results
             return
-        with torch.cuda.stream(s):
+        torch.cuda.set_stream(s)       # (the context manager of the same takes 10 us more)
+        try:
             yield s, results
+        finally:
+            torch.cuda.set_stream(cur)
         for t in results:
             if t is not None:
                 t.record_stream(cur)
