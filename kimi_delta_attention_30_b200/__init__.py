@@ -684,6 +684,11 @@ def _binding():
     global _torch_binding
     if _torch_binding is None:
         lib()                                   # builds both when stale; the module links libkda.so
+        from . import build as _build
+        if _build.binding_built_for() != _build._binding_target():
+            raise RuntimeError(f"_torch_binding.so was built for {_build.binding_built_for()}, this is "
+                               f"{_build._binding_target()}, and it could not be rebuilt: "
+                               f"run python -m {__name__}.build")
         try:
             mod = importlib.import_module("._torch_binding", __name__)
         except ImportError as exc:

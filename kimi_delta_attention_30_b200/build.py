@@ -9,6 +9,7 @@ Set ``KDA_NVCC_FLAGS`` to append flags (e.g. ``-Xptxas -v``).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import shlex
@@ -23,6 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BINDING = os.path.join(PKG, "_torch_binding.so")
+BINDING_STAMP = os.path.join(PKG, "_torch_binding.built_for")   # what the binding beside it was built for
 
 
 def nvcc() -> str:
@@ -56,8 +58,22 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _binding_target() -> str:
+    """The torch and Python whose binary interfaces the binding is compiled to."""
+    import torch
+    return f"torch {torch.__version__} {torch.version.git_version}, {sys.implementation.cache_tag}"
+
+
+def binding_built_for() -> str:
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read()
+    except OSError:
+        return "unknown"
+
+
 def _binding_stale() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or binding_built_for() != _binding_target():
         return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(p) > t for p in [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
@@ -82,7 +98,12 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(BINDING_STAMP)      # never beside a binding that it does not describe
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(_binding_target())
+    os.replace(tmp, BINDING_STAMP)
     return BINDING
 
 
