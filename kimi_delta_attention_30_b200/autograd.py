@@ -14,6 +14,9 @@ sections 6, 8 and 9).  The essay says training needs the chunkwise parallel
 form but gives no backward pass; the library's is the chain rule applied to
 that form.
 
+Gradients of gradients are not offered: a backward pass through one of them
+raises an error.
+
 ``ops`` replaces the (forward, backward) pair with two callables of the same
 signatures as :func:`chunk_fwd` and :func:`chunk_bwd`; that is how the routing
 of gradients is tested without a GPU.
@@ -21,6 +24,7 @@ of gradients is tested without a GPU.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 
 class _ChunkKDA(torch.autograd.Function):
@@ -33,6 +37,7 @@ class _ChunkKDA(torch.autograd.Function):
         return o, final_state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_final_state):
         q, k, v, log_alpha, beta, init_state = ctx.saved_tensors
         need_d_init = init_state is not None and ctx.needs_input_grad[5]
@@ -66,6 +71,7 @@ class _LinearChunk(torch.autograd.Function):
         return o, final_state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_final_state):
         q, k, v, log_alpha, init_state = ctx.saved_tensors
         if log_alpha.dim() == 1 and ctx.needs_input_grad[3]:
@@ -100,6 +106,7 @@ class _NormRope(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_q, d_k):
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         d_q = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if d_q is None else d_q

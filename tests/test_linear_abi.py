@@ -283,3 +283,22 @@ def test_norm_rope_routes_gradients():
     y, z = norm_rope(q, k, w, None, torch.arange(6), torch.ones(2), ops=(fwd, bwd))
     (y.sum() + z.sum()).backward()
     assert [float(t.grad.flatten()[0]) for t in (q, k, w)] == [1, 2, 3]
+
+
+def test_gradients_of_gradients_are_refused():
+    """The backward kernels are not differentiable: a penalty on a gradient would otherwise lose
+    what flows through the operator without a word."""
+    from kimi_delta_attention_30_b200.autograd import kda_chunk
+    mk = lambda *s: torch.randn(*s).requires_grad_()
+    q, k, v, la = mk(1, 6, 2, 4), mk(1, 6, 2, 4), mk(1, 6, 2, 4), mk(1, 6, 2)
+    state = torch.ones(1, 2, 4, 4)
+    lin = (lambda q, k, v, la, **kw: (v * 1, state),
+           lambda q, k, v, la, d_o, **kw: (q * d_o, k * d_o, v * d_o, la * 1, None))
+    kda3 = (lambda q, k, v, la, b, **kw: (v * 1, state),
+            lambda q, k, v, la, b, d_o, **kw: (q * d_o, k * d_o, v * d_o, la * 1, b * 1, None))
+    rope = (lambda q, k, *a, **kw: (q * 1, k * 1), lambda q, k, w, x, p, f, dq, dk, **kw: (q * dq, k * dk, None, None))
+    for out in (linear_chunk(q, k, v, la, ops=lin)[0], kda_chunk(q, k, v, q.clone(), la, ops=kda3)[0],
+                norm_rope(q, k, None, None, torch.arange(6), torch.ones(2), ops=rope)[0]):
+        (g,) = torch.autograd.grad(out.square().sum(), [q], create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.square().sum() + out.sum()).backward()
