@@ -27,10 +27,17 @@ import torch
 from torch.autograd.function import once_differentiable
 
 
+def _own_offsets(cu_seqlens):
+    """A copy: the caller's may have changed by the time of the backward pass."""
+    from . import _offsets
+    return None if cu_seqlens is None else list(_offsets(cu_seqlens))
+
+
 class _ChunkKDA(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_alpha, beta, init_state, cu_seqlens, C, ops):
         fwd, bwd = ops
+        cu_seqlens = _own_offsets(cu_seqlens)
         o, final_state = fwd(q, k, v, log_alpha, beta, init_state=init_state, cu_seqlens=cu_seqlens, C=C)
         ctx.save_for_backward(q, k, v, log_alpha, beta, init_state)
         ctx.cu_seqlens, ctx.C, ctx.bwd = cu_seqlens, C, bwd
@@ -65,6 +72,7 @@ class _LinearChunk(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_alpha, init_state, cu_seqlens, ops):
         fwd, bwd = ops
+        cu_seqlens = _own_offsets(cu_seqlens)
         o, final_state = fwd(q, k, v, log_alpha, init_state=init_state, cu_seqlens=cu_seqlens)
         ctx.save_for_backward(q, k, v, log_alpha, init_state)
         ctx.cu_seqlens, ctx.bwd = cu_seqlens, bwd

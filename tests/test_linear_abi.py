@@ -302,3 +302,21 @@ def test_gradients_of_gradients_are_refused():
         (g,) = torch.autograd.grad(out.square().sum(), [q], create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (g.square().sum() + out.sum()).backward()
+
+
+@pytest.mark.parametrize("make", [list, np.array, torch.tensor], ids=["list", "numpy", "torch"])
+def test_offsets_of_the_forward_call_are_those_of_the_backward(make):
+    """A caller that fills one buffer with every batch's offsets."""
+    from kimi_delta_attention_30_b200.autograd import kda_chunk
+    mk = lambda *s: torch.randn(*s).requires_grad_()
+    q, v, la = mk(1, 6, 2, 4), mk(1, 6, 2, 4), mk(1, 6, 2)
+    seen = []
+    fwd = lambda *a, cu_seqlens=None, **kw: (seen.append(list(cu_seqlens)), (a[2] * 1, torch.ones(2, 2, 4, 4)))[1]
+    bwd = lambda *a, cu_seqlens=None, **kw: (seen.append(list(cu_seqlens)), (*a[:-1], None))[1]
+    for f, args in ((linear_chunk, (q, q, v, la)), (kda_chunk, (q, q, v, q, la))):
+        cu = make([0, 2, 6])
+        seen.clear()
+        o, _ = f(*args, cu_seqlens=cu, ops=(fwd, bwd))
+        cu[1] = 5
+        o.sum().backward()
+        assert seen == [[0, 2, 6]] * 2 and all(type(x) is int for x in seen[0])
