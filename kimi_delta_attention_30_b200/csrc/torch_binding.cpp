@@ -395,6 +395,8 @@ struct NormRope {
             rot = 2 * small("rot", f.size(0));
             if (a[4] == Py_None) throw BadValue("positions are required with inv_freq");
             pos = dense("positions", a[4], dev, at::kInt, lead);
+        } else if (a[4] != Py_None) {
+            throw BadValue("inv_freq is required with positions");
         }
         const double e = PyFloat_AsDouble(a[6]);
         if (e == -1.0 && PyErr_Occurred()) throw PythonError();

@@ -249,3 +249,13 @@ def test_channels_that_do_not_turn_stay_apart(cuda_ok, dt, d, rot, inter):
         one = torch.zeros(d, dtype=torch.bool, device="cuda")
         one[c] = True
         assert not g[2][one].isfinite().any() and torch.equal(g[2][~one], want[2][~one])
+
+
+def test_positions_without_frequencies_are_refused(cuda_ok):
+    """Either both or neither: the norm alone is no answer to a call with positions."""
+    import kimi_delta_attention_30_b200 as kda
+    x = make("bf16", (4,), 2, 2, 64, 64, "bf16", False, seed=13)
+    with pytest.raises(ValueError, match="inv_freq is required"):
+        kda.qk_norm_rope(x["q"], x["k"], x["wq"], x["wk"], x["pos"])
+    with pytest.raises(ValueError, match="inv_freq is required"):
+        kda.qk_norm_rope_bwd(x["q"], x["k"], x["wq"], x["wk"], x["pos"], None, x["dq"], x["dk"])
