@@ -503,7 +503,8 @@ typedef enum {
  *   workspace : >= kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
  *               aligned, contents on entry ignored; calls that overlap on the
  *               GPU need workspaces of their own
- * final_state may alias init_state; o must not overlap an input.  Packed batches
+ * final_state may be init_state; otherwise results must not overlap an input
+ * (KDA_ERR_SHAPE).  Packed batches
  * (cu_seqlens_host, B = 1) and empty sequences as in kda_chunk_fwd.  bf16 with
  * dk = dv = 128 runs on the tensor cores: products of bf16 operands with fp32
  * accumulation; the state's update takes the decayed keys (or values) as a bf16
@@ -536,8 +537,8 @@ KDA_API kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda
  *                is below the floor of -100).  KDA_DECAY_HEAD: a fixed decay has
  *                no gradient here; the argument is ignored and may be NULL
  *   d_init_state : device [N, H, dk, dv] fp32, or NULL (not written)
- * d_final_state may be NULL (zero) and may alias d_init_state.  The other
- * outputs must not overlap an input.  Results are reproducible bit for bit.
+ * d_final_state may be NULL (zero) and may be d_init_state; otherwise results must
+ * not overlap an input (KDA_ERR_SHAPE).  Results are reproducible bit for bit.
  * On the tensor cores dq, dk and dv carry one operand rounded to bf16 (the
  * scores, or a copy of a state), dlog_alpha two: each of its terms, the product
  * of the state and its gradient among them, is off by at most 2^-7 of itself.
@@ -558,7 +559,8 @@ KDA_API kda_status kda_linear_chunk_bwd_device_status(const void* workspace, kda
 /*
  * One token for each of N sequences, the states updated in place (as
  * kda_decode_step): q, k [N, H, dk], v, o [N, H, dv], state [N, H, dk, dv] fp32,
- * log_alpha [N, H] (KDA_DECAY_TOKEN) or [H] fp32 (KDA_DECAY_HEAD).
+ * log_alpha [N, H] (KDA_DECAY_TOKEN) or [H] fp32 (KDA_DECAY_HEAD).  o and state
+ * must not overlap an input, nor one another (KDA_ERR_SHAPE).
  */
 KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const void* log_alpha,
                                           kda_decay decay, kda_dtype dtype, float* state, int N, int H, int dk,

@@ -1,6 +1,7 @@
 // Host side of linear attention with one decay a head (kda_linear_* in include/kda.h):
 // argument checks, workspace layout and dispatch.  Nothing here allocates device memory.
 #include <algorithm>
+#include <initializer_list>
 
 #include "kda_host.cuh"
 #include "kda_launch.cuh"
@@ -245,6 +246,35 @@ bool all_aligned(const void* const (&ptrs)[N]) {
     return true;
 }
 
+// Contiguous arrays of one call.  Results in an input's memory are refused, since blocks read
+// inputs that others have written results over by then; but the last result, a state, may be the
+// last input itself.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+kda_status check_apart(std::initializer_list<Span> results, std::initializer_list<Span> inputs) {
+    for (const Span& r : results)
+        for (const Span& x : inputs) {
+            if (!r.p || !x.p || (&r == results.end() - 1 && &x == inputs.end() - 1 && r.p == x.p)) continue;
+            if ((uintptr_t)r.p < (uintptr_t)x.p + x.bytes && (uintptr_t)x.p < (uintptr_t)r.p + r.bytes)
+                return KDA_ERR_SHAPE;
+        }
+    return KDA_OK;
+}
+
+// Bytes of the arrays of n token-heads and their sequences' states.
+struct Sizes {
+    size_t k, v, la, state;
+    Sizes(kda_dtype dtype, kda_decay decay, size_t n, size_t seqs, int H, int dk, int dv) {
+        const size_t e = dtype == KDA_F32 ? 4 : 2;
+        k = n * dk * e;
+        v = n * dv * e;
+        la = decay == KDA_DECAY_HEAD ? (size_t)H * 4 : n * e;
+        state = seqs * H * dk * dv * sizeof(float);
+    }
+};
+
 TestStall take_stall() {
     TestStall t;
     t.walk = take_test_wait(KDA_TEST_WAIT_LINEAR_WALK);
@@ -321,10 +351,16 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
             ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
         const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
+        const Sizes z(dtype, decay, (size_t)p.total_tokens * H, p.n_seqs, H, dk, dv);
+        const auto apart = [&] {
+            return check_apart({{o, z.v}, {final_state, z.state}},
+                               {{q, z.k}, {k, z.k}, {v, z.v}, {log_alpha, z.la}, {init_state, z.state}});
+        };
         if (tc) {
             TcLayout L;
             if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, false, L)) != KDA_OK) return st;
             if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+            if ((st = apart()) != KDA_OK) return st;
             if ((st = check_device()) != KDA_OK) return st;
             if (p.n_seqs == 0) return KDA_OK;
             cudaStream_t s = (cudaStream_t)stream;
@@ -344,6 +380,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         }
         const LinLayout L = simt_layout(p, H, dk, dv, false);
         if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+        if ((st = apart()) != KDA_OK) return st;
         if ((st = check_device()) != KDA_OK) return st;
         if (p.n_seqs == 0) return KDA_OK;
         cudaStream_t s = (cudaStream_t)stream;
@@ -405,10 +442,18 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
             ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
         const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
+        const Sizes z(dtype, decay, (size_t)p.total_tokens * H, p.n_seqs, H, dk, dv);
+        const auto apart = [&] {
+            return check_apart({{dq, z.k}, {dk_out, z.k}, {dv_out, z.v},
+                                {decay == KDA_DECAY_HEAD ? nullptr : dlog_alpha, z.la}, {d_init_state, z.state}},
+                               {{q, z.k}, {k, z.k}, {v, z.v}, {log_alpha, z.la}, {d_o, z.v}, {init_state, z.state},
+                                {d_final_state, z.state}});
+        };
         if (tc) {
             TcLayout L;
             if ((st = tc_layout(p, cu_seqlens_host, n_seqs, B, T, H, true, L)) != KDA_OK) return st;
             if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+            if ((st = apart()) != KDA_OK) return st;
             if ((st = check_device()) != KDA_OK) return st;
             if (p.n_seqs == 0) return KDA_OK;
             cudaStream_t s = (cudaStream_t)stream;
@@ -435,6 +480,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
         }
         const LinLayout L = simt_layout(p, H, dk, dv, true);
         if (workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+        if ((st = apart()) != KDA_OK) return st;
         if ((st = check_device()) != KDA_OK) return st;
         if (p.n_seqs == 0) return KDA_OK;
         cudaStream_t s = (cudaStream_t)stream;
@@ -467,6 +513,10 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, c
     if (N == 0) return KDA_OK;
     if (!q || !k || !v || !log_alpha || !state || !o) return KDA_ERR_NULL;
     if (!all_aligned({q, k, v, log_alpha, (const void*)state, (const void*)o})) return KDA_ERR_ALIGN;
+    const Sizes z(dtype, decay, (size_t)N * H, N, H, dk, dv);
+    if ((st = check_apart({{o, z.v}, {state, z.state}},
+                          {{q, z.k}, {k, z.k}, {v, z.v}, {log_alpha, z.la}, {state, z.state}})) != KDA_OK)
+        return st;
     if ((st = check_device()) != KDA_OK) return st;
     const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
     return launch_lin_decode(dtype, q, k, v, dec, state, N, H, dk, dv, o, (cudaStream_t)stream) == cudaSuccess

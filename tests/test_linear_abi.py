@@ -320,3 +320,55 @@ def test_offsets_of_the_forward_call_are_those_of_the_backward(make):
         cu[1] = 5
         o.sum().backward()
         assert seen == [[0, 2, 6]] * 2 and all(type(x) is int for x in seen[0])
+
+
+# ---- results in an input's memory --------------------------------------------------
+
+_MB = 1 << 20
+
+
+def _apart():
+    """Arguments whose arrays lie apart (1 MB each)."""
+    names = ("q", "k", "v", "la", "s0", "o", "fs", "do", "dfs", "dq", "dk_", "dv_", "dla", "ds0", "ws")
+    return {n: (i + 1) * _MB for i, n in enumerate(names)}
+
+
+FWD = ("q", "k", "v", "la", "s0", "o", "fs", "ws")
+BWD = ("q", "k", "v", "la", "s0", "do", "dfs", "dq", "dk_", "dv_", "dla", "ds0", "ws")
+
+
+@pytest.mark.parametrize("dtype,d", [(1, 64), (0, 128)])
+def test_results_that_overlap_inputs_are_refused(dtype, d):
+    if torch.cuda.is_available():
+        pytest.skip("valid arguments would launch")
+    size = dict(dtype=dtype, dk=d, dv=d, T=256, H=2)
+    far = _apart()
+    fwd = {n: far[n] for n in FWD}
+    bwd = {n: far[n] for n in BWD}
+    ok = _fwd(**size, **fwd)
+    assert ok not in (OK, E_SHAPE, E_ALIGN, E_NULL, E_WS)          # accepted but for the missing device
+    assert _bwd(**size, **bwd) == ok
+    nbytes = 256 * 2 * d * (4 if dtype else 2)
+    for r in ("o", "fs"):
+        for x in ("q", "k", "v", "la", "s0"):
+            for shift in (0, 16):                                   # the same start, and partly
+                want = ok if (r, x, shift) == ("fs", "s0", 0) else E_SHAPE
+                assert _fwd(**size, **{**fwd, r: fwd[x] + shift}) == want, (r, x)
+    assert _fwd(**size, **{**fwd, "o": fwd["v"] - nbytes}) == ok    # one behind the other
+    assert _fwd(**size, **{**fwd, "o": fwd["v"] - nbytes + 16}) == E_SHAPE
+    for r in ("dq", "dk_", "dv_", "dla", "ds0"):
+        for x in ("q", "k", "v", "la", "do", "s0", "dfs"):
+            for shift in (0, 16):
+                want = ok if (r, x, shift) == ("ds0", "dfs", 0) else E_SHAPE
+                assert _bwd(**size, **{**bwd, r: bwd[x] + shift}) == want, (r, x)
+    assert _bwd(**size, **{**bwd, "decay": 1, "dla": bwd["q"]}) == ok   # not written
+    f = kda.lib().kda_linear_decode_step
+
+    def dec(**kw):
+        a = {n: far[n] for n in ("q", "k", "v", "la", "s0", "o")}
+        a.update(kw)
+        return f(vp(a["q"]), vp(a["k"]), vp(a["v"]), vp(a["la"]), 0, dtype, vp(a["s0"]), 5, 2, d, d, vp(a["o"]), None)
+
+    assert dec() == ok
+    for r, x in [("o", x) for x in ("q", "k", "v", "la", "s0")] + [("s0", x) for x in ("q", "k", "v", "la")]:
+        assert dec(**{r: far[x]}) == E_SHAPE and dec(**{r: far[x] + 16}) == E_SHAPE, (r, x)
