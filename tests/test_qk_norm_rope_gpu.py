@@ -259,3 +259,17 @@ def test_positions_without_frequencies_are_refused(cuda_ok):
         kda.qk_norm_rope(x["q"], x["k"], x["wq"], x["wk"], x["pos"])
     with pytest.raises(ValueError, match="inv_freq is required"):
         kda.qk_norm_rope_bwd(x["q"], x["k"], x["wq"], x["wk"], x["pos"], None, x["dq"], x["dk"])
+
+
+FEW_HEADS = [   # many tokens, fewer heads a side than a warp takes at a time
+    ("bf16", (20011,), 1, 1, 128, 128, "bf16", True, False, False),
+    ("bf16", (3, 5003), 4, 1, 64, 32, "f32", False, True, True),
+    ("f32", (9001,), 2, 1, 128, 64, "f32", False, False, True),
+    ("f32", (12001,), 1, 3, 64, 64, None, True, True, False),
+]
+
+
+@pytest.mark.parametrize("case", FEW_HEADS, ids=["-".join(str(y) for y in c).replace(" ", "") for c in FEW_HEADS])
+def test_few_heads_many_tokens(cuda_ok, case):
+    test_forward(cuda_ok, case)
+    test_backward(cuda_ok, case)
