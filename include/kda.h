@@ -490,6 +490,8 @@ KDA_API kda_status kda_chunk_fwd_noalloc_device_status(kda_dtype dtype, const in
  *   KDA_DECAY_TOKEN : log_alpha is [B, T, H] in the inputs' dtype, data dependent
  *   KDA_DECAY_HEAD  : log_alpha is [H] fp32, the same for every token
  * Either way log_alpha <= 0 and the floor of -100 applies, as in the KDA calls.
+ * log_alpha and dlog_alpha are 4-byte aligned (a step's or a layer's part of a table
+ * of decays), the other arrays 16-byte.
  */
 typedef enum {
     KDA_DECAY_TOKEN = 0,

@@ -246,6 +246,10 @@ bool all_aligned(const void* const (&ptrs)[N]) {
     return true;
 }
 
+// log_alpha and its gradient are read and written one element at a time; slices of a table of
+// decays seldom start on 16 bytes.
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
 // Contiguous arrays of one call.  Results in an input's memory are refused, since blocks read
 // inputs that others have written results over by then; but the last result, a state, may be the
 // last input itself.
@@ -347,8 +351,8 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         if (st != KDA_OK) return st;
         if (p.total_tokens > 0 && (!q || !k || !v || !log_alpha || !o)) return KDA_ERR_NULL;
         if (!workspace) return KDA_ERR_WORKSPACE;
-        if (!all_aligned({q, k, v, log_alpha, (const void*)init_state, (const void*)o, (const void*)final_state}) ||
-            ((uintptr_t)workspace & (kAlign - 1)) != 0)
+        if (!all_aligned({q, k, v, (const void*)init_state, (const void*)o, (const void*)final_state}) ||
+            !aligned4(log_alpha) || ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
         const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
         const Sizes z(dtype, decay, (size_t)p.total_tokens * H, p.n_seqs, H, dk, dv);
@@ -436,10 +440,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                                    (decay == KDA_DECAY_TOKEN && !dlog_alpha)))
             return KDA_ERR_NULL;
         if (!workspace) return KDA_ERR_WORKSPACE;
-        if (!all_aligned({q, k, v, log_alpha, (const void*)init_state, d_o, (const void*)d_final_state,
-                          (const void*)dq, (const void*)dk_out, (const void*)dv_out, (const void*)dlog_alpha,
-                          (const void*)d_init_state}) ||
-            ((uintptr_t)workspace & (kAlign - 1)) != 0)
+        if (!all_aligned({q, k, v, (const void*)init_state, d_o, (const void*)d_final_state, (const void*)dq,
+                          (const void*)dk_out, (const void*)dv_out, (const void*)d_init_state}) ||
+            !aligned4(log_alpha) || !aligned4(dlog_alpha) || ((uintptr_t)workspace & (kAlign - 1)) != 0)
             return KDA_ERR_ALIGN;
         const LinDecay dec{log_alpha, decay == KDA_DECAY_HEAD};
         const Sizes z(dtype, decay, (size_t)p.total_tokens * H, p.n_seqs, H, dk, dv);
@@ -512,7 +515,7 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, c
     if ((long long)N * H * (dv / 32) > 0x7fffffffLL) return KDA_ERR_SHAPE;   // the grid
     if (N == 0) return KDA_OK;
     if (!q || !k || !v || !log_alpha || !state || !o) return KDA_ERR_NULL;
-    if (!all_aligned({q, k, v, log_alpha, (const void*)state, (const void*)o})) return KDA_ERR_ALIGN;
+    if (!all_aligned({q, k, v, (const void*)state, (const void*)o}) || !aligned4(log_alpha)) return KDA_ERR_ALIGN;
     const Sizes z(dtype, decay, (size_t)N * H, N, H, dk, dv);
     if ((st = check_apart({{o, z.v}, {state, z.state}},
                           {{q, z.k}, {k, z.k}, {v, z.v}, {log_alpha, z.la}, {state, z.state}})) != KDA_OK)

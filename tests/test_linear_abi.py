@@ -372,3 +372,19 @@ def test_results_that_overlap_inputs_are_refused(dtype, d):
     assert dec() == ok
     for r, x in [("o", x) for x in ("q", "k", "v", "la", "s0")] + [("s0", x) for x in ("q", "k", "v", "la")]:
         assert dec(**{r: far[x]}) == E_SHAPE and dec(**{r: far[x] + 16}) == E_SHAPE, (r, x)
+
+
+def test_decays_need_four_bytes():
+    if torch.cuda.is_available():
+        pytest.skip("valid arguments would launch")
+    far = _apart()
+    for dtype, d in ((1, 64), (0, 128)):
+        size = dict(dtype=dtype, dk=d, dv=d, T=256, H=2)
+        fwd, bwd = ({n: far[n] for n in names} for names in (FWD, BWD))
+        ok = _fwd(**size, **fwd)
+        for off in (4, 8, 12):
+            assert _fwd(**size, **{**fwd, "la": far["la"] + off}) == ok
+            assert _fwd(**size, **{**fwd, "la": far["la"] + off, "decay": 1}) == ok
+            assert _bwd(**size, **{**bwd, "la": far["la"] + off, "dla": far["dla"] + off}) == ok
+        assert _fwd(**size, **{**fwd, "la": far["la"] + 2}) == E_ALIGN
+        assert _bwd(**size, **{**bwd, "dla": far["dla"] + 2}) == E_ALIGN

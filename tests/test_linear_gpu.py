@@ -655,3 +655,34 @@ def test_more_shapes(cuda_ok, shape):
         operands = 0 if not _tc(dt, dk, dv) or "state" in name else 2 if name == "dlog_alpha" else 1
         stored = 2.0 ** -8 * np.abs(ref[name]) if t.dtype == torch.bfloat16 else 0.0
         close(f"{label} {name}", t, ref[name], (F32U + operands * 2.0 ** -8) * mag[name] + stored)
+
+
+def test_decays_from_a_table(cuda_ok):
+    """A step's decays out of [T, N, H], a layer's out of [layers, H], a prompt's out of a longer buffer:
+    slices that start on 4 bytes."""
+    import kimi_delta_attention_30_b200 as kda
+    N, H, d = 3, 2, 128
+    for dt, dk in (("bf16", d), ("f32", 64)):
+        x = make(dt, (1,) * N, H, dk, d, False, seed=110)
+        steps = (-torch.rand(4, N, H, generator=torch.Generator().manual_seed(1))).to(DT[dt]).cuda()
+        layers = (-torch.rand(5, 3, generator=torch.Generator().manual_seed(2))).cuda()
+        for la in (steps[1], steps[3], layers[1, :H], layers[3, 1:]):
+            assert la.data_ptr() % 16 and la.data_ptr() % 4 == 0
+            st = [x["init"].clone(), x["init"].clone()]
+            o = [kda.linear_decode_step(x["q"][:, 0], x["k"][:, 0], x["v"][:, 0], a, s)
+                 for a, s in zip((la, la.clone()), st)]
+            assert torch.equal(*o) and torch.equal(*st)
+        y = make(dt, (200,), H, dk, d, False, seed=111)
+        buf = torch.zeros(1, 203, H, dtype=DT[dt], device="cuda")
+        la = buf[:, 1:201] if dt == "bf16" else buf.flatten()[3:403].view(1, 200, H)
+        la.copy_(y["log_alpha"])
+        dla = torch.zeros(1, 203, H, dtype=DT[dt], device="cuda").flatten()[2:402].view(1, 200, H)
+        assert la.data_ptr() % 16 and dla.data_ptr() % 16
+        args = (y["q"], y["k"], y["v"])
+        assert all(torch.equal(a, b) for a, b in zip(kda.linear_chunk_fwd(*args, la),
+                                                     kda.linear_chunk_fwd(*args, y["log_alpha"])))
+        want = kda.linear_chunk_bwd(*args, y["log_alpha"], y["d_o"])
+        g = [torch.empty_like(t) for t in want]
+        g[3] = dla
+        got = kda.linear_chunk_bwd(*args, la, y["d_o"], grads=tuple(g))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
