@@ -32,7 +32,9 @@ cudaError_t launch_behind(void (*kern)(P...), dim3 grid, dim3 block, size_t smem
     c.stream = s;
     c.attrs = early;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kern, P(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&c, kern, P(args)...);
+    if (e != cudaSuccess) cudaGetLastError();   // reported by the call, and not once more by the next one
+    return e;
 }
 
 }  // namespace kda

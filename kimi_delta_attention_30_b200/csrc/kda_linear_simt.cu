@@ -551,6 +551,8 @@ cudaError_t update_and_chain(UpdateSide<Tin> fwd, UpdateSide<Tin> rev, int sides
         }
         update<<<dim3(n_chunks, H, small ? 4 * tiles : tiles), small ? 64 : kThreads, 0, s>>>(fwd, rev, dec, cmap, H, dk, dv,
                                                                                              gam);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
     const int e4 = dk * dv / 4;
     const dim3 grid((unsigned)n_seqs * H, e4 / kThreads, sides);

@@ -783,6 +783,7 @@ cudaError_t launch_lin_tc_fwd(const void* q, const void* k, const void* v, LinDe
         const StateSide side{nullptr, nullptr, seg_state, seg_gam, nullptr, nullptr};
         lin_state<<<(unsigned)n_segs * H, kStateThreads, kStSmem, s>>>(mk, mv, mk, mv, dec, segs, nullptr, H, n_segs * H, side,
                                                                      side, 1, err, stall.state);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         e = launch_behind(seg_chain<false>, dim3((unsigned)n_seqs * H, kD * kD / 1024), 256, 0, s, seg_state, seg_gam,
                           init_state, smap, H);
         if (e != cudaSuccess) return e;
@@ -821,6 +822,7 @@ cudaError_t launch_lin_tc_states(const void* q, const void* k, const void* v, co
         const StateSide r{nullptr, nullptr, d_seg, d_gam, nullptr, nullptr};
         lin_state<<<2u * units, kStateThreads, kStSmem, s>>>(mk, mv, mq, mdo, dec, segs, nullptr, H, units, f, r, 1, err,
                                                            stall.state);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const dim3 grid((unsigned)n_seqs * H, kD * kD / 1024);
         if ((e = launch_behind(seg_chain<false>, grid, 256, 0, s, seg_state, seg_gam, init_state, smap, H)) != cudaSuccess ||
             (e = launch_behind(seg_chain<true>, grid, 256, 0, s, d_seg, d_gam, d_final, smap, H)) != cudaSuccess)

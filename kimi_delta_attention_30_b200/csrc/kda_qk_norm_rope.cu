@@ -524,6 +524,8 @@ cudaError_t run(const NormRopeArgs& A, bool inter, bool bwd, float* partial, int
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         kern<<<blocks, kThreads, smem, s>>>(A, dw ? partial : nullptr);
+        const cudaError_t launched = cudaGetLastError();
+        if (launched != cudaSuccess) return launched;
         if (dw) return launch_behind(norm_rope_dw<Tw, D>, dim3(D / 32, 2), 1024, 0, s, partial, blocks, dwq, dwk);
     }
     return cudaGetLastError();
