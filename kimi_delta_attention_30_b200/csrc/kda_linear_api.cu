@@ -176,7 +176,7 @@ kda_status check_decay(kda_decay decay) {
 }
 
 // The checks that the chunk calls share; fills the plan.  Grids put heads on y and
-// sequence-heads on x.
+// sequence-heads on x, two blocks each (both directions of a backward pass, two column halves).
 kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_seqs, int B, int T, int H, int dk,
                     int dv, int C, Plan& p) {
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
@@ -185,7 +185,7 @@ kda_status plan_for(kda_decay decay, kda_dtype dtype, const int32_t* cu, int n_s
     if (T > 0x7fffffff - C) return KDA_ERR_SHAPE;   // chunk ends are ints
     st = make_plan(B, T, H, dk, dv, C, cu, n_seqs, p);
     if (st != KDA_OK) return st;
-    if (H > 65535 || (long long)p.n_seqs * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if (H > 65535 || 2LL * p.n_seqs * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
     return KDA_OK;
 }
 

@@ -388,3 +388,11 @@ def test_decays_need_four_bytes():
             assert _bwd(**size, **{**bwd, "la": far["la"] + off, "dla": far["dla"] + off}) == ok
         assert _fwd(**size, **{**fwd, "la": far["la"] + 2}) == E_ALIGN
         assert _bwd(**size, **{**bwd, "dla": far["dla"] + 2}) == E_ALIGN
+
+
+@pytest.mark.parametrize("dtype,d", [(1, 64), (0, 128)])
+def test_more_sequence_heads_than_a_grid_takes_are_refused(dtype, d):
+    """Empty sequences take no memory, so their number is bounded by the launch alone."""
+    n = 20000
+    kw = dict(dtype=dtype, dk=d, dv=d, T=1, H=65535, cu=[0] * n + [1], n=n)
+    assert _fwd(**kw) == E_SHAPE and _bwd(**kw) == E_SHAPE
