@@ -258,7 +258,10 @@ constexpr int kPos = 16;   // bytes behind a stage's pieces: the token's positio
 
 template <typename Tin, int VECS> constexpr int stage_bytes() { return VECS * pieces8<Tin>() * kPiece + kPos; }
 
-template <typename Tin, typename Tw, int D, bool INTER>
+// FULL (here and in the backward kernel): every channel turns, rot = D.  Where that is left open, the
+// channels that do not turn are kept apart by a branch, which costs 1 to 3 % of the time (52.1 instead
+// of 51.1 us forward, 82 instead of 80 backward, at the size above).
+template <typename Tin, typename Tw, int D, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_fwd(const __grid_constant__ NormRopeArgs A) {
     constexpr int LANES = D / 16, ROWS = 32 / LANES;   // lanes a row, rows a warp at a time
     constexpr int DEPTH = kDepth<Tin>(), BYTES = stage_bytes<Tin, 2>(), VEC = pieces8<Tin>() * kPiece;
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_
         const float2 r = make_float2(r1, r1);
         float2 u[4], v[4];
         // channels that do not turn stay apart: 0 times an infinity or NaN of another is none of theirs
-        if (L.turns) {
+        if (FULL || L.turns) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 u[i] = mul2(fma2(ca[i], x[i], mul2(sb[i], y[i])), r);
@@ -353,8 +356,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 5 : 4) norm_rope_
 // the side's shared-memory row of its own at the end of the side's steps of a token.
 template <typename Tin> constexpr int kBwdDepth() { return sizeof(Tin) == 2 ? 4 : 3; }
 
-// FULL: every channel turns (rot = D).  Where that is left open, the channels that do not turn
-// are kept apart by a branch, which costs 1 to 3 % of the time (82 instead of 80 us at the size above).
 template <typename Tin, typename Tw, int D, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 3) norm_rope_bwd(const __grid_constant__ NormRopeArgs A,
                                                                                    float* __restrict__ partial) {
@@ -511,7 +512,9 @@ cudaError_t run(const NormRopeArgs& A, bool inter, bool bwd, float* partial, int
                 cudaStream_t s) {
     constexpr int ROWS = 512 / D, CS = D / 2 * 8;
     if (!bwd) {
-        auto kern = inter ? norm_rope_fwd<Tin, Tw, D, true> : norm_rope_fwd<Tin, Tw, D, false>;
+        auto kern = A.rot == D ? inter ? norm_rope_fwd<Tin, Tw, D, true, true> : norm_rope_fwd<Tin, Tw, D, false, true>
+                    : inter    ? norm_rope_fwd<Tin, Tw, D, true, false>
+                               : norm_rope_fwd<Tin, Tw, D, false, false>;
         constexpr int smem = kWarps * (kDepth<Tin>() * stage_bytes<Tin, 2>() + CS);
         static_assert(smem <= 48 * 1024, "the default limit");
         kern<<<blocks, kThreads, smem, s>>>(A);
