@@ -510,8 +510,8 @@ typedef enum {
  * (cu_seqlens_host, B = 1) and empty sequences as in kda_chunk_fwd.  bf16 with
  * dk = dv = 128 runs on the tensor cores: products of bf16 operands with fp32
  * accumulation; the state's update takes the decayed keys (or values) as a bf16
- * pair, 16 bits, which leaves some 5e-6 relative in the fp32 states, while the
- * scores and the state's copy that the queries read are rounded to bf16 once, as
+ * pair, 16 bits, which leaves some 2.3e-6 relative (2-norm) in the fp32 states
+ * (fp32 sums alone: 2e-7), while the scores and the state's copy that the queries read are rounded to bf16 once, as
  * o itself is.  Other shapes and fp32 run in fp32 on the CUDA cores.  Inputs are
  * finite (log_alpha may be -inf, a reset): an infinity or NaN, a NaN log_alpha
  * among them, reaches its whole chunk (up to 128 tokens) and what follows it in
@@ -542,8 +542,10 @@ KDA_API kda_status kda_linear_chunk_fwd_device_status(const void* workspace, kda
  * d_final_state may be NULL (zero) and may be d_init_state; otherwise results must
  * not overlap an input (KDA_ERR_SHAPE).  Results are reproducible bit for bit.
  * On the tensor cores dq, dk and dv carry one operand rounded to bf16 (the
- * scores, or a copy of a state), dlog_alpha two: each of its terms, the product
- * of the state and its gradient among them, is off by at most 2^-7 of itself.
+ * scores, or a copy of a state), dlog_alpha two.  Written out as sums of products
+ * of single elements, dq, dk and dv are off by at most 2^-8, dlog_alpha by 2^-7 of
+ * the sum of the products' magnitudes (which may cancel), besides fp32 roundings and
+ * the result's own; d_init_state, as final_state, by 2^-15.
  */
 KDA_API size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, kda_dtype dtype,
                                                    const int32_t* cu_seqlens_host, int n_seqs);

@@ -41,9 +41,10 @@ constexpr int kSms = 148;
 // half of them, and the state alone; a block's start and end; and what a split adds (the
 // segments' chain, two more launches).  From 1 to 10 segments a sequence, 8 to 512 chunks
 // and 16 to 704 blocks, times estimated with these are within 15 % of the measured ones
-// (batches of unequal sequences take up to 30 % longer).  What the choice gains: 64 pairs of
-// 32 chunks in 73 us with half the columns a block, 98 with all, 107 in segments; 16 pairs of
-// 128 chunks 103 us in segments, 255 and 367 without; 32 of 512: 607, 1003 and 1465.
+// (batches of unequal sequences take up to 30 % longer).  What the choice gains, in calls back to
+// back: 64 pairs of 32 chunks in 73 us with half the columns a block, 98 with all, 107 in
+// segments; 16 pairs of 128 chunks 103 us in segments, 255 and 367 without; 32 of 512: 607 to 619,
+// 1003 and 1465.
 constexpr double kWalk128 = 3.2, kWalk64 = 2.1, kStateOnly = 1.95, kRamp = 4.0, kSplitCost = 20.0;
 
 long long longest_of(const Plan& chunks) {   // chunks of the longest sequence

@@ -6,17 +6,17 @@
 //   dQ = e^g (dO S^T) + B K      dK = w (V Z^T) + B^T Q      dV = w (K Z) + P^T dO
 //   dlog_alpha_t = sum_{i >= t} q_i . e^{g_i} (S dO_i) + sum_{j < t} k_j . w_j (Z v_j)
 //                + e^{g_C} <Z, S> + sum_{i >= t > j} P_ij (dO V^T)_ij
-// Every term of the last lines is one that t's decay enters, so sums do not cancel; the
-// last one, over a rectangle of M = P . (dO V^T) in fp32, is put together from sums over
+// Every term of the last lines is one that t's decay enters, so none is added and taken away
+// again; the last one, over a rectangle of M = P . (dO V^T) in fp32, is put together from sums over
 // 32 x 32 blocks: columns and rows of the blocks wholly inside, and a running sum in the
 // block on the diagonal.
 //
 // Eight products of 128^3 a chunk (4096 tensor cycles) against 288 KB of memory traffic
 // (6.6 us an SM at the measured copy rate): bound by memory as long as loads overlap the
-// work.  2048 (chunk, head) units take 138 us, 4.3 TB/s; of a unit's 17 K cycles the
-// elementwise warps spend 14 K, and 3 K waiting for the next Q and K.  A block keeps one chunk
-// in six 32 KB slots; a slot is loaded for the block's next chunk as soon as nothing needs it.  P and B replace S and V.  The results leave through
-// slots too (dV Z's, dQ K's, dK Q's: free by then, and needed last by the next chunk), one box
+// work.  2048 (chunk, head) units take 138 to 146 us, 4.1 to 4.3 TB/s; of a unit's 17 K cycles
+// the elementwise warps spend 14 K, and 3 K waiting for the next Q and K.  A block keeps one chunk
+// in six 32 KB slots; a slot is loaded for the block's next chunk as soon as nothing needs it.
+// P and B replace S and V.  The results leave through slots too (dV Z's, dQ K's, dK Q's: free by then, and needed last by the next chunk), one box
 // a warp: stored from registers, a row a lane, they held the load/store pipe for 3000 cycles.
 // 16 warps do the elementwise work: warp (R, B) owns rows 32 R + lane and columns
 // 32 B + [0, 32).

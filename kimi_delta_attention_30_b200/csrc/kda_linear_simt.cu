@@ -17,7 +17,8 @@
 //   dv_j = e^{g_C - g_j} dS'^T k_j + sum_i P_ij d_o_i
 //   dlog_alpha_t = sum_{i >= t} e^{g_i} q_i . S d_o_i + sum_{j < t} e^{g_C - g_j} k_j . dS' v_j
 //                + e^{g_C} <dS', S> + sum_{i >= t > j} dA_ij (q_i . k_j)
-// where every term of the last lines is one that t's decay enters, so nothing cancels:
+// where every term of the last lines is one that t's decay enters, so none is added and taken
+// away again (the terms themselves have signs):
 // the last sum runs over a rectangle of the pair products, taken as running sums along
 // each row and then down the columns.  (Suffix sums of q_i . dq_i - k_i . dk_i give the
 // same number, but the pairs with both ends behind t cancel there and leave their
@@ -33,8 +34,11 @@
 // Decays are formed from g as a (hi, lo) pair.  Small problems are chains of short launches;
 // each kernel behind the first starts early and loads and multiplies what needs only the
 // call's inputs (outputs: the scores; gradients: the pair products) before it waits.  fp32,
-// 256 tokens of 2 heads of 64: 12.4 us (20.5 without); backward of 5 sequences, 705 tokens of
-// 3 heads of 64 x 128: 43 us.
+// 256 tokens of 2 heads of 64: 12.3 us (20.5 without); backward of 5 sequences, 705 tokens of
+// 3 heads of 64 x 128: 43 us, each from a cold cache.  Large sizes are far from their bytes: fp32,
+// 2048 tokens of 16 heads of 64 (128): 56 (161) us forward, 134 (387) backward; bf16 heads of 64,
+// which have no tensor-core path, 4 x 4096 tokens of 32 heads: 767 us forward, 2263 backward, at
+// 42 and 73 us for the bytes.
 #include "kda_launch.cuh"
 #include "kda_linear.cuh"
 

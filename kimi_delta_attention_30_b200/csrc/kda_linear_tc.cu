@@ -12,7 +12,10 @@
 //   S <- e^{g_C} S + U             fp32
 // The only roundings to 8 bits are P and the copy of S that the queries read, both of the
 // kind that o itself takes when it is stored; the state sees 16-bit operands, since its
-// errors would be carried from chunk to chunk and it is returned in fp32.
+// errors would be carried from chunk to chunk and it is returned in fp32.  That pair is what the
+// fp32 states are off by: 2.2e-6 of their 2-norm against 64 bits, the sums alone 5.5e-7 (fp32
+// products on the CUDA cores 2e-7).  A third part would take half of U's time again, on the path
+// from chunk to chunk, and 32 KB (16 KB) of shared memory that neither layout has left.
 //
 // Roles, each with its own barriers, so that they work on different chunks at once: 8 warps
 // form o and keep the state (warp w: rows 32 (w % 4) + lane, column half w / 4), 8 weight the
@@ -22,8 +25,8 @@
 //   All 128 value columns a block: five 32 KB slots hold Q, K, V in turn; products in the order
 //   P V, Q S, U, then Q K^T of the next chunk (the keys are weighted in place, behind the
 //   scores).  A chunk moves 576 KB through shared memory, 4500 cycles at 128 bytes a cycle, of
-//   5500 seen; 148 blocks of 32 chunks take 112 to 118 us, 5.3 to 5.5 TB/s, 0.82 to 0.85 of
-//   the copy rate.
+//   5500 seen; 148 blocks of 32 chunks take 112 to 119 us, 5.2 to 5.5 TB/s, 0.81 to 0.85 of
+//   the copy rate (128 us from a cold cache; times below too are of calls back to back).
 //   Half of them, where the pairs of sequence and head are fewer than the SMs: two chunks of
 //   each operand and two sets of scores; products in the order Q S, U, then Q K^T of the next
 //   chunk and P V, which give the state's warps time for S (86 us for 64 pairs of 32 chunks)
@@ -31,7 +34,7 @@
 //   bring a chunk to 3700 cycles of 1920 that the products take alone: it is bound by
 //   latencies around the one warp that issues them.  98 us with all columns a block.  Two
 //   warps issuing (one Q S and U, the other Q K^T and P V) took 87 us instead of 78: the
-//   second's products delay the state's.
+//   second's products delay the state's.  A single call from a cold cache takes 77 to 82 us.
 // Rows past a sequence's end are loaded with the box (they belong to the next sequence); K's
 // are weighted with zero, V's are cleared, Q's only reach rows of o that are not stored.
 #include <algorithm>

@@ -9,7 +9,10 @@
 // Bound by HBM: a row is read once and written once, some five instructions an element (packed
 // fp32 pairs), which is near the issue limit too: at 16 channels a lane a step of four rows
 // takes about 80 instructions a warp forward.  16384 tokens of 32 heads of 128 bf16 channels:
-// forward 49 us, 5.5 TB/s, 0.85 of the copy rate; backward 82 us, 4.9 TB/s.  A warp walks tokens and, for each, its heads
+// forward 47.5 us, 5.7 TB/s, 0.88 of the copy rate; backward 80 us, 5.0 TB/s (calls back to
+// back; 51 and 89 us from a cold cache).  With few heads most lanes have no row of their own: 65536
+// tokens of one query and one key head take 83 us forward, 134 backward, at 10 and 16 us for the
+// bytes.  A warp walks tokens and, for each, its heads
 // (or a part of them when there are few tokens), four or eight rows at a time: d / 16 lanes
 // share a row, and a lane holds the two 8-channel vectors that rotate with each other
 // (halves: vectors p and p + rot / 16; neighbours: vectors 2 p and 2 p + 1), so a rotation
