@@ -9,9 +9,9 @@ Set ``KDA_NVCC_FLAGS`` to append flags (e.g. ``-Xptxas -v``).
 from __future__ import annotations
 
 import concurrent.futures as cf
-import contextlib
 import glob
 import os
+import re
 import shlex
 import subprocess
 import sys
@@ -24,7 +24,6 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BINDING = os.path.join(PKG, "_torch_binding.so")
-BINDING_STAMP = os.path.join(PKG, "_torch_binding.built_for")   # what the binding beside it was built for
 
 
 def nvcc() -> str:
@@ -65,11 +64,13 @@ def _binding_target() -> str:
 
 
 def binding_built_for() -> str:
+    """The same of the binding that is there, which carries it as text (read before it is loaded)."""
     try:
-        with open(BINDING_STAMP) as f:
-            return f.read()
+        with open(BINDING, "rb") as f:
+            m = re.search(rb"kda binding built for \[([^\]]*)\]", f.read())
     except OSError:
-        return "unknown"
+        return "nothing"
+    return m.group(1).decode() if m else "unknown"
 
 
 def _binding_stale() -> bool:
@@ -91,6 +92,7 @@ def build_binding(force: bool = False) -> str:
     cuda = os.path.dirname(cuda_lib_dir())
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f'-DKDA_BUILT_FOR="{_binding_target()}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
            *(f"-isystem{p}" for p in ext.include_paths()), BINDING_SRC, "-o", tmp, "-L", PKG, "-l:libkda.so", "-L", libs, "-lc10", "-lc10_cuda",
@@ -98,12 +100,7 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    with contextlib.suppress(FileNotFoundError):
-        os.remove(BINDING_STAMP)      # never beside a binding that it does not describe
     os.replace(tmp, BINDING)
-    with open(tmp, "w") as f:
-        f.write(_binding_target())
-    os.replace(tmp, BINDING_STAMP)
     return BINDING
 
 

@@ -22,6 +22,10 @@
 
 #include "kda.h"
 
+// What this module is compiled for (build.py reads it before the module is loaded).
+extern "C" __attribute__((used, visibility("default"))) const char kda_binding_built_for[] =
+    "kda binding built for [" KDA_BUILT_FOR "]";
+
 namespace {
 
 PyObject* g_error = nullptr;   // KdaError
