@@ -261,7 +261,7 @@ struct Span {
 kda_status check_apart(std::initializer_list<Span> results, std::initializer_list<Span> inputs) {
     for (const Span& r : results)
         for (const Span& x : inputs) {
-            if (!r.p || !x.p || (&r == results.end() - 1 && &x == inputs.end() - 1 && r.p == x.p)) continue;
+            if (!r.p || !x.p || !r.bytes || !x.bytes || (&r == results.end() - 1 && &x == inputs.end() - 1 && r.p == x.p)) continue;
             if ((uintptr_t)r.p < (uintptr_t)x.p + x.bytes && (uintptr_t)x.p < (uintptr_t)r.p + r.bytes)
                 return KDA_ERR_SHAPE;
         }

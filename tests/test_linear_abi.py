@@ -396,3 +396,15 @@ def test_more_sequence_heads_than_a_grid_takes_are_refused(dtype, d):
     n = 20000
     kw = dict(dtype=dtype, dk=d, dv=d, T=1, H=65535, cu=[0] * n + [1], n=n)
     assert _fwd(**kw) == E_SHAPE and _bwd(**kw) == E_SHAPE
+
+
+def test_arrays_without_elements_overlap_nothing():
+    if torch.cuda.is_available():
+        pytest.skip("valid arguments would launch")
+    far = _apart()
+    for dtype, d in ((1, 64), (0, 128)):
+        fwd = {n: far[n] for n in FWD}
+        size = dict(dtype=dtype, dk=d, dv=d, H=2)
+        ok = _fwd(**size, T=256, **fwd)
+        assert _fwd(**size, T=0, **{**fwd, "o": fwd["s0"] + 256}) == ok
+        assert _fwd(**size, T=0, **{**fwd, "fs": fwd["s0"] + 256}) == E_SHAPE
